@@ -6,13 +6,15 @@ stream and plain sizes cross the boundary.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from pathlib import Path
 
 LQ_OK, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_ALIGNMENT, LQ_ERR_WORKSPACE, LQ_ERR_CUDA, LQ_ERR_TIMEOUT, \
-    LQ_ERR_RANGE = range(8)
+    LQ_ERR_RANGE, LQ_ERR_INDEX = range(9)
 FMT_2BIT, FMT_NF4, FMT_INT4, FMT_NF4_DQ = 1, 2, 3, 4
 F32, F16, BF16 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 
 #: every entry point include/lq.h declares
 EXPORTED = ("lq_create", "lq_destroy", "lq_status_string", "lq_sync", "lq_dequant", "lq_gemv",
@@ -20,6 +22,7 @@ EXPORTED = ("lq_create", "lq_destroy", "lq_status_string", "lq_sync", "lq_dequan
             "lq_gemv_grouped", "lq_gemv_layers", "lq_gemm", "lq_gemm_grouped", "lq_gemv_noalloc",
             "lq_select_anchors", "lq_quantize_2bit", "lq_quantize_nf4",
             "lq_stream_create", "lq_stream_run", "lq_stream_destroy", "lq_stream_run_direct",
+            "lq_rope_table", "lq_rope", "lq_kv_tile_bytes", "lq_kv_append", "lq_kv_read", "lq_kv_attention",
             "lq_selftest_wait")
 
 _LIB = None
@@ -44,6 +47,44 @@ class lq_problem(ctypes.Structure):
         ("stride_anchor_idx", ctypes.c_int64), ("stride_anchor_w", ctypes.c_int64),
         ("stride_x", ctypes.c_int64), ("stride_y", ctypes.c_int64),
     ]
+
+
+class lq_rope_config(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("low_rotations", ctypes.c_double),
+                ("high_rotations", ctypes.c_double), ("mscale", ctypes.c_float)]
+
+
+class lq_rope_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int), ("positions", ctypes.c_void_p), ("layout", ctypes.c_int),
+                ("inverse", ctypes.c_int)]
+
+
+class lq_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("bits", ctypes.c_int)]
+
+
+class lq_kv_append_args(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("dtype", ctypes.c_int), ("n", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("k_token_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64), ("q_out_token_stride", ctypes.c_int64), ("slots", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_rows", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class lq_kv_attention_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("q_token_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("lens", ctypes.c_void_p), ("prefix_table", ctypes.c_void_p), ("prefix_len", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 def library_path() -> Path:
@@ -102,6 +143,19 @@ def load_library(build_if_missing: bool = True):
     L.lq_stream_destroy.restype = I
     L.lq_stream_run_direct.argtypes = [P, P, S, S, I, ctypes.POINTER(lq_problem), I, ctypes.c_int64, P]
     L.lq_stream_run_direct.restype = I
+    C = ctypes.POINTER(lq_kv_cache)
+    L.lq_rope_table.argtypes = [P, ctypes.POINTER(lq_rope_config), I, I, P, P]
+    L.lq_rope_table.restype = I
+    L.lq_rope.argtypes = [P, ctypes.POINTER(lq_rope_args), P]
+    L.lq_rope.restype = I
+    L.lq_kv_tile_bytes.argtypes = [I, I]
+    L.lq_kv_tile_bytes.restype = I
+    L.lq_kv_append.argtypes = [P, C, ctypes.POINTER(lq_kv_append_args), P]
+    L.lq_kv_append.restype = I
+    L.lq_kv_read.argtypes = [P, C, P, I, P, P, I, P]
+    L.lq_kv_read.restype = I
+    L.lq_kv_attention.argtypes = [P, C, ctypes.POINTER(lq_kv_attention_args), P]
+    L.lq_kv_attention.restype = I
     L.lq_selftest_wait.argtypes = [P, ctypes.c_uint, P]
     L.lq_selftest_wait.restype = I
     _LIB = L
@@ -121,6 +175,15 @@ def _ptr(t) -> int | None:
 def _dtype_code(t) -> int:
     import torch
     return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[t.dtype]
+
+
+@functools.lru_cache(maxsize=None)
+def _code(dtype) -> int:
+    import torch
+    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    if dtype not in codes:
+        raise ValueError(f"dtype {dtype} is not float32, float16 or bfloat16")
+    return codes[dtype]
 
 
 def _stream(stream) -> int | None:
@@ -167,6 +230,30 @@ class QuantWeights:
     def args(self):
         return (self.format, _ptr(self.codes), _ptr(self.scales), _ptr(self.offsets), _ptr(self.anchor_idx),
                 _ptr(self.anchor_w), int(self.A), int(self.ld_anchor))
+
+
+class KVCache:
+    """A paged low-bit cache of keys and values (layout as in include/lq.h): uint8 pages
+    [num_pages][kv_heads][page_size / 16][tile bytes], made here (zeroed) or the caller's."""
+
+    def __init__(self, pages=None, *, page_size: int, kv_heads: int, head_dim: int, bits: int, num_pages: int = 0,
+                 device="cuda"):
+        import torch
+        tile = load_library().lq_kv_tile_bytes(int(bits), int(head_dim))
+        if tile == 0:
+            raise ValueError(f"no cache with {bits} bits and heads of {head_dim}")
+        if page_size < 16 or page_size % 16:
+            raise ValueError("page_size must be a multiple of 16")
+        if pages is None:
+            pages = torch.zeros((num_pages, kv_heads, page_size // 16, tile), dtype=torch.uint8, device=device)
+        if (pages.dtype != torch.uint8 or not pages.is_contiguous() or
+                tuple(pages.shape[1:]) != (kv_heads, page_size // 16, tile)):
+            raise ValueError(f"pages must be contiguous uint8 [num_pages][{kv_heads}][{page_size // 16}][{tile}]")
+        self.pages = pages
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.bits = \
+            pages.shape[0], page_size, kv_heads, head_dim, bits
+        self._c = lq_kv_cache(pages.data_ptr(), self.num_pages, page_size, kv_heads, head_dim, bits)
+        self._ref = ctypes.byref(self._c)
 
 
 class Handle:
@@ -282,6 +369,176 @@ class Handle:
         st = self._lib.lq_selftest_wait(self._h, int(limit_us), _stream(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_selftest_wait")
+
+    # ---- rotary positions, the low-bit KV cache and attention over it ----
+
+    def _out(self, stream, shape, dtype, device):
+        """A result on the current stream's allocator, kept until `stream` (when another) is done with it."""
+        import torch
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
+
+    def _raw(self, stream):
+        import torch
+        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else int(stream.cuda_stream)
+
+    def _rows(self, name, t, heads, dim, dtype=None):
+        """Token stride of a [n][heads][dim] operand of this device."""
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (dtype is not None and t.dtype != dtype):
+            raise ValueError(f"{name} must be [n][{heads}][{dim}]" + (f" of {dtype}" if dtype is not None else ""))
+        st = t.stride()
+        if (st[2] != 1 or (st[1] != dim and heads > 1)) and t.numel():
+            raise ValueError(f"{name}'s heads and dimensions must be contiguous")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on cuda:{self.device}")
+        return st[0] if t.shape[0] > 1 else heads * dim
+
+    def _indices(self, name, t, dtype, n):
+        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or \
+                t.get_device() != self.device:
+            raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype} on cuda:{self.device}")
+        return t.data_ptr()
+
+    def _table(self, table):
+        import torch
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or \
+                table.get_device() != self.device:
+            raise ValueError(f"table must be a contiguous fp32 [rows][rot_dim] tensor on cuda:{self.device}")
+        return table.data_ptr()
+
+    def rope_table(self, count, rot_dim, base=10000.0, first=0, factor=1.0, original_length=0.0, low_rotations=1.0,
+                   high_rotations=32.0, mscale=1.0, out=None, stream=None):
+        """Rows first .. first + count - 1 of the rotation table, fp32 [count][rot_dim]: cosines, then
+        sines.  factor stretches the positions: every frequency (original_length 0) or by parts."""
+        import torch
+        if out is None:
+            out = self._out(stream, (count, rot_dim), torch.float32, torch.device("cuda", self.device))
+        elif tuple(out.shape) != (count, rot_dim):
+            raise ValueError(f"out must be [{count}][{rot_dim}]")
+        c = lq_rope_config(rot_dim, base, factor, original_length, low_rotations, high_rotations, mscale)
+        st = self._lib.lq_rope_table(self._h, ctypes.byref(c), first, count, self._table(out), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_rope_table")
+        return out
+
+    def rope(self, x, positions, table, layout=ROPE_HALF, inverse=False, out=None, stream=None):
+        """Rotate the first table.shape[1] dimensions of x [n][heads][dim] (any token and head stride) by
+        its int32 positions' table rows; inverse=True applies the transpose (the gradient)."""
+        import torch
+        n, heads, dim = x.shape
+        if out is None:
+            out = self._out(stream, (n, heads, dim), x.dtype, x.device)
+        elif out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and dtype")
+        xs, ys = x.stride(), out.stride()
+        if (xs[2] != 1 or ys[2] != 1) and dim > 1:
+            raise ValueError("dimensions must be contiguous")
+        if x.get_device() != self.device or out.get_device() != self.device:
+            raise ValueError(f"x and out must be on cuda:{self.device}")
+        a = lq_rope_args(x.data_ptr(), out.data_ptr(), _code(x.dtype), n, heads, dim, table.shape[1], xs[0], xs[1], ys[0],
+                         ys[1], self._table(table), table.shape[0], self._indices("positions", positions, torch.int32, n),
+                         layout, bool(inverse))
+        if n == 0:
+            return out
+        st = self._lib.lq_rope(self._h, ctypes.byref(a), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_rope")
+        return out
+
+    def kv_append(self, cache: KVCache, k, v, slots, q=None, table=None, positions=None, layout=ROPE_HALF, q_out=None,
+                  stream=None):
+        """Quantise k and v [n][kv_heads][dim] into the cache's int64 slots (negative: skipped).  With a
+        table, k is rotated first, and so is q [n][q_heads][dim] when given, into the returned tensor."""
+        import torch
+        dt, n, dim = k.dtype, k.shape[0], cache.head_dim
+        ks, vs = self._rows("k", k, cache.kv_heads, dim), self._rows("v", v, cache.kv_heads, dim, dt)
+        if v.shape[0] != n:
+            raise ValueError("k and v must have the same tokens")
+        qp = op = None
+        hq = qs = os = 0
+        if q is not None:
+            hq = q.shape[1]
+            if q_out is None:
+                q_out = self._out(stream, (n, hq, dim), dt, q.device)
+            qs, os = self._rows("q", q, hq, dim, dt), self._rows("q_out", q_out, hq, dim, dt)
+            if q.shape[0] != n or q_out.shape[0] != n:
+                raise ValueError("q and q_out must have k's tokens")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        tp = pp = None
+        rows = rot = 0
+        if table is not None:
+            rows, rot = table.shape
+            tp, pp = self._table(table), self._indices("positions", positions, torch.int32, n)
+        a = lq_kv_append_args(k.data_ptr(), v.data_ptr(), qp, op, _code(dt), n, hq, ks, vs, qs, os,
+                              self._indices("slots", slots, torch.int64, n), tp, rows, pp, rot, layout)
+        if n == 0:
+            return q_out
+        st = self._lib.lq_kv_append(self._h, cache._ref, ctypes.byref(a), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_kv_append")
+        return q_out
+
+    def kv_read(self, cache: KVCache, slots, dtype=None, stream=None):
+        """The cached keys and values of int64 slots [n], dense [n][kv_heads][dim] (default bfloat16)."""
+        import torch
+        dt, n = dtype or torch.bfloat16, slots.shape[0]
+        shape = (n, cache.kv_heads, cache.head_dim)
+        k, v = self._out(stream, shape, dt, slots.device), self._out(stream, shape, dt, slots.device)
+        sp = self._indices("slots", slots, torch.int64, n)
+        if n == 0:
+            return k, v
+        st = self._lib.lq_kv_read(self._h, cache._ref, sp, n, k.data_ptr(), v.data_ptr(), _code(dt), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_kv_read")
+        return k, v
+
+    def kv_attention(self, q, cache: KVCache, block_table, lens, scale=None, prefix_table=None, prefix_len=None, out=None,
+                     lse=None, stream=None):
+        """Attention of q [batch][tokens][q_heads][dim] (each request's newest tokens, already in the cache)
+        over the cache: request b's own tokens in the pages block_table[b] (int32), lens[b] (int32) of
+        them, after the prefix_len tokens of prefix_table's pages, which all requests share.  Returns
+        out (q's shape and dtype) and the fp32 log-sum-exp [batch][tokens][q_heads]."""
+        import torch
+        B, T, hq, dim = q.shape
+        qs, dt = q.stride(), q.dtype
+        if out is None:
+            out = self._out(stream, (B, T, hq, dim), dt, q.device)
+        if lse is None:
+            lse = self._out(stream, (B, T, hq), torch.float32, q.device)
+        os = out.stride()
+        if dim != cache.head_dim or out.shape != q.shape or out.dtype != dt or lse.shape != q.shape[:3]:
+            raise ValueError(f"q and out must be [batch][tokens][heads][{cache.head_dim}] of one dtype, lse [batch][tokens][heads]")
+        for name, s in (("q", qs), ("out", os)):
+            if s[3] != 1 or (s[2] != dim and hq > 1) or (B > 1 and T > 1 and s[0] != T * s[1]):
+                raise ValueError(f"{name} must be rows of contiguous heads with one token stride")
+        if lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+                (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+            raise ValueError(f"block_table must be int32 [{B}][pages], rows contiguous")
+        dev = self.device
+        if q.get_device() != dev or out.get_device() != dev or lse.get_device() != dev or block_table.get_device() != dev:
+            raise ValueError(f"q, out, lse and block_table must be on cuda:{dev}")
+        pages = block_table.shape[1]
+        pp = None
+        if prefix_table is not None:
+            pp = self._indices("prefix_table", prefix_table, torch.int32, prefix_table.shape[0])
+            room = prefix_table.shape[0] * cache.page_size
+            prefix_len = room if prefix_len is None else prefix_len
+            if prefix_len > room:
+                raise ValueError("prefix_table has too few pages for prefix_len")
+        a = lq_kv_attention_args(q.data_ptr(), out.data_ptr(), lse.data_ptr(), _code(dt), B, T, hq,
+                                 qs[1] if T > 1 else (qs[0] if B > 1 else hq * dim),
+                                 os[1] if T > 1 else (os[0] if B > 1 else hq * dim), block_table.data_ptr(),
+                                 block_table.stride(0) if B > 1 else pages, pages,
+                                 self._indices("lens", lens, torch.int32, B), pp, prefix_len or 0,
+                                 dim ** -0.5 if scale is None else scale)
+        st = self._lib.lq_kv_attention(self._h, cache._ref, ctypes.byref(a), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_kv_attention")
+        return out, lse
 
     # ---- quantizers (the converter step; include/lq.h gives the definitions) ----
 

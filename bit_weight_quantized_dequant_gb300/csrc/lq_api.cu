@@ -143,6 +143,7 @@ LQ_API const char* lq_status_string(int status) {
         case LQ_ERR_CUDA: return "CUDA error";
         case LQ_ERR_TIMEOUT: return "a bounded device-side wait ran out";
         case LQ_ERR_RANGE: return "a dequantized weight is outside the binary16 range of the decode GEMV's operands";
+        case LQ_ERR_INDEX: return "a position, slot or page was outside its table or cache and was left out";
         default: return "unknown status";
     }
 }
@@ -226,6 +227,12 @@ LQ_API lq_status lq_sync(lq_handle h) {
         if (cudaMemset(h->status_flag, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
             return LQ_ERR_CUDA;
         return LQ_ERR_RANGE;
+    }
+    if (flag & lq::kStatusIndex) {
+        // a rotation, cache or attention kernel left out an element whose index was out of range
+        if (cudaMemset(h->status_flag, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+            return LQ_ERR_CUDA;
+        return LQ_ERR_INDEX;
     }
     return LQ_OK;
 }
@@ -393,6 +400,130 @@ LQ_API lq_status lq_quantize_nf4(lq_handle h, const float* W, int N, int K, uint
     DeviceGuard guard(h->device);
     if (!guard.ok) return LQ_ERR_CUDA;
     return lq::launch_quantize_nf4(W, N, K, codes, absmax, static_cast<cudaStream_t>(stream));
+}
+
+// ---- rotary positions, the low-bit KV cache and attention over it -------------------
+
+namespace {
+
+lq_status check_cache(const lq_kv_cache* c) {
+    if (!c || !c->pages || c->num_pages < 1 || c->page_size < 1 || c->page_size % 16 != 0 || c->kv_heads < 1)
+        return LQ_ERR_INVALID_ARG;
+    if (lq_kv_tile_bytes(c->bits, c->head_dim) == 0) return LQ_ERR_UNSUPPORTED;
+    if (!aligned16(c->pages)) return LQ_ERR_ALIGNMENT;
+    return LQ_OK;
+}
+
+int dtype_bytes(int dtype) { return dtype == LQ_F32 ? 4 : 2; }
+
+// A row operand: its first element and its token stride on 16-byte boundaries.
+bool aligned_rows(const void* p, int64_t token_stride, int dtype) {
+    return aligned16(p) && token_stride * dtype_bytes(dtype) % 16 == 0;
+}
+
+}  // namespace
+
+LQ_API int lq_kv_tile_bytes(int bits, int head_dim) {
+    if ((bits != 4 && bits != 8) || (head_dim != 64 && head_dim != 128)) return 0;
+    return 16 * (2 * head_dim * bits / 8 + 2 * (head_dim / 32) * 4);
+}
+
+LQ_API lq_status lq_rope_table(lq_handle h, const lq_rope_config* config, int first, int count, float* table,
+                               void* stream) {
+    if (!h || !config || !table || first < 0 || count < 1 || (int64_t)first + count > 0x7fffffffLL) return LQ_ERR_INVALID_ARG;
+    const lq_rope_config& c = *config;
+    if (c.rot_dim < 2 || c.rot_dim % 2 != 0) return LQ_ERR_INVALID_ARG;
+    if (c.rot_dim > 256) return LQ_ERR_UNSUPPORTED;
+    if (!(c.base > 1.0) || !(c.factor > 0.0) || !(c.original_length >= 0.0)) return LQ_ERR_INVALID_ARG;
+    if (c.factor < 1.0) return LQ_ERR_UNSUPPORTED;   // (frequencies stay within one radian per position)
+    if (c.original_length > 0.0 && !(c.high_rotations > c.low_rotations)) return LQ_ERR_INVALID_ARG;
+    if (!aligned16(table)) return LQ_ERR_ALIGNMENT;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_rope_table(h, c, first, count, table, static_cast<cudaStream_t>(stream));
+}
+
+LQ_API lq_status lq_rope(lq_handle h, const lq_rope_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_rope_args& a = *args;
+    if (!a.x || !a.y || !a.table || !a.positions || !valid_dtype(a.dtype)) return LQ_ERR_INVALID_ARG;
+    if (a.n < 0 || a.heads < 1 || a.head_dim < 1 || a.table_rows < 1) return LQ_ERR_INVALID_ARG;
+    if (a.rot_dim < 2 || a.rot_dim % 2 != 0 || a.rot_dim > a.head_dim) return LQ_ERR_INVALID_ARG;
+    if (a.layout != LQ_ROPE_HALF && a.layout != LQ_ROPE_INTERLEAVED) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)a.heads * a.head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if (a.x == a.y && (a.x_token_stride != a.y_token_stride || a.x_head_stride != a.y_head_stride)) return LQ_ERR_INVALID_ARG;
+    const uintptr_t e = (uintptr_t)dtype_bytes(a.dtype) - 1;
+    if ((reinterpret_cast<uintptr_t>(a.x) & e) || (reinterpret_cast<uintptr_t>(a.y) & e) ||
+        (reinterpret_cast<uintptr_t>(a.table) & 3) || (reinterpret_cast<uintptr_t>(a.positions) & 3))
+        return LQ_ERR_ALIGNMENT;
+    if (a.n == 0) return LQ_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_rope(h, a, static_cast<cudaStream_t>(stream));
+}
+
+LQ_API lq_status lq_kv_append(lq_handle h, const lq_kv_cache* cache, const lq_kv_append_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_status s = check_cache(cache);
+    if (s != LQ_OK) return s;
+    const lq_kv_append_args& a = *args;
+    if (!a.k || !a.v || !a.slots || !valid_dtype(a.dtype) || a.n < 0) return LQ_ERR_INVALID_ARG;
+    if (a.q && (!a.q_out || a.q_heads < 1)) return LQ_ERR_INVALID_ARG;
+    if (a.q && (int64_t)a.q_heads * cache->head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)cache->kv_heads * cache->head_dim > 0x3fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if (a.q && a.q == a.q_out && a.q_token_stride != a.q_out_token_stride) return LQ_ERR_INVALID_ARG;
+    if (a.table) {
+        if (!a.positions || a.table_rows < 1 || a.rot_dim < 2 || a.rot_dim > cache->head_dim) return LQ_ERR_INVALID_ARG;
+        if (a.layout != LQ_ROPE_HALF && a.layout != LQ_ROPE_INTERLEAVED) return LQ_ERR_INVALID_ARG;
+        if (a.rot_dim % 16 != 0) return LQ_ERR_UNSUPPORTED;
+        if (!aligned16(a.table) || (reinterpret_cast<uintptr_t>(a.positions) & 3)) return LQ_ERR_ALIGNMENT;
+    }
+    if (!aligned_rows(a.k, a.k_token_stride, a.dtype) || !aligned_rows(a.v, a.v_token_stride, a.dtype) ||
+        (reinterpret_cast<uintptr_t>(a.slots) & 7))
+        return LQ_ERR_ALIGNMENT;
+    if (a.q && (!aligned_rows(a.q, a.q_token_stride, a.dtype) || !aligned_rows(a.q_out, a.q_out_token_stride, a.dtype)))
+        return LQ_ERR_ALIGNMENT;
+    if (a.n == 0) return LQ_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_kv_append(h, *cache, a, static_cast<cudaStream_t>(stream));
+}
+
+LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t* slots, int n, void* k_out, void* v_out,
+                            int dtype, void* stream) {
+    if (!h) return LQ_ERR_INVALID_ARG;
+    const lq_status s = check_cache(cache);
+    if (s != LQ_OK) return s;
+    if (!slots || n < 0 || (!k_out && !v_out) || !valid_dtype(dtype)) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)cache->kv_heads * cache->head_dim > 0x3fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if (!aligned16(k_out) || !aligned16(v_out) || (reinterpret_cast<uintptr_t>(slots) & 7)) return LQ_ERR_ALIGNMENT;
+    if (n == 0) return LQ_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_kv_read(h, *cache, slots, n, k_out, v_out, dtype, static_cast<cudaStream_t>(stream));
+}
+
+LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_status s = check_cache(cache);
+    if (s != LQ_OK) return s;
+    const lq_kv_attention_args& a = *args;
+    if (!a.q || !a.out || !a.block_table || !a.lens) return LQ_ERR_INVALID_ARG;
+    if (a.dtype != LQ_F16 && a.dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
+    if (a.batch < 1 || a.tokens < 1 || a.q_heads < 1 || a.q_heads % cache->kv_heads != 0) return LQ_ERR_INVALID_ARG;
+    if (a.batch > lq::kMaxAttnBatch || a.tokens > lq::kMaxAttnTokens) return LQ_ERR_UNSUPPORTED;
+    if (a.max_pages < 1 || a.block_table_stride < a.max_pages || a.prefix_len < 0) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)a.max_pages * cache->page_size > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if (a.prefix_len > 0 && !a.prefix_table) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)a.q_heads * cache->head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if (!(a.scale > 0.f) || !(a.scale < 3.0e38f)) return LQ_ERR_INVALID_ARG;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(a.block_table) | reinterpret_cast<uintptr_t>(a.lens) |
+                            reinterpret_cast<uintptr_t>(a.prefix_table) | reinterpret_cast<uintptr_t>(a.lse);
+    if (!aligned_rows(a.q, a.q_token_stride, a.dtype) || !aligned_rows(a.out, a.out_token_stride, a.dtype) || (words & 3))
+        return LQ_ERR_ALIGNMENT;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_kv_attention(h, *cache, a, static_cast<cudaStream_t>(stream));
 }
 
 // ---- the allocation-free GEMV entry point ---------------------------------------

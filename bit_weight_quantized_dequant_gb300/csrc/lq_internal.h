@@ -107,4 +107,15 @@ lq_status launch_quantize_2bit(lq_handle h, const float* W, int N, int K, const 
 lq_status launch_quantize_nf4(const float* W, int N, int K, uint8_t* codes, float* absmax, cudaStream_t stream);
 lq_status launch_gemm_grouped(lq_handle h, const lq_problem* problems, int count, cudaStream_t stream);
 
+constexpr int kStatusIndex = 4;         // status word: a position, slot or page out of range was left out
+constexpr int kMaxAttnBatch = 1024;     // requests of one attention call
+constexpr int kMaxAttnTokens = 64;      // query tokens of a request
+
+lq_status launch_rope_table(lq_handle h, const lq_rope_config& c, int first, int count, float* table, cudaStream_t stream);
+lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream);
+lq_status launch_kv_append(lq_handle h, const lq_kv_cache& c, const lq_kv_append_args& a, cudaStream_t stream);
+lq_status launch_kv_read(lq_handle h, const lq_kv_cache& c, const int64_t* slots, int n, void* k, void* v, int dtype,
+                         cudaStream_t stream);
+lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, cudaStream_t stream);
+
 }  // namespace lq

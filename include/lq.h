@@ -116,8 +116,10 @@ typedef enum lq_status {
     LQ_ERR_WORKSPACE = 4,     /* the handle's workspace is too small for this call */
     LQ_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
     LQ_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out (reported by lq_sync) */
-    LQ_ERR_RANGE = 7          /* a decode GEMV met a weight table value |S*C+Z| >= 65520, outside the
+    LQ_ERR_RANGE = 7,         /* a decode GEMV met a weight table value |S*C+Z| >= 65520, outside the
                                  binary16 range of its tensor-core operands (reported by lq_sync) */
+    LQ_ERR_INDEX = 8          /* a kernel met a position outside the rotation table, or a slot or page
+                                 outside the cache, and left that element out (reported by lq_sync) */
 } lq_status;
 
 typedef enum lq_format {
@@ -414,6 +416,155 @@ LQ_API lq_status lq_stream_destroy(lq_layer_stream s);
 LQ_API lq_status lq_stream_run_direct(lq_handle h, const void* host_layers, size_t host_stride, size_t layer_bytes,
                                       int L, const lq_problem* problems, int count, int64_t y_layer_stride,
                                       void* stream);
+
+/* ---- The attention block of a decode step ---------------------------------------------
+ *
+ * Between the q, k, v projections and the output projection of a decoder layer: rotary
+ * positions, a low-bit paged cache of keys and values, and attention over it.  The shared
+ * conventions hold, with these differences: tables, positions, slots, block tables and
+ * lengths are device arrays whose contents the kernels check as they read them (a bad
+ * entry is left out and reported by the next lq_sync as LQ_ERR_INDEX), and lq_rope takes
+ * rows of any alignment.
+ */
+
+/*
+ * The rotation table: row p (p = first .. first + count - 1) holds cos(p w_i) * mscale for
+ * i = 0 .. rot_dim/2 - 1, then sin(p w_i) * mscale, fp32.  w_i = base^(-2i/rot_dim), scaled
+ * for contexts longer than the model was made for:
+ *   original_length = 0: w_i / factor (factor 1: unscaled);
+ *   original_length > 0: by parts.  With r_i = original_length * w_i / (2 pi) rotations over
+ *     the original length and a = clamp((r_i - low_rotations) / (high_rotations -
+ *     low_rotations), 0, 1): w_i (a + (1 - a) / factor).
+ * The angle is p * w_i in 64-bit fixed-point turns, exact modulo one turn at every position.
+ * rot_dim even, 2 .. 256; base > 1; factor >= 1; high_rotations > low_rotations when by parts.
+ */
+typedef struct lq_rope_config {
+    int rot_dim;
+    double base, factor, original_length, low_rotations, high_rotations;
+    float mscale;
+} lq_rope_config;
+
+LQ_API lq_status lq_rope_table(lq_handle h, const lq_rope_config* config, int first, int count, float* table,
+                               void* stream);
+
+typedef enum lq_rope_layout {
+    LQ_ROPE_HALF = 0,         /* pairs (i, i + rot_dim/2) */
+    LQ_ROPE_INTERLEAVED = 1   /* pairs (2i, 2i + 1) */
+} lq_rope_layout;
+
+/*
+ * lq_rope — rotate the first rot_dim dimensions of every head of n tokens, copy the others:
+ * pair (a, b) with the table row of positions[token] becomes (a c - b s, a s + b c), or with
+ * `inverse` (a c + b s, b c - a s), the transpose, which carries the gradient back.  Each
+ * product and sum is rounded to fp32, the result once to dtype.  x and y: [n][heads][head_dim]
+ * with the given token and head strides (in elements, dimensions contiguous); y may be x when
+ * the strides are equal.  Rows aligned to 16 bytes, head_dim % 8 == 0 (up to 256) and
+ * rot_dim % 16 == 0 take the wide path; anything else runs one pair per thread.
+ */
+typedef struct lq_rope_args {
+    const void* x;
+    void* y;
+    int dtype;                 /* LQ_F32, LQ_F16 or LQ_BF16, of x and y */
+    int n, heads, head_dim, rot_dim;
+    int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+    const float* table;        /* [table_rows][rot_dim], lq_rope_table's rows from position 0 */
+    int table_rows;
+    const int32_t* positions;  /* [n]; outside [0, table_rows): copied unrotated, LQ_ERR_INDEX */
+    int layout, inverse;
+} lq_rope_args;
+
+LQ_API lq_status lq_rope(lq_handle h, const lq_rope_args* args, void* stream);
+
+/*
+ * The cache: `num_pages` pages of `page_size` tokens (a multiple of 16) for `kv_heads` heads of
+ * `head_dim` (64 or 128) dimensions, keys and values in `bits` (4 or 8) bits.  A slot is
+ * page * page_size + token of the page.  For each token, head and group of 32 dimensions, of
+ * keys and of values, with x clamped to +-65504:
+ *     Z = binary16(min x),  S = binary16((max x - min x) * fl32(1 / (2^bits - 1)))
+ *     c = clamp(rint((x - Z) / S), 0, 2^bits - 1), 0 when S == 0      (fp32, each step rounded)
+ *     value = S * c + Z                                                (fp32, exact or one rounding)
+ * A NaN in the group makes its S and Z NaN.  Infinities are clamped with the rest.
+ * Storage: [num_pages][kv_heads][page_size / 16] tiles of lq_kv_tile_bytes(bits, head_dim)
+ * bytes, each the codes of 16 tokens' keys, then values, in the order of the attention
+ * kernel's operand fragments, then their S and Z (csrc/lq_kv.cuh writes the order down).
+ * The memory is the caller's and may start as anything: attention never uses a slot at or
+ * past a request's length.
+ */
+typedef struct lq_kv_cache {
+    void* pages;
+    int64_t num_pages;
+    int page_size, kv_heads, head_dim, bits;
+} lq_kv_cache;
+
+/* Bytes of a tile (16 tokens of one head), 0 for bits or head_dim that the cache does not have.  Host-only. */
+LQ_API int lq_kv_tile_bytes(int bits, int head_dim);
+
+/*
+ * lq_kv_append — write n tokens' keys and values into the cache: token i into slots[i] (a
+ * negative slot writes nothing; two tokens of one call with the same slot race).  With a
+ * table, the keys are rotated first as lq_rope does (rounded to dtype, then quantised), and
+ * so is q, when given, into q_out: one launch for a decode step's rotation and cache write.
+ * k, v: [n][kv_heads][head_dim], q, q_out: [n][q_heads][head_dim], token strides in
+ * elements, heads and dimensions contiguous, rows 16-byte aligned.  rot_dim % 16 == 0.
+ * q_out may be q.  Without q, q_heads is ignored; without a table, table_rows, positions,
+ * rot_dim and layout are, and q is copied.
+ */
+typedef struct lq_kv_append_args {
+    const void *k, *v, *q;
+    void* q_out;
+    int dtype;                 /* LQ_F32, LQ_F16 or LQ_BF16, of k, v, q and q_out */
+    int n, q_heads;
+    int64_t k_token_stride, v_token_stride, q_token_stride, q_out_token_stride;
+    const int64_t* slots;      /* [n]; past the last slot: nothing written, LQ_ERR_INDEX */
+    const float* table;
+    int table_rows;
+    const int32_t* positions;
+    int rot_dim, layout;
+} lq_kv_append_args;
+
+LQ_API lq_status lq_kv_append(lq_handle h, const lq_kv_cache* cache, const lq_kv_append_args* args, void* stream);
+
+/*
+ * lq_kv_read — the cached values of n slots as dense rows: k_out and v_out [n][kv_heads]
+ * [head_dim] in dtype (either may be NULL), S * c + Z rounded once.  A negative slot, or one
+ * past the last (LQ_ERR_INDEX), gives zeros.
+ */
+LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t* slots, int n, void* k_out, void* v_out,
+                            int dtype, void* stream);
+
+/*
+ * lq_kv_attention — attention of the newest `tokens` (1 .. 64) tokens of each of `batch`
+ * (1 .. 1024) requests over the cache: for query head h of token t of request b,
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
+ * over kv head h / (q_heads / kv_heads) and these keys j, in 32-bit statistics:
+ *   - the prefix_len tokens of the pages prefix_table[], which all requests share: their
+ *     part is computed once for all requests' rows together;
+ *   - the request's own tokens j < lens[b] - tokens + 1 + t (lens counts the query tokens,
+ *     which are in the cache already), token j in slot block_table[b][j / page_size] *
+ *     page_size + j % page_size.
+ * A row with no key gives out = 0 and lse = -inf.  lens[b] is taken as 0 below 0 and as
+ * max_pages * page_size above that.  A page outside the cache (LQ_ERR_INDEX) hides its tokens.
+ * q, out: [batch][tokens][q_heads][head_dim] of dtype (LQ_F16 or LQ_BF16), token strides in
+ * elements, rows 16-byte aligned; lse: fp32 [batch][tokens][q_heads] or NULL.  S of the
+ * cache is not negative.  Uses the handle's workspace; LQ_ERR_WORKSPACE when it is too small.
+ */
+typedef struct lq_kv_attention_args {
+    const void* q;
+    void* out;
+    float* lse;
+    int dtype;
+    int batch, tokens, q_heads;
+    int64_t q_token_stride, out_token_stride;
+    const int32_t* block_table;   /* [batch][block_table_stride], max_pages of each row used */
+    int64_t block_table_stride;
+    int max_pages;
+    const int32_t* lens;          /* [batch] */
+    const int32_t* prefix_table;  /* [ceil(prefix_len / page_size)], NULL when prefix_len == 0 */
+    int prefix_len;
+    float scale;
+} lq_kv_attention_args;
+
+LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, void* stream);
 
 /*
  * lq_selftest_wait — exercises the timeout path of the kernels' bounded waits.  One
