@@ -45,8 +45,14 @@ namespace lq {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kUnitCost = 28;    // what a unit costs a block besides its tiles, in tiles
+constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
 constexpr float kTau = 3.f;      // a row's reference moves when a score passes it by 2^3
 constexpr float kPBits = 11.f;   // P = 2^11 p
+// S 2^ks stays at or below kMostS (2^14 times that is finite); ks = 0 where the first tile's largest S lies
+// between the two, so that the multiplication is skipped; otherwise it brings the largest into [1, 2)
+constexpr float kMostS = 3.9f, kLeastS = 0x1p-8f;
+constexpr int kUnset = 99;
 
 struct AttnParams {
     KvView cache;
@@ -72,24 +78,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
+// m16n8k16 with binary16 operands and fp32 sums: D += A B, and D = A B.  (Not volatile: free to
+// be scheduled among the mask instructions around them.)
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -131,8 +137,7 @@ struct AttnSmem {
     static constexpr int kMl = kRed + 4 * kRows * kPitch * 4;              // [warps][rows] m, l
     static constexpr int kTot = kMl + kWarps * kRows * 8;                  // [rows] m, l of the unit
     static constexpr int kBars = kTot + kRows * 8;
-    static constexpr int kFlags = kBars + kWarps * kStages * 8;
-    static constexpr int kCum = (kFlags + kWarps * kStages * 4 + 15) / 16 * 16;   // then [requests + 1] int64
+    static constexpr int kCum = kBars + kWarps * kStages * 8;              // then [requests + 1] int2
 };
 
 // The rows' sums of one warp.
@@ -140,7 +145,8 @@ template <int D, int NT>
 struct State {
     float o[NT][D / 16][4];   // O^T, code part: dims (8 (2 i) + n, 8 (2 i + 1) + n) x rows (2 t, 2 t + 1), scaled
     float oz[NT][4];          // sum p Z: group n x rows
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2]; // rows' references and sums of P
+    float ref[NT][2];         // what scores lose before 2^x: m - 11, 0 while m is -inf
     int ks;
 };
 
@@ -152,7 +158,7 @@ struct QFrag {
 };
 
 template <int BITS, int D, int NT, class T>
-__device__ __forceinline__ void load_q(const AttnParams& P, QFrag<BITS, D, NT>& Q, int64_t row0, int rows, int head, int n, int t) {
+__device__ __forceinline__ void load_q(const AttnParams& P, QFrag<BITS, D, NT>& Q, int row0, int rows, int head, int n, int t) {
     constexpr int G = D / 32;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -160,9 +166,9 @@ __device__ __forceinline__ void load_q(const AttnParams& P, QFrag<BITS, D, NT>& 
         float v[G][8];
         float top = 0.f;
         if (r < rows) {
-            const int64_t row = row0 + r, bt = row / P.group;
+            const int row = row0 + r, bt = row / P.group;
             const uint16_t* src = static_cast<const uint16_t*>(P.q) + bt * P.q_stride +
-                                  (int64_t)(head * P.group + (int)(row - bt * P.group)) * D + 8 * t;
+                                  (int64_t)(head * P.group + (row - bt * P.group)) * D + 8 * t;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const uint4 u = *reinterpret_cast<const uint4*>(src + 32 * g);
@@ -220,11 +226,11 @@ __device__ __forceinline__ void load_q(const AttnParams& P, QFrag<BITS, D, NT>& 
     }
 }
 
-// One 16-token tile in shared memory at `tile`: scores, new statistics, O.  `left`: tokens of the
-// request from the tile's first on; vis: the same for each row (fewer for earlier query tokens).
-template <int BITS, int D, int NT>
-__device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT>& Q, State<D, NT>& A, int left, bool edge,
-                                          const int (&vis)[NT][2], int lane) {
+// One 16-token tile in shared memory at `tile`, its first token j0: scores, new statistics, O.
+// Rows see seen[] tokens of the request's len (kEdge: some row may not see the whole tile).
+template <int BITS, int D, int NT, bool kEdge>
+__device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS, D, NT>& Q, State<D, NT>& A, int j0, int len,
+                                          const int (&seen)[NT][2], int lane) {
     using L = KvLayout<BITS, D>;
     constexpr int G = D / 32, MT = D / 16, WK = L::WK, WV = L::WV;
     const int n = lane >> 2, t = lane & 3;
@@ -251,16 +257,8 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
         }
         float tot[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[nt][i] = 0.f;
-#pragma unroll
         for (int g = 0; g < G; ++g) {
             float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 uint32_t a0, a1, a2, a3;
@@ -272,28 +270,29 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
                     a0 = w0 & 0x00ff00ffu, a1 = w1 & 0x00ff00ffu, a2 = (w0 >> 8) & 0x00ff00ffu, a3 = (w1 >> 8) & 0x00ff00ffu;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt], a0, a1, a2, a3, Q.b[nt][2 * g + u][0], Q.b[nt][2 * g + u][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (u == 0) mma_first(acc[nt], a0, a1, a2, a3, Q.b[nt][2 * g][0], Q.b[nt][2 * g][1]);
+                    else mma_add(acc[nt], a0, a1, a2, a3, Q.b[nt][2 * g + 1][0], Q.b[nt][2 * g + 1][1]);
+                }
             }
             const float2 f0 = unpack2(s0[g >> 1]), f1 = unpack2(s1[g >> 1]);
             const float sa = g & 1 ? f0.y : f0.x, sb = g & 1 ? f1.y : f1.x;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                tot[nt][0] = fmaf(sa, acc[nt][0], tot[nt][0]);
-                tot[nt][1] = fmaf(sa, acc[nt][1], tot[nt][1]);
-                tot[nt][2] = fmaf(sb, acc[nt][2], tot[nt][2]);
-                tot[nt][3] = fmaf(sb, acc[nt][3], tot[nt][3]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tot[nt][i] = g ? fmaf(i < 2 ? sa : sb, acc[nt][i], tot[nt][i]) : (i < 2 ? sa : sb) * acc[nt][i];
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float az[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(az, z0, z1, z0, z1, Q.z[nt][0], Q.z[nt][1]);
+            float az[4];
+            mma_first(az, z0, z1, z0, z1, Q.z[nt][0], Q.z[nt][1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(tot[nt][i], 16777216.f, az[i]) * Q.f[nt][i & 1];
-            if (edge) {
+            if (kEdge) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (n + 8 * (i >> 1) >= vis[nt][i & 1]) x[nt][i] = -INFINITY;
+                    if (j0 + n + 8 * (i >> 1) >= seen[nt][i & 1]) x[nt][i] = -INFINITY;
             }
         }
     }
@@ -301,46 +300,53 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
     // ---- values' scales, and whether a row's reference or the scales' power of two has to move ----
     uint32_t vs[G][2];
     uint32_t zz[2] = {0u, 0u};
+    // whatever lies past the request's end counts as zero
+    const int left = len - j0;
+    const uint32_t k0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
+    const uint32_t k1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+    auto load_scales = [&] {
 #pragma unroll
-    for (int g = 0; g < G; ++g) *reinterpret_cast<uint2*>(vs[g]) = lds64(tile + L::kVs + g * 32 + 8 * t);
-    if (n < G) *reinterpret_cast<uint2*>(zz) = lds64(tile + L::kVz + n * 32 + 8 * t);
-    if (edge && left < kKvTile) {   // whatever lies past the request's end counts as zero
-        const uint32_t k0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
-        const uint32_t k1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+        for (int g = 0; g < G; ++g) *reinterpret_cast<uint2*>(vs[g]) = lds64(tile + L::kVs + g * 32 + 8 * t);
+        if (kEdge) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) vs[g][0] &= k0, vs[g][1] &= k1;
-        zz[0] &= k0, zz[1] &= k1;
-    }
-    uint32_t sc[G][2];
-    auto scaled = [&] {
-        const uint32_t k2 = (uint32_t)(A.ks + 15) * 0x04000400u;   // binary16 2^ks, twice
-#pragma unroll
-        for (int g = 0; g < G; ++g) sc[g][0] = hmul2(vs[g][0], k2), sc[g][1] = hmul2(vs[g][1], k2);
+            for (int g = 0; g < G; ++g) vs[g][0] &= k0, vs[g][1] &= k1;
+        }
     };
-    scaled();
-    uint32_t big = hmax2(sc[0][0], sc[0][1]);
+    load_scales();
+    if (n < G) *reinterpret_cast<uint2*>(zz) = lds64(tile + L::kVz + n * 32 + 8 * t);
+    if (kEdge) zz[0] &= k0, zz[1] &= k1;
+    // S 2^ks: below 3.9, so that P S stays finite, and not tiny; S as it is (ks = 0) in between
+    auto largest = [&] {
+        uint32_t m = hmax2(vs[0][0], vs[0][1]);
 #pragma unroll
-    for (int g = 1; g < G; ++g) big = hmax2(big, hmax2(sc[g][0], sc[g][1]));
+        for (int g = 1; g < G; ++g) m = hmax2(m, hmax2(vs[g][0], vs[g][1]));
+        return m;
+    };
+    auto scale_by = [&](int e) {
+        const uint32_t k2 = (uint32_t)(e + 15) * 0x04000400u;   // binary16 2^e, twice
+#pragma unroll
+        for (int g = 0; g < G; ++g) vs[g][0] = hmul2(vs[g][0], k2), vs[g][1] = hmul2(vs[g][1], k2);
+    };
+    if (A.ks != 0 && A.ks != kUnset) scale_by(A.ks);
+    const uint32_t big = largest();
     const float2 bf = unpack2(big);
-    bool move = fmaxf(bf.x, bf.y) > 3.9f;
+    bool move = fmaxf(bf.x, bf.y) > kMostS || A.ks == kUnset;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) move |= fmaxf(x[nt][i], x[nt][i + 2]) > A.m[nt][i] + kTau;
     if (__any_sync(0xffffffffu, move)) {
-        float top = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 s = unpack2(vs[g][i]);
-                top = fmaxf(top, fmaxf(s.x, s.y));
-            }
+        const int had = A.ks == kUnset ? 0 : A.ks;
+        if (had != 0) load_scales();   // (S as stored: times 2^had it may have overflowed)
+        const float2 raw = unpack2(largest());
+        float top = fmaxf(raw.x, raw.y);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int ks = A.ks;
-        if (top * pow2i(ks) > 3.9f) ks = max(-14, 127 - (int)(__float_as_uint(top) >> 23));
-        const float down = pow2i(ks - A.ks);
+        int ks = had;
+        if (top * pow2i(had) > kMostS || (A.ks == kUnset && top < kLeastS))
+            ks = min(max(127 - (int)(__float_as_uint(top) >> 23), -14), 15);
+        if (ks != 0) scale_by(ks);
+        const float down = pow2i(ks - had);
         A.ks = ks;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -353,6 +359,7 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
                 const float now = mx > A.m[nt][i] + kTau ? mx : A.m[nt][i];
                 a[i] = A.m[nt][i] == now ? 1.f : ex2(A.m[nt][i] - now);
                 A.m[nt][i] = now;
+                A.ref[nt][i] = now == -INFINITY ? 0.f : now - kPBits;
                 A.l[nt][i] *= a[i];
             }
 #pragma unroll
@@ -362,20 +369,19 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
 #pragma unroll
                 for (int i = 0; i < 4; ++i) A.o[nt][k][i] *= a[i & 1] * down;
         }
-        scaled();
     }
 
     // ---- probabilities, transposed to the second product's operand ----
     uint32_t p[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = A.m[nt][0] == -INFINITY ? 0.f : A.m[nt][0] - kPBits, r1 = A.m[nt][1] == -INFINITY ? 0.f : A.m[nt][1] - kPBits;
-        const float e0 = ex2(x[nt][0] - r0), e1 = ex2(x[nt][1] - r1), e2 = ex2(x[nt][2] - r0), e3 = ex2(x[nt][3] - r1);
+        const float e0 = ex2(x[nt][0] - A.ref[nt][0]), e1 = ex2(x[nt][1] - A.ref[nt][1]);
+        const float e2 = ex2(x[nt][2] - A.ref[nt][0]), e3 = ex2(x[nt][3] - A.ref[nt][1]);
         A.l[nt][0] += e0 + e2;
         A.l[nt][1] += e1 + e3;
         p[nt][0] = movmatrix(pack_half2_rn(e0, e1));
         p[nt][1] = movmatrix(pack_half2_rn(e2, e3));
-        mma_f16_16816(A.oz[nt], zz[0], 0u, zz[1], 0u, p[nt][0], p[nt][1]);
+        mma_add(A.oz[nt], zz[0], 0u, zz[1], 0u, p[nt][0], p[nt][1]);
     }
 
     // ---- O^T += V^T (P S)^T ----
@@ -399,38 +405,110 @@ __device__ __forceinline__ void tile_step(uint32_t tile, const QFrag<BITS, D, NT
     for (int g = 0; g < G; ++g) {
         uint32_t b[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) b[nt][0] = hmul2(p[nt][0], sc[g][0]), b[nt][1] = hmul2(p[nt][1], sc[g][1]);
+        for (int nt = 0; nt < NT; ++nt) b[nt][0] = hmul2(p[nt][0], vs[g][0]), b[nt][1] = hmul2(p[nt][1], vs[g][1]);
 #pragma unroll
         for (int k = 2 * g; k < 2 * g + 2; ++k) {
             const uint32_t a0 = slab(2 * k, 0), a1 = slab(2 * k + 1, 0), a2 = slab(2 * k, 1), a3 = slab(2 * k + 1, 1);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(A.o[nt][k], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_add(A.o[nt][k], a0, a1, a2, a3, b[nt][0], b[nt][1]);
         }
     }
 }
 
-// A finished row's element: v / l, joined with the prefix's row in the second run.
+// Where a row's result goes, and its factors: out = v * own (+ the prefix's row * pre).
 template <int D, class T>
-__device__ __forceinline__ void finish(const AttnParams& P, int64_t row, int head, int d, float v, float m, float l) {
-    float o = l == 0.f ? 0.f : v / l, s = l == 0.f ? -INFINITY : m + log2f(l) - kPBits;
-    const int64_t at = (int64_t)head * P.all_rows + row;
-    if (P.prefix == 1) {
-        P.pre_o[at * D + d] = o;
-        if (d == 0) P.pre_lse[at] = s;
-        return;
-    }
-    if (P.prefix == 2) {
-        const float s2 = P.pre_lse[at], top = fmaxf(s, s2);
-        if (top != -INFINITY) {
-            const float a = exp2f(s - top), c = exp2f(s2 - top);
-            o = (o * a + P.pre_o[at * D + d] * c) / (a + c);
-            s = top + log2f(a + c);
+struct RowOut {
+    T* out;
+    float *pre, own, shared;
+    // row: of all requests' rows of a kv head; (m, l): reference and sum of P.  One lane (`writes`)
+    // stores the log-sum-exp.
+    __device__ __forceinline__ RowOut(const AttnParams& P, int row, int head, float m, float l, bool writes) {
+        float s = l == 0.f ? -INFINITY : m + log2f(l) - kPBits;
+        own = l == 0.f ? 0.f : 1.f / l;
+        shared = 0.f;
+        const int64_t at = (int64_t)head * P.all_rows + row;
+        pre = P.pre_o + at * D;
+        if (P.prefix == 1) {
+            if (writes) P.pre_lse[at] = s;
+            return;
         }
+        if (P.prefix == 2) {
+            const float s2 = __ldcg(P.pre_lse + at), top = fmaxf(s, s2);
+            if (top != -INFINITY) {
+                const float a = ex2(s - top), c = ex2(s2 - top), f = 1.f / (a + c);
+                own *= a * f;
+                shared = c * f;
+                s = top + log2f(a + c);
+            }
+        }
+        const int bt = row / P.group, qh = head * P.group + (row - bt * P.group);
+        out = static_cast<T*>(P.out) + bt * P.out_stride + (int64_t)qh * D;
+        if (writes && P.lse) P.lse[(int64_t)bt * P.q_heads + qh] = s * 0.6931471805599453f;
     }
-    const int64_t bt = row / P.group;
-    const int qh = head * P.group + (int)(row - bt * P.group);
-    static_cast<T*>(P.out)[bt * P.out_stride + (int64_t)qh * D + d] = (T)o;
-    if (d == 0 && P.lse) P.lse[bt * P.q_heads + qh] = s * 0.6931471805599453f;
+    // V dimensions from d on
+    template <int V>
+    __device__ __forceinline__ void store(const AttnParams& P, int d, float (&v)[V]) const {
+        if (P.prefix == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) pre[d + i] = v[i] * own;
+            return;
+        }
+        alignas(4 * V) T o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] *= own;
+            if (P.prefix == 2) v[i] = fmaf(__ldcg(pre + d + i), shared, v[i]);
+            o[i] = (T)v[i];
+        }
+        if (V == 4) *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(o);
+        else *reinterpret_cast<uint32_t*>(out + d) = *reinterpret_cast<const uint32_t*>(o);
+    }
+};
+
+// A unit's partial sums of blocks c0 .. c1, joined in block order: a warp per row, D / 32
+// dimensions per lane, the blocks' factors 32 at a time (one per lane).
+template <int D, int R, class T>
+__device__ __forceinline__ void join(const AttnParams& P, int c0, int c1, int warp, int lane, int rows, int row0, int head) {
+    constexpr int V = D / 32;
+    constexpr int kSlot = R * (D + 2);   // (slots of all blocks together: within 32 bits)
+    auto from = [&](int k) { return P.part + (unsigned)(2 * k + (k == c0 ? 1 : 0)) * kSlot; };
+    for (int r = warp; r < rows; r += kWarps) {
+        float top = -INFINITY, l = 0.f, v[V] = {};
+        for (int k = c0 + lane; k <= c1; k += 32) top = fmaxf(top, __ldcg(from(k) + R * D + 2 * r));
+        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float ref = top == -INFINITY ? 0.f : top;
+        for (int k0 = c0; k0 <= c1; k0 += 32) {
+            const int m = min(32, c1 + 1 - k0);
+            float f = 0.f;
+            if (lane < m) {
+                const float2 e = __ldcg(reinterpret_cast<const float2*>(from(k0 + lane) + R * D + 2 * r));
+                f = ex2(e.x - ref);
+                l = fmaf(e.y, f, l);
+            }
+            // sixteen blocks' values in flight at a time
+            for (int j0 = 0; j0 < m; j0 += 16) {
+                float o[16][V];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float* a = from(k0 + min(j0 + j, m - 1)) + r * D + V * lane;
+#pragma unroll
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 e = __ldcg(reinterpret_cast<const float2*>(a + i));
+                        o[j][i] = e.x, o[j][i + 1] = e.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (j0 + j < m) v[i] = fmaf(o[j][i], fj, v[i]);
+                }
+            }
+        }
+        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+        RowOut<D, T>(P, row0 + r, head, top, l, lane == 0).store(P, V * lane, v);
+    }
 }
 
 template <int BITS, int D, int NT, class T>
@@ -442,110 +520,143 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
     float* red = reinterpret_cast<float*>(smem + M::kRed);
     float2* ml = reinterpret_cast<float2*>(smem + M::kMl);
     float2* total_ml = reinterpret_cast<float2*>(smem + M::kTot);
-    volatile int* flags = reinterpret_cast<volatile int*>(smem + M::kFlags);
-    int64_t* cum = reinterpret_cast<int64_t*>(smem + M::kCum);
+    int2* cum = reinterpret_cast<int2*>(smem + M::kCum);   // running sums over requests of a unit's (tiles, pieces)
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, t = lane & 3;
 
-    // tiles of each request (one at least, so that every unit is somebody's), their running sum
-    for (int b = tid; b < P.requests; b += 32 * kWarps) {
-        const int len = P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len;
-        cum[b + 1] = max(1, (len + kKvTile - 1) / kKvTile);
-    }
     const uint32_t bars = smem_u32(smem + M::kBars) + 8 * S * warp;
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
     }
+    pdl_launch_dependents();
+    pdl_wait();
+    auto len_of = [&](int b) { return P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len; };
+    // a unit has one tile at least, so that every unit is somebody's
+    for (int b = tid; b < P.requests; b += 32 * kWarps) {
+        const int tiles = max(1, (len_of(b) + kKvTile - 1) / kKvTile);
+        cum[b + 1] = make_int2(tiles, (tiles + kPiece - 1) / kPiece);
+    }
     __syncthreads();
     if (warp == 0) {
-        int64_t base = 0;
+        int2 base = make_int2(0, 0);
         for (int b0 = 0; b0 < P.requests; b0 += 32) {
-            int64_t v = b0 + lane < P.requests ? cum[b0 + lane + 1] : 0;
+            int2 v = b0 + lane < P.requests ? cum[b0 + lane + 1] : make_int2(0, 0);
             for (int s = 1; s < 32; s <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, v, s);
-                if (lane >= s) v += o;
+                const int x = __shfl_up_sync(0xffffffffu, v.x, s), y = __shfl_up_sync(0xffffffffu, v.y, s);
+                if (lane >= s) v.x += x, v.y += y;
             }
-            if (b0 + lane < P.requests) cum[b0 + lane + 1] = base + v;
-            base += __shfl_sync(0xffffffffu, v, 31);
+            if (b0 + lane < P.requests) cum[b0 + lane + 1] = make_int2(base.x + v.x, base.y + v.y);
+            base.x += __shfl_sync(0xffffffffu, v.x, 31);
+            base.y += __shfl_sync(0xffffffffu, v.y, 31);
         }
-        if (lane == 0) cum[0] = 0;
+        if (lane == 0) cum[0] = make_int2(0, 0);
     }
     __syncthreads();
 
-    // this block's range of the tile sequence; with few tiles, fewer blocks of a tile per warp
-    const int per_tile = P.cache.kv_heads * P.row_tiles;   // units of a request
-    const int64_t total = cum[P.requests] * per_tile;
-    const int64_t C = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
-    const int64_t c = blockIdx.x;
-    if (c >= C) return;
-    const int64_t g0 = total * c / C, g1 = total * (c + 1) / C;
-    auto request_of = [&](int64_t gt) {   // last b with per_tile * cum[b] <= gt
+    // This block's tiles [g0, g1) of the sequence: a piece of one unit where all pieces fit the grid at once,
+    // an equal share of all tiles otherwise.
+    const int per = P.cache.kv_heads * P.row_tiles;   // units of a request
+    const int c = blockIdx.x, C = gridDim.x;
+    const bool pieces = (int64_t)cum[P.requests].y * per <= C;
+    // (a share counts kUnitCost tiles before each unit's own, for what a unit costs a block besides them)
+    const int total = (cum[P.requests].x + kUnitCost * P.requests) * per, q = total / C, rem = total - q * C;
+    auto last = [&](auto start, int at) {             // last request b with per * start(b) <= at
         int lo = 0, hi = P.requests - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] * per_tile <= gt) lo = mid;
+            if (start(mid) * per <= at) lo = mid;
             else hi = mid - 1;
         }
         return lo;
     };
+    auto request_of = [&](int gt) { return last([&](int i) { return cum[i].x; }, gt); };
+    auto costly = [&](int i) { return cum[i].x + kUnitCost * i; };
+    auto block_of = [&](int at) { return at < rem * (q + 1) ? at / (q + 1) : rem + (at - rem * (q + 1)) / q; };
+    auto tile_at = [&](int at) {                      // first tile at or after a place of the shares' sequence
+        if (at >= total) return cum[P.requests].x * per;
+        const int i = last(costly, at), tiles = cum[i + 1].x - cum[i].x, in = at - costly(i) * per;
+        const int u = in / (tiles + kUnitCost);
+        return cum[i].x * per + u * tiles + max(0, in - u * (tiles + kUnitCost) - kUnitCost);
+    };
+    int g0, g1, b, unit, piece = 0, of = 1;
+    if (pieces) {
+        if (c >= cum[P.requests].y * per) return;
+        b = last([&](int i) { return cum[i].y; }, c);
+        of = cum[b + 1].y - cum[b].y;
+        unit = (c - cum[b].y * per) / of;
+        piece = c - cum[b].y * per - unit * of;
+        const int each = cum[b + 1].x - cum[b].x, us = cum[b].x * per + unit * each;
+        const int pq = each / of, pr = each - pq * of;
+        g0 = us + pq * piece + min(piece, pr);
+        g1 = us + pq * (piece + 1) + min(piece + 1, pr);
+    } else {
+        g0 = tile_at(q * c + min(c, rem));
+        g1 = tile_at(q * (c + 1) + min(c + 1, rem));
+        if (g0 >= g1) return;
+        b = request_of(g0);
+        unit = (g0 - cum[b].x * per) / (cum[b + 1].x - cum[b].x);
+    }
 
     // ---- this warp's tiles: 32 addresses at a time, one per lane, issued S ahead ----
     const uint32_t ring = smem_u32(smem) + warp * S * L::kBytes;
-    const int64_t mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
-    int64_t issued = 0;
+    const int mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+    int issued = 0, is = 0;               // tiles issued, the stage of the next
+    uint32_t known = 0, there = 0;        // bit per lane: tile in the cache; bit per stage: the same
     const uint8_t* src = nullptr;
-    auto issue = [&] {   // the next tile, if any, into stage issued % S
+    auto issue = [&] {
         if (issued >= mine) return;
-        if ((issued & 31) == 0) {
-            const int64_t gt = g0 + warp + kWarps * (issued + lane);
+        const int who = issued & 31;
+        if (who == 0) {
+            const int gt = g0 + warp + kWarps * (issued + lane);
             src = nullptr;
             if (gt < g1) {
-                const int b = request_of(gt);
-                const int64_t in = gt - cum[b] * per_tile, each = cum[b + 1] - cum[b];
-                const int unit = (int)(in / each), tile = (int)(in - unit * each), head = unit / P.row_tiles;
-                const int len = P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len;
-                if (tile * kKvTile < len) {
+                const int bb = pieces ? b : request_of(gt);
+                const int in = gt - cum[bb].x * per, each = cum[bb + 1].x - cum[bb].x;
+                const int u = in / each, tile = in - u * each, head = u / P.row_tiles;
+                if (tile * kKvTile < len_of(bb)) {
                     const int pi = tile / P.cache.tiles_per_page;
-                    const int page = __ldg(P.block_table + b * P.bt_stride + pi);
+                    const int page = __ldg(P.block_table + bb * P.bt_stride + pi);
                     if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
                     else
                         src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + head) * P.cache.tiles_per_page +
                                                (tile - pi * P.cache.tiles_per_page)) * (int64_t)L::kBytes;
                 }
             }
+            known = __ballot_sync(0xffffffffu, src != nullptr);
         }
-        if (lane == (int)(issued & 31)) {
-            const int s = (int)(issued % S);
-            flags[warp * S + s] = src != nullptr;
+        if (lane == who) {
             if (src) {
-                mbar_arrive_expect_tx(bars + 8 * s, L::kBytes);
-                bulk_load(ring + s * L::kBytes, src, L::kBytes, bars + 8 * s);
+                mbar_arrive_expect_tx(bars + 8 * is, L::kBytes);
+                bulk_load(ring + is * L::kBytes, src, L::kBytes, bars + 8 * is);
             } else {
-                mbar_arrive(bars + 8 * s);
+                mbar_arrive(bars + 8 * is);
             }
         }
+        there = (there & ~(1u << is)) | ((known >> who & 1u) << is);
+        is = is + 1 == S ? 0 : is + 1;
         ++issued;
     };
+#pragma unroll 1
     for (int s = 0; s < S; ++s) issue();
 
-    int64_t done = 0;   // tiles of this warp already computed
+    int done = 0, ds = 0;                 // tiles of this warp already computed, the stage of the next
+    uint32_t parity = 0;
     int own_abort = 0;
-    int b = request_of(g0);
-    int64_t first = cum[b] * per_tile, each = cum[b + 1] - cum[b];   // of the request: first tile, tiles per unit
-    int unit = (int)((g0 - first) / each);
+    int first = cum[b].x * per, each = cum[b + 1].x - cum[b].x;   // of the request: first tile, tiles per unit
+#pragma unroll 1
     for (;;) {
-        const int64_t us = first + unit * each, ue = us + each;
+        const int us = first + unit * each, ue = us + each;
         const int head = unit / P.row_tiles, rt = unit - head * P.row_tiles;
         const int rows = min(R, P.rows - rt * R);                    // live rows of this unit
-        const int64_t row0 = (int64_t)b * P.rows + rt * R;
-        const int len = P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len;
+        const int row0 = b * P.rows + rt * R;
+        const int len = len_of(b);
 
         QFrag<BITS, D, NT> Q;
         load_q<BITS, D, NT, T>(P, Q, row0, rows, head, n, t);
         State<D, NT> A;
         int seen[NT][2];   // tokens that rows 2 t, 2 t + 1 see
-        A.ks = 15;
+        A.ks = kUnset;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -553,7 +664,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 A.m[nt][i] = -INFINITY;
-                A.l[nt][i] = 0.f;
+                A.l[nt][i] = A.ref[nt][i] = 0.f;
                 const int r = rt * R + 8 * nt + 2 * t + i;
                 seen[nt][i] = P.prefix == 1 ? len : len - P.tokens + 1 + min(r / P.group, P.tokens - 1);
             }
@@ -562,25 +673,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) A.o[nt][k][i] = 0.f;
         }
-        const int whole = P.prefix == 1 ? len : len - P.tokens + 1;   // tokens that every row sees
+        const int whole = (P.prefix == 1 ? len : len - P.tokens + 1) - kKvTile;   // later tiles: not every row sees all
 
-        const int64_t hi = min(ue, g1);
-        for (; done < mine; ++done) {
-            const int64_t gt = g0 + warp + kWarps * done;
-            if (gt >= hi) break;
-            const int s = (int)(done % S);
-            mbar_wait_bounded(bars + 8 * s, (uint32_t)(done / S) & 1u, &own_abort, P.status);
-            if (flags[warp * S + s]) {
-                const int j0 = (int)(gt - us) * kKvTile;
-                int vis[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) vis[nt][i] = seen[nt][i] - j0;
-                tile_step<BITS, D, NT>(ring + s * L::kBytes, Q, A, len - j0, j0 + kKvTile > whole, vis, lane);
+        const int upto = min(ue, g1) - g0 - warp;   // tiles of this warp: kWarps * done < upto
+        int j0 = (g0 + warp + kWarps * done - us) * kKvTile;
+#pragma unroll 1
+        for (; kWarps * done < upto; ++done, j0 += kWarps * kKvTile) {
+            mbar_wait_bounded(bars + 8 * ds, parity, &own_abort, P.status);
+            if (there >> ds & 1u) {
+                const uint8_t* tile = smem + (warp * S + ds) * L::kBytes;
+                if (j0 > whole) tile_step<BITS, D, NT, true>(tile, Q, A, j0, len, seen, lane);
+                else tile_step<BITS, D, NT, false>(tile, Q, A, j0, len, seen, lane);
             }
             __syncwarp();   // all lanes have read the stage: it may be filled again
             issue();
+            if (++ds == S) ds = 0, parity ^= 1u;
         }
 
         // ---- the warps' sums of this unit joined, in warp order ----
@@ -606,7 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
                 fac[nt][i] = ex2(A.m[nt][i] - ref);
                 if (warp == 0 && n == 0) total_ml[r] = make_float2(top, l);
             }
-        const float up = pow2i(24 - A.ks);
+        const float up = pow2i(24 - (A.ks == kUnset ? 0 : A.ks));
         auto put = [&](bool add) {   // this warp's rows into (or onto) slot warp % 4
             float* dst = red + (warp & 3) * R * M::kPitch;
 #pragma unroll
@@ -630,55 +737,45 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         if (warp < 4) put(true);
         __syncthreads();
 
-        const bool ends_here = ue <= g1, all_here = us >= g0 && ends_here;
+        const bool all_here = us >= g0 && ue <= g1;
         float* slot = P.part + (2 * c + (us >= g0 ? 1 : 0)) * (int64_t)(R * (D + 2));
-        for (int i = tid; i < R * D; i += 32 * kWarps) {
-            const int r = i / D, d = i % D;
-            if (r >= rows) break;
-            const float* a = red + r * M::kPitch + d;
-            const float v = (a[0] + a[R * M::kPitch]) + (a[2 * R * M::kPitch] + a[3 * R * M::kPitch]);
-            if (all_here) finish<D, T>(P, row0 + r, head, d, v, total_ml[r].x, total_ml[r].y);
-            else slot[r * D + d] = v;
+        constexpr int V = D / 32;   // a warp per row
+        for (int r = warp; r < rows; r += kWarps) {
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float* a = red + r * M::kPitch + V * lane + i;
+                v[i] = (a[0] + a[R * M::kPitch]) + (a[2 * R * M::kPitch] + a[3 * R * M::kPitch]);
+            }
+            if (all_here) {
+                RowOut<D, T>(P, row0 + r, head, total_ml[r].x, total_ml[r].y, lane == 0).store(P, V * lane, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) slot[r * D + V * lane + i] = v[i];
+            }
         }
         if (!all_here) {
             if (tid < rows) *reinterpret_cast<float2*>(slot + R * D + 2 * tid) = total_ml[tid];
-            const int64_t c0 = ((us + 1) * C - 1) / total, c1 = (ue * C - 1) / total;   // the blocks that share the unit
-            unsigned* count = P.counters + (int64_t)b * per_tile + unit;
+            // the blocks that share the unit
+            const int from = costly(b) * per + unit * (each + kUnitCost) + kUnitCost;
+            const int c0 = pieces ? c - piece : block_of(from), c1 = pieces ? c0 + of - 1 : block_of(from + each - 1);
+            unsigned* count = P.counters + (int64_t)b * per + unit;
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                auto from = [&](int64_t k) { return P.part + (2 * k + (k == c0 ? 1 : 0)) * (int64_t)(R * (D + 2)); };
-                for (int r = warp; r < rows; r += kWarps) {
-                    float top = -INFINITY, l = 0.f;
-                    for (int64_t k = c0 + lane; k <= c1; k += 32) top = fmaxf(top, __ldcg(from(k) + R * D + 2 * r));
-                    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    for (int64_t k = c0 + lane; k <= c1; k += 32)
-                        l += __ldcg(from(k) + R * D + 2 * r + 1) * ex2(__ldcg(from(k) + R * D + 2 * r) - ref);
-                    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-                    if (lane == 0) total_ml[r] = make_float2(top, l);
-                }
-                __syncthreads();
-                for (int i = tid; i < rows * D; i += 32 * kWarps) {
-                    const int r = i / D, d = i % D;
-                    const float top = total_ml[r].x, ref = top == -INFINITY ? 0.f : top;
-                    float v = 0.f;
-#pragma unroll 8
-                    for (int64_t k = c0; k <= c1; ++k) v = fmaf(__ldcg(from(k) + r * D + d), ex2(__ldcg(from(k) + R * D + 2 * r) - ref), v);
-                    finish<D, T>(P, row0 + r, head, d, v, top, total_ml[r].y);
-                }
+                join<D, R, T>(P, c0, c1, warp, lane, rows, row0, head);
                 if (tid == 0) *count = 0;
             }
         }
         if (ue >= g1) break;
-        if (++unit == per_tile) {
+        if (++unit == per) {
             unit = 0;
             ++b;
-            first = cum[b] * per_tile;
-            each = cum[b + 1] - cum[b];
+            first = cum[b].x * per;
+            each = cum[b + 1].x - cum[b].x;
         }
         __syncthreads();   // the sums' buffers are free again
     }
@@ -719,9 +816,20 @@ lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream
     if (blocks < 1) return LQ_ERR_CUDA;
     if ((size_t)P.requests * P.cache.kv_heads * P.row_tiles > h->num_counters) return LQ_ERR_WORKSPACE;
     if ((size_t)blocks * 2 * R * (D + 2) * sizeof(float) > room) return LQ_ERR_WORKSPACE;
+    // (tile indices are 32-bit)
+    if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     P.part = reinterpret_cast<float*>(scratch);
-    attn_kernel<BITS, D, NT, T><<<blocks, 32 * kWarps, smem, stream>>>(P);
-    return cudaPeekAtLastError() == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(32 * kWarps, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_kernel<BITS, D, NT, T>, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
 }
 
 template <int BITS, int D>
@@ -743,6 +851,7 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
     P.scale_log2 = a.scale * 1.4426950408889634f;
     P.counters = h->counters;
     P.status = h->status_flag;
+    if ((int64_t)a.batch * a.tokens * P.group > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     P.all_rows = a.batch * a.tokens * P.group;
     // workspace: the prefix's rows and log-sum-exps, then partial sums
     char* ws = reinterpret_cast<char*>(h->partials);
