@@ -28,18 +28,15 @@
 // (one fixed order: results repeat bit for bit).  Lengths are read on the device: no host
 // synchronisation, and a captured graph serves any lengths.
 //
-// A shared prefix is the same kernel with every request's rows as one unit list over the prefix
-// pages, run first; its normalised rows and log-sum-exps join at the end of the second run.
-
-#include <math.h>
+// A shared prefix runs first, with every request's rows as one unit list over the prefix pages; its
+// normalised rows and log-sum-exps join at the end of the second run.  Few rows or a short prefix
+// take this kernel for it, many rows the tensor-memory kernel (lq_attn_prefix.cu).
 
 #include <algorithm>
 #include <mutex>
 #include <vector>
 
-#include "lq_internal.h"
-#include "lq_kv.cuh"
-#include "lq_tma.cuh"
+#include "lq_attn.cuh"
 
 namespace lq {
 namespace {
@@ -47,83 +44,10 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kUnitCost = 28;    // what a unit costs a block besides its tiles, in tiles
 constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
-constexpr float kTau = 3.f;      // a row's reference moves when a score passes it by 2^3
-constexpr float kPBits = 11.f;   // P = 2^11 p
 // S 2^ks stays at or below kMostS (2^14 times that is finite); ks = 0 where the first tile's largest S lies
 // between the two, so that the multiplication is skipped; otherwise it brings the largest into [1, 2)
 constexpr float kMostS = 3.9f, kLeastS = 0x1p-8f;
 constexpr int kUnset = 99;
-
-struct AttnParams {
-    KvView cache;
-    const void* q;
-    void* out;
-    float* lse;
-    int64_t q_stride, out_stride, bt_stride;
-    const int32_t *block_table, *lens;   // (prefix run: the prefix pages, lens null)
-    int requests, rows;                  // units' outer count and rows of each per kv head
-    int tokens, group, q_heads;
-    int max_len, row_tiles;
-    float scale_log2;                    // scale * log2(e)
-    float* part;                         // partial sums: 2 slots per block
-    unsigned* counters;                  // one per unit, zero between calls
-    float *pre_o, *pre_lse;              // the prefix's rows [kv_heads][rows of all requests][D] and log2-sum-exps
-    int all_rows;                        // rows of all requests per kv head
-    int prefix;                          // 0: none, 1: this is the prefix run, 2: join the prefix's rows
-    int* status;
-};
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
-// m16n8k16 with binary16 operands and fp32 sums: D += A B, and D = A B.  (Not volatile: free to
-// be scheduled among the mask instructions around them.)
-__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
-__device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
-__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
-    uint32_t d;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ float2 unpack2(uint32_t h) {
-    return make_float2(half_bits_to_float((uint16_t)h), half_bits_to_float((uint16_t)(h >> 16)));
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-
-template <class T>
-__device__ __forceinline__ float elem_to_float(uint16_t bits);
-template <>
-__device__ __forceinline__ float elem_to_float<__half>(uint16_t bits) { return half_bits_to_float(bits); }
-template <>
-__device__ __forceinline__ float elem_to_float<__nv_bfloat16>(uint16_t bits) { return bf16_bits_to_float(bits); }
 
 template <int BITS, int D, int NT>
 struct AttnSmem {
@@ -415,102 +339,6 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
     }
 }
 
-// Where a row's result goes, and its factors: out = v * own (+ the prefix's row * pre).
-template <int D, class T>
-struct RowOut {
-    T* out;
-    float *pre, own, shared;
-    // row: of all requests' rows of a kv head; (m, l): reference and sum of P.  One lane (`writes`)
-    // stores the log-sum-exp.
-    __device__ __forceinline__ RowOut(const AttnParams& P, int row, int head, float m, float l, bool writes) {
-        float s = l == 0.f ? -INFINITY : m + log2f(l) - kPBits;
-        own = l == 0.f ? 0.f : 1.f / l;
-        shared = 0.f;
-        const int64_t at = (int64_t)head * P.all_rows + row;
-        pre = P.pre_o + at * D;
-        if (P.prefix == 1) {
-            if (writes) P.pre_lse[at] = s;
-            return;
-        }
-        if (P.prefix == 2) {
-            const float s2 = __ldcg(P.pre_lse + at), top = fmaxf(s, s2);
-            if (top != -INFINITY) {
-                const float a = ex2(s - top), c = ex2(s2 - top), f = 1.f / (a + c);
-                own *= a * f;
-                shared = c * f;
-                s = top + log2f(a + c);
-            }
-        }
-        const int bt = row / P.group, qh = head * P.group + (row - bt * P.group);
-        out = static_cast<T*>(P.out) + bt * P.out_stride + (int64_t)qh * D;
-        if (writes && P.lse) P.lse[(int64_t)bt * P.q_heads + qh] = s * 0.6931471805599453f;
-    }
-    // V dimensions from d on
-    template <int V>
-    __device__ __forceinline__ void store(const AttnParams& P, int d, float (&v)[V]) const {
-        if (P.prefix == 1) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) pre[d + i] = v[i] * own;
-            return;
-        }
-        alignas(4 * V) T o[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] *= own;
-            if (P.prefix == 2) v[i] = fmaf(__ldcg(pre + d + i), shared, v[i]);
-            o[i] = (T)v[i];
-        }
-        if (V == 4) *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(o);
-        else *reinterpret_cast<uint32_t*>(out + d) = *reinterpret_cast<const uint32_t*>(o);
-    }
-};
-
-// A unit's partial sums of blocks c0 .. c1, joined in block order: a warp per row, D / 32
-// dimensions per lane, the blocks' factors 32 at a time (one per lane).
-template <int D, int R, class T>
-__device__ __forceinline__ void join(const AttnParams& P, int c0, int c1, int warp, int lane, int rows, int row0, int head) {
-    constexpr int V = D / 32;
-    constexpr int kSlot = R * (D + 2);   // (slots of all blocks together: within 32 bits)
-    auto from = [&](int k) { return P.part + (unsigned)(2 * k + (k == c0 ? 1 : 0)) * kSlot; };
-    for (int r = warp; r < rows; r += kWarps) {
-        float top = -INFINITY, l = 0.f, v[V] = {};
-        for (int k = c0 + lane; k <= c1; k += 32) top = fmaxf(top, __ldcg(from(k) + R * D + 2 * r));
-        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        const float ref = top == -INFINITY ? 0.f : top;
-        for (int k0 = c0; k0 <= c1; k0 += 32) {
-            const int m = min(32, c1 + 1 - k0);
-            float f = 0.f;
-            if (lane < m) {
-                const float2 e = __ldcg(reinterpret_cast<const float2*>(from(k0 + lane) + R * D + 2 * r));
-                f = ex2(e.x - ref);
-                l = fmaf(e.y, f, l);
-            }
-            // sixteen blocks' values in flight at a time
-            for (int j0 = 0; j0 < m; j0 += 16) {
-                float o[16][V];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float* a = from(k0 + min(j0 + j, m - 1)) + r * D + V * lane;
-#pragma unroll
-                    for (int i = 0; i < V; i += 2) {
-                        const float2 e = __ldcg(reinterpret_cast<const float2*>(a + i));
-                        o[j][i] = e.x, o[j][i + 1] = e.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (j0 + j < m) v[i] = fmaf(o[j][i], fj, v[i]);
-                }
-            }
-        }
-        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-        RowOut<D, T>(P, row0 + r, head, top, l, lane == 0).store(P, V * lane, v);
-    }
-}
-
 template <int BITS, int D, int NT, class T>
 __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_constant__ AttnParams P) {
     using L = KvLayout<BITS, D>;
@@ -766,7 +594,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join<D, R, T>(P, c0, c1, warp, lane, rows, row0, head);
+                join<D, R, kWarps, T>(P, c0, c1, warp, lane, rows, row0, head);
                 if (tid == 0) *count = 0;
             }
         }
@@ -870,7 +698,9 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
         P.prefix = 1;
         P.block_table = a.prefix_table, P.bt_stride = 0, P.lens = nullptr;
         P.requests = 1, P.rows = P.all_rows, P.max_len = a.prefix_len;
-        const lq_status s = go(P);
+        const lq_status s = prefix_tc_takes(P.all_rows, a.prefix_len)
+                                ? launch_prefix_tc(h, P, c.bits, c.head_dim, bf16, ws + pre, cap - pre, stream)
+                                : go(P);
         if (s != LQ_OK) return s;
     }
     P.prefix = a.prefix_len > 0 ? 2 : 0;

@@ -1,9 +1,12 @@
 // Rotary positions and the low-bit KV cache: the rotation table, the rotation of a row (and its
 // transpose), rows quantised into cache tiles as they are written, and tiles read back.
 //
-// All of it is bound by memory: a few operations per value, one pass over the data.  Rows are
-// taken by D / 8 lanes, 8 values (16 bytes of a 16-bit type) each; what a rotation or a group's
-// range needs of other lanes comes by shuffles, so each value is read once and written once.
+// All of it is bound by memory: a few operations per value, one pass over the data.  A row (one
+// head of one token) is taken by D / 8 lanes, 8 values (16 bytes of a 16-bit type) each; what a
+// rotation or a group's range needs of other lanes comes by shuffles, so each value is read once
+// and written once.  A group of lanes stays with its token, whose cosines and sines it holds in
+// registers, and walks a chunk of its rows, four loads at a time; neighbouring groups have
+// neighbouring tokens, which lie in the same cache tiles.
 
 #include <math.h>
 #include <string.h>
@@ -12,6 +15,7 @@
 
 #include "lq_internal.h"
 #include "lq_kv.cuh"
+#include "lq_tma.cuh"
 
 namespace lq {
 namespace {
@@ -130,11 +134,11 @@ __device__ __forceinline__ Vec8<T> turned(const Vec8<T>& x, const Turn& u) {
 
 // Row of the table for a token's position; null (and the status word's bit 2) when it has none.
 __device__ __forceinline__ const float* table_row(const float* table, const int* positions, int64_t n, int rows, int rot,
-                                                  int* status) {
+                                                  int* status, bool report) {
     if (!table) return nullptr;
-    const int p = positions[n];
+    const int p = __ldg(positions + n);
     if (p < 0 || p >= rows) {
-        if (threadIdx.x == 0) atomicOr(status, kStatusIndex);
+        if (report) atomicOr(status, kStatusIndex);
         return nullptr;
     }
     return table + (int64_t)p * rot;
@@ -146,28 +150,38 @@ struct RopeParams {
     int64_t xt, xh, yt, yh;   // token and head strides in elements
     const float* table;
     const int* positions;
-    int heads, D, rot, rows, layout, inverse;
+    int n, heads, D, rot, rows, layout, inverse;
     int lanes;                // lanes of a row: the power of two >= D / 8
+    int chunk;                // rows of a token that one group of lanes takes
     int* status;
 };
 
-// One block: one token, a chunk of its heads; each lane keeps its cos and sin for all of them.
-template <class T>
+// blockIdx.x: 256 / lanes neighbouring tokens; blockIdx.y: a chunk of their heads.
+template <class T, int U>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams P) {
-    const int64_t n = blockIdx.x;
-    const int j = threadIdx.x & (P.lanes - 1), r0 = threadIdx.x / P.lanes, step = 256 / P.lanes;
-    const float* row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status);
-    const Turn u = turn_for(row, j, threadIdx.x & 31, P.rot, P.layout, P.inverse != 0);
-    const bool live = 8 * j < P.D;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int j = threadIdx.x & (P.lanes - 1);
+    const int64_t n = (int64_t)blockIdx.x * (256 / P.lanes) + threadIdx.x / P.lanes;
+    const bool live = 8 * j < P.D && n < P.n;
     const T* x = static_cast<const T*>(P.x) + n * P.xt + 8 * j;
     T* y = static_cast<T*>(P.y) + n * P.yt + 8 * j;
-    const int per = (P.heads + gridDim.y - 1) / gridDim.y, h1 = min(P.heads, (int)(blockIdx.y + 1) * per);
-    for (int hb = blockIdx.y * per; hb < h1; hb += step) {   // (uniform over the block: the shuffles need all lanes)
-        const int h = hb + r0;
-        Vec8<T> v = {};
-        if (live && h < h1) v = load8(x + h * P.xh);
-        v = turned(v, u);
-        if (live && h < h1) store8(y + h * P.yh, v);
+    const int h0 = blockIdx.y * P.chunk, h1 = min(P.heads, h0 + P.chunk);
+    Turn u;
+    for (int hb = h0; hb < h1; hb += U) {   // (uniform over the block: the shuffles need all lanes)
+        Vec8<T> v[U] = {};
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (live && hb + k < h1) v[k] = load8(x + (hb + k) * P.xh);
+        if (hb == h0) {                     // after the first rows' loads are on their way
+            const float* row = n < P.n ? table_row(P.table, P.positions, n, P.rows, P.rot, P.status, j == 0) : nullptr;
+            u = turn_for(row, j, threadIdx.x & 31, P.rot, P.layout, P.inverse != 0);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const Vec8<T> r = turned(v[k], u);
+            if (live && hb + k < h1) store8(y + (hb + k) * P.yh, r);
+        }
     }
 }
 
@@ -175,8 +189,10 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
 // unrotated dimension.
 template <class T>
 __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ RopeParams P) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t n = blockIdx.x;
-    const float* row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status);
+    const float* row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status, threadIdx.x == 0);
     const int half = P.rot / 2, each = half + P.D - P.rot;   // pairs, then single dimensions
     for (int i = blockIdx.y * 256 + threadIdx.x; i < P.heads * each; i += gridDim.y * 256) {
         const int h = i / each, k = i - h * each;
@@ -204,22 +220,65 @@ constexpr int kMaxRot = 256;
 struct TableParams {
     uint64_t step[kMaxRot / 2];   // turns per position as 64-bit fractions
     float* out;
-    int half, first, count;
+    int half, first, count, steps;
     float mscale;
 };
 
 // cos and sin of 2 pi frac(p u): the product wraps modulo 2^64, that is modulo one turn, exactly,
 // whatever the position; its top 32 bits give the angle to 1.5e-9 radians.
+__device__ __forceinline__ float2 turns(uint64_t a) {
+    float s, c;
+    sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // (2^-31 half turns)
+    return make_float2(c, s);
+}
+
+constexpr int kFine = 32, kCoarse = 16;   // positions of a step, steps of a block at most
+
+// A position is a multiple of kFine (from the block's first) plus the rest: its angle's cosine and
+// sine are the product of two unit numbers, each evaluated as above once per block.  That leaves
+// one evaluation per 11 outputs and two products and two sums each, which the stores hide; direct
+// evaluation was bound by its arithmetic (131072 x 128: 18.7 us, and FIGURE this way).
+template <int V>
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableParams P) {
-    const int i = threadIdx.x % P.half, per = 256 / P.half;
-    if ((int)threadIdx.x >= per * P.half) return;
-    const uint64_t u = P.step[i];
-    for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / P.half; r < P.count; r += (int64_t)gridDim.x * per) {
-        const uint64_t a = (uint64_t)(P.first + r) * u;
-        float s, c;
-        sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // (2^-31 half turns)
-        P.out[r * 2 * P.half + i] = c * P.mscale;
-        P.out[r * 2 * P.half + P.half + i] = s * P.mscale;
+    __shared__ float2 fine[kFine][kMaxRot / 2], coarse[kCoarse][kMaxRot / 2];   // [coarse: times mscale]
+    pdl_launch_dependents();
+    const int half = P.half, quads = half / V;
+    const int64_t r0 = (int64_t)blockIdx.x * (kFine * P.steps);
+    {   // a thread keeps to one frequency (the parameters are read once)
+        const int i = threadIdx.x % half, share = 256 / half;
+        const uint64_t u = P.step[i];
+        for (int f = threadIdx.x / half; f < kFine + P.steps; f += share) {
+            if (threadIdx.x / half >= share) break;
+            if (f < kFine) {
+                fine[f][i] = turns((uint64_t)f * u);
+            } else {
+                const float2 z = turns((uint64_t)(P.first + r0 + (f - kFine) * kFine) * u);
+                coarse[f - kFine][i] = make_float2(z.x * P.mscale, z.y * P.mscale);
+            }
+        }
+    }
+    __syncthreads();
+    pdl_wait();   // (the rows may still be read by the kernel before)
+    const int per = 256 / quads, i0 = (threadIdx.x % quads) * V;
+    if ((int)threadIdx.x >= per * quads) return;
+    for (int f = threadIdx.x / quads; f < kFine * P.steps; f += per) {
+        const int64_t r = r0 + f;
+        if (r >= P.count) break;
+        alignas(16) float c[V], s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 w = fine[f % kFine][i0 + v], z = coarse[f / kFine][i0 + v];
+            c[v] = fmaf(z.x, w.x, -z.y * w.y);
+            s[v] = fmaf(z.x, w.y, z.y * w.x);
+        }
+        float* o = P.out + r * 2 * half + i0;
+        if (V == 4) {
+            *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(c);
+            *reinterpret_cast<float4*>(o + half) = *reinterpret_cast<const float4*>(s);
+        } else {
+            o[0] = c[0];
+            o[half] = s[0];
+        }
     }
 }
 
@@ -244,97 +303,138 @@ struct AppendParams {
     const int64_t* slots;
     const float* table;
     const int* positions;
-    int q_heads, rot, rows, layout;
+    int n, q_heads, rot, rows, layout;
+    int chunk;                    // rows of a token that one group of lanes takes
     int* status;
 };
 
-__device__ __forceinline__ uint8_t* tile_of(const KvView& c, int64_t slot, int head, int tile_bytes) {
-    const int64_t page = slot / c.page_size;
-    const int off = (int)(slot - page * c.page_size);
-    return c.pages + ((page * c.kv_heads + head) * c.tiles_per_page + (off >> 4)) * (int64_t)tile_bytes;
+// A slot's tile of head 0 and its token there; null when the cache has no such slot (reported
+// when it lies past the end).
+struct Place {
+    uint8_t* tile;
+    int64_t head_bytes;
+    int tok;
+};
+__device__ __forceinline__ Place place_of(const KvView& c, const int64_t* slots, int64_t n, int tile_bytes, int* status, bool report) {
+    const int64_t slot = __ldg(slots + n);
+    Place p{nullptr, (int64_t)c.tiles_per_page * tile_bytes, (int)(slot & 15)};
+    const int64_t tile = slot >> 4;   // (pages are whole tiles)
+    if (slot < 0 || tile >= c.num_pages * c.tiles_per_page) {
+        if (slot >= 0 && report) atomicOr(status, kStatusIndex);
+        return p;
+    }
+    const int64_t page = (tile >> 32) ? tile / c.tiles_per_page : (int64_t)((uint32_t)tile / (uint32_t)c.tiles_per_page);
+    p.tile = c.pages + page * c.kv_heads * p.head_bytes + (tile - page * c.tiles_per_page) * tile_bytes;
+    return p;
 }
 
-// One block: one token, a chunk of its rows (q heads, then k, then v).  A key or value row's
-// group of 32 is four lanes: its range by two shuffles, its codes by the definition's fp32
-// operations (correctly rounded each, so the stored bits are one and the same everywhere).
-template <int BITS, int D, class T>
+// A key or value row's group of 32 is four lanes: its range by two shuffles, its codes by the
+// definition's fp32 operations (correctly rounded each, so the stored bits are one and the same
+// everywhere).  blockIdx.x: neighbouring tokens; blockIdx.y: a chunk of their rows (q heads, then
+// k, then v), the same for the whole block.
+template <int BITS, int D, class T, int U>
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams P) {
     using L = KvLayout<BITS, D>;
-    constexpr int kLanes = D / 8, kStep = 256 / kLanes;
+    constexpr int kLanes = D / 8;
     constexpr float kTop = (float)((1 << BITS) - 1);
-    const int64_t n = blockIdx.x;
-    const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes, g = j >> 2;
+    const int64_t n = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const bool live = n < P.n;
     const int hq = P.q_heads, hkv = P.cache.kv_heads, all = hq + 2 * hkv;
-    const int64_t slot = P.slots[n], cap = P.cache.num_pages * P.cache.page_size;
-    if (slot >= cap && threadIdx.x == 0) atomicOr(P.status, kStatusIndex);
-    const bool kept = slot >= 0 && slot < cap;
-    const float* row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status);
-    const Turn u = turn_for(row, j, lane, P.rot, P.layout, false);
-    const int per = (all + gridDim.y - 1) / gridDim.y, h1 = min(all, (int)(blockIdx.y + 1) * per);
-    const int tok = kept ? (int)(slot % P.cache.page_size) & 15 : 0;
-    for (int hb = blockIdx.y * per; hb < h1; hb += kStep) {
-        const int h = hb + r0;
-        const bool live = h < h1, is_q = h < hq, is_v = h >= hq + hkv;
-        Vec8<T> x = {};
-        if (live) {
-            const T* src = is_q   ? static_cast<const T*>(P.q) + n * P.qt + h * D
-                           : is_v ? static_cast<const T*>(P.v) + n * P.vt + (h - hq - hkv) * D
-                                  : static_cast<const T*>(P.k) + n * P.kt + (h - hq) * D;
-            x = load8(src + 8 * j);
-        }
-        Vec8<T> y = turned(x, u);
-        if (is_v) y = x;
-        if (live && is_q) store8(static_cast<T*>(P.q_out) + n * P.ot + h * D + 8 * j, y);
-        if (!__any_sync(0xffffffffu, live && !is_q)) continue;
-
-        float f[8], lo, hi;
+    const int h0 = blockIdx.y * P.chunk, h1 = min(all, h0 + P.chunk);
+    Place at{nullptr, 0, 0};
+    Turn u;
+    for (int hb = h0; hb < h1; hb += U) {
+        Vec8<T> x[U] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] = max_nan(min_nan(to_f(y.v[i]), 65504.f), -65504.f);
-            lo = i ? min_nan(lo, f[i]) : f[0];
-            hi = i ? max_nan(hi, f[i]) : f[0];
-        }
-#pragma unroll
-        for (int s = 1; s <= 2; s <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-        }
-        const __half S = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / kTop)), Z = __float2half_rn(lo);
-        const float s = __half2float(S), z = __half2float(Z);
-        uint32_t w[2] = {0u, 0u};   // the row's 8 codes, dimension order
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t c = 0;
-            if (s > 0.f) c = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(f[i], z), s)), 0.f), kTop);
-            if (BITS == 4) w[0] |= c << (4 * i);
-            else w[i >> 2] |= c << (8 * (i & 3));
-        }
-        // values: codes of one dimension of eight (four) lanes' rows side by side
-        uint32_t v0, v1 = 0;
-        if (BITS == 4) {
-            v0 = kv_transpose_nibbles(w[0], j / L::WV, L::WV);
-        } else {
-            v0 = kv_transpose_bytes(w[0], j / L::WV, L::WV);
-            v1 = kv_transpose_bytes(w[1], j / L::WV, L::WV);
-        }
-        if (!live || is_q || !kept) continue;
-        const int head = is_v ? h - hq - hkv : h - hq, g = j >> 2;
-        uint8_t* t = tile_of(P.cache, slot, head, L::kBytes);
-        if (!is_v) {
-            const int ln = 4 * (tok & 7) + (j & 3), q = (tok >> 3) * L::WK + g * (L::WK / L::G);
-            if (BITS == 4) *reinterpret_cast<uint32_t*>(t + kv_word_at(ln, q)) = w[0];
-            else *reinterpret_cast<uint2*>(t + kv_word_at(ln, q)) = make_uint2(w[0], w[1]);
-            if ((j & 3) == 0) {
-                reinterpret_cast<__half*>(t + L::kKs)[tok * L::G + g] = S;
-                reinterpret_cast<__half*>(t + L::kKz)[tok * L::G + g] = Z;
+        for (int k = 0; k < U; ++k) {
+            const int h = hb + k;
+            if (live && h < h1) {
+                const T* src = h < hq         ? static_cast<const T*>(P.q) + n * P.qt + h * D
+                               : h < hq + hkv ? static_cast<const T*>(P.k) + n * P.kt + (h - hq) * D
+                                              : static_cast<const T*>(P.v) + n * P.vt + (h - hq - hkv) * D;
+                x[k] = load8(src + 8 * j);
             }
-        } else {
-            const int e = j / L::WV, wi = j % L::WV, jt = (tok & 1) + 2 * (tok >> 3), t4 = (tok & 7) >> 1;
-            *reinterpret_cast<uint32_t*>(t + L::kVc + kv_word_at(4 * e + t4, jt * L::WV + wi)) = v0;
-            if (BITS == 8) *reinterpret_cast<uint32_t*>(t + L::kVc + kv_word_at(4 * (e + 4) + t4, jt * L::WV + wi)) = v1;
-            if ((j & 3) == 0) {
-                reinterpret_cast<__half*>(t + L::kVs)[g * kKvTile + kv_vmeta_pos(tok)] = S;
-                reinterpret_cast<__half*>(t + L::kVz)[g * kKvTile + kv_vmeta_pos(tok)] = Z;
+        }
+        if (hb == h0) {   // after the first rows' loads are on their way
+            const float* row = nullptr;
+            if (live) {
+                if (h1 > hq) at = place_of(P.cache, P.slots, n, L::kBytes, P.status, j == 0);
+                if (h0 < hq + hkv) row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status, j == 0);
+            }
+            u = turn_for(row, j, lane, P.rot, P.layout, false);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = hb + k;
+            if (h >= h1) break;
+            const bool is_v = h >= hq + hkv;
+            Vec8<T> y = is_v ? x[k] : turned(x[k], u);
+            if (h < hq) {
+                if (live) store8(static_cast<T*>(P.q_out) + n * P.ot + h * D + 8 * j, y);
+                continue;
+            }
+            float f[8], lo, hi;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] = max_nan(min_nan(to_f(y.v[i]), 65504.f), -65504.f);
+                lo = i ? min_nan(lo, f[i]) : f[0];
+                hi = i ? max_nan(hi, f[i]) : f[0];
+            }
+#pragma unroll
+            for (int s = 1; s <= 2; s <<= 1) {
+                lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+                hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+            }
+            const __half S = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / kTop)), Z = __float2half_rn(lo);
+            const float s = __half2float(S), z = __half2float(Z);
+            // rint of the rounded quotient, without a division per value: a product with 1 / s is off
+            // by at most 255 * 2^-22.4 = 4.6e-5, so it has the same nearest whole number unless it lies
+            // within 1e-4 of a half
+            const float inv = __fdiv_rn(1.f, s);
+            uint32_t w[2] = {0u, 0u};   // the row's 8 codes, dimension order
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = __fsub_rn(f[i], z);
+                float r = d * inv, c = rintf(r);
+                if (fabsf(r - c) > 0.4999f) c = rintf(__fdiv_rn(d, s));
+                const uint32_t code = s > 0.f ? (uint32_t)fminf(fmaxf(c, 0.f), kTop) : 0u;
+                if (BITS == 4) w[0] |= code << (4 * i);
+                else w[i >> 2] |= code << (8 * (i & 3));
+            }
+            uint8_t* t = at.tile + (h - hq - (is_v ? hkv : 0)) * at.head_bytes;
+            const bool kept = live && at.tile != nullptr;
+            const int tok = at.tok;
+            if (!is_v) {
+                const int ln = 4 * (tok & 7) + (j & 3), q = (tok >> 3) * L::WK + g * (L::WK / L::G);
+                if (kept) {
+                    if (BITS == 4) *reinterpret_cast<uint32_t*>(t + kv_word_at(ln, q)) = w[0];
+                    else *reinterpret_cast<uint2*>(t + kv_word_at(ln, q)) = make_uint2(w[0], w[1]);
+                    if ((j & 3) == 0) {
+                        reinterpret_cast<__half*>(t + L::kKs)[tok * L::G + g] = S;
+                        reinterpret_cast<__half*>(t + L::kKz)[tok * L::G + g] = Z;
+                    }
+                }
+            } else {
+                // codes of one dimension of eight (four) lanes' rows side by side
+                uint32_t v0, v1 = 0;
+                const int e = j / L::WV, wi = j % L::WV, jt = (tok & 1) + 2 * (tok >> 3), t4 = (tok & 7) >> 1;
+                if (BITS == 4) {
+                    v0 = kv_transpose_nibbles(w[0], e, L::WV);
+                } else {
+                    v0 = kv_transpose_bytes(w[0], e, L::WV);
+                    v1 = kv_transpose_bytes(w[1], e, L::WV);
+                }
+                if (kept) {
+                    *reinterpret_cast<uint32_t*>(t + L::kVc + kv_word_at(4 * e + t4, jt * L::WV + wi)) = v0;
+                    if (BITS == 8) *reinterpret_cast<uint32_t*>(t + L::kVc + kv_word_at(4 * (e + 4) + t4, jt * L::WV + wi)) = v1;
+                    if ((j & 3) == 0) {
+                        reinterpret_cast<__half*>(t + L::kVs)[g * kKvTile + kv_vmeta_pos(tok)] = S;
+                        reinterpret_cast<__half*>(t + L::kVz)[g * kKvTile + kv_vmeta_pos(tok)] = Z;
+                    }
+                }
             }
         }
     }
@@ -344,71 +444,92 @@ struct ReadParams {
     KvView cache;
     const int64_t* slots;
     void *k, *v;   // [n][kv_heads][D], either may be null
+    int n, chunk;
     int* status;
 };
 
-template <int BITS, int D, class T>
+// blockIdx.x: neighbouring slots; blockIdx.y: a chunk of their rows (k heads, then v).
+template <int BITS, int D, class T, int U>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ ReadParams P) {
     using L = KvLayout<BITS, D>;
-    constexpr int kLanes = D / 8, kStep = 256 / kLanes;
-    const int64_t n = blockIdx.x;
-    const int j = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes, g = j >> 2;
+    constexpr int kLanes = D / 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int j = threadIdx.x % kLanes, g = j >> 2;
+    const int64_t n = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const bool live = n < P.n;
     const int hkv = P.cache.kv_heads, first = P.k ? 0 : hkv, all = P.v ? 2 * hkv : hkv;
-    const int64_t slot = P.slots[n], cap = P.cache.num_pages * P.cache.page_size;
-    if (slot >= cap && threadIdx.x == 0) atomicOr(P.status, kStatusIndex);
-    const bool kept = slot >= 0 && slot < cap;
-    const int tok = kept ? (int)(slot % P.cache.page_size) & 15 : 0;
-    const int per = (all - first + gridDim.y - 1) / gridDim.y, h0 = first + blockIdx.y * per, h1 = min(all, h0 + per);
-    for (int hb = h0; hb < h1; hb += kStep) {
-        const int h = hb + r0;
-        const bool live = h < h1, is_v = h >= hkv;
-        const int head = is_v ? h - hkv : h;
-        uint32_t w[2] = {0u, 0u};
-        float s = 0.f, z = 0.f;
-        if (live && kept) {
-            const uint8_t* t = tile_of(P.cache, slot, head, L::kBytes);
-            if (!is_v) {
-                const int ln = 4 * (tok & 7) + (j & 3), q = (tok >> 3) * L::WK + g * (L::WK / L::G);
-                w[0] = *reinterpret_cast<const uint32_t*>(t + kv_word_at(ln, q));
-                if (BITS == 8) w[1] = *reinterpret_cast<const uint32_t*>(t + kv_word_at(ln, q + 1));
-                s = __half2float(reinterpret_cast<const __half*>(t + L::kKs)[tok * L::G + g]);
-                z = __half2float(reinterpret_cast<const __half*>(t + L::kKz)[tok * L::G + g]);
-            } else {
-                const int e = j / L::WV, wi = j % L::WV, jt = (tok & 1) + 2 * (tok >> 3), t4 = (tok & 7) >> 1;
-                w[0] = *reinterpret_cast<const uint32_t*>(t + L::kVc + kv_word_at(4 * e + t4, jt * L::WV + wi));
-                if (BITS == 8)
-                    w[1] = *reinterpret_cast<const uint32_t*>(t + L::kVc + kv_word_at(4 * (e + 4) + t4, jt * L::WV + wi));
-                s = __half2float(reinterpret_cast<const __half*>(t + L::kVs)[g * kKvTile + kv_vmeta_pos(tok)]);
-                z = __half2float(reinterpret_cast<const __half*>(t + L::kVz)[g * kKvTile + kv_vmeta_pos(tok)]);
+    const int h0 = first + blockIdx.y * P.chunk, h1 = min(all, h0 + P.chunk);
+    Place at{nullptr, 0, 0};
+    if (live) at = place_of(P.cache, P.slots, n, L::kBytes, P.status, j == 0);
+    const int tok = at.tok, e = j / L::WV;
+    // byte of this lane's word(s) and of its group's S, for keys and for values
+    const int kw = kv_word_at(4 * (tok & 7) + (j & 3), (tok >> 3) * L::WK + g * (L::WK / L::G));
+    const int vw = L::kVc + kv_word_at(4 * e + ((tok & 7) >> 1), ((tok & 1) + 2 * (tok >> 3)) * L::WV + j % L::WV);
+    const int km = L::kKs + 2 * (tok * L::G + g), vm = L::kVs + 2 * (g * kKvTile + kv_vmeta_pos(tok));
+    for (int hb = h0; hb < h1; hb += U) {
+        uint32_t w[U][2] = {};
+        __half s[U] = {}, z[U] = {};
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = hb + k;
+            if (at.tile && h < h1) {
+                const bool is_v = h >= hkv;
+                const uint8_t* t = at.tile + (h - (is_v ? hkv : 0)) * at.head_bytes;
+                const uint8_t* c = t + (is_v ? vw : kw);
+                w[k][0] = *reinterpret_cast<const uint32_t*>(c);
+                if (BITS == 8) w[k][1] = *reinterpret_cast<const uint32_t*>(c + (is_v ? 16 * 16 : 4));   // (lane 16 further)
+                const uint8_t* m = t + (is_v ? vm : km);
+                s[k] = *reinterpret_cast<const __half*>(m);
+                z[k] = *reinterpret_cast<const __half*>(m + L::kMeta);
             }
         }
-        uint32_t v0, v1 = 0;
-        if (BITS == 4) {
-            v0 = kv_transpose_nibbles(w[0], j / L::WV, L::WV);
-        } else {
-            v0 = kv_transpose_bytes(w[0], j / L::WV, L::WV);
-            v1 = kv_transpose_bytes(w[1], j / L::WV, L::WV);
-        }
-        if (!live) continue;
-        if (is_v) w[0] = v0, w[1] = v1;
-        Vec8<T> y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t c = BITS == 4 ? (w[0] >> (4 * i)) & 15u : (w[i >> 2] >> (8 * (i & 3))) & 255u;
-            y.v[i] = from_f<T>(__fmaf_rn((float)c, s, z));
+        for (int k = 0; k < U; ++k) {
+            const int h = hb + k;
+            if (h >= h1) break;
+            const bool is_v = h >= hkv;
+            if (is_v) {
+                if (BITS == 4) {
+                    w[k][0] = kv_transpose_nibbles(w[k][0], e, L::WV);
+                } else {
+                    w[k][0] = kv_transpose_bytes(w[k][0], e, L::WV);
+                    w[k][1] = kv_transpose_bytes(w[k][1], e, L::WV);
+                }
+            }
+            const float sf = __half2float(s[k]), zf = __half2float(z[k]);
+            Vec8<T> y;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c = BITS == 4 ? (w[k][0] >> (4 * i)) & 15u : (w[k][i >> 2] >> (8 * (i & 3))) & 255u;
+                y.v[i] = from_f<T>(__fmaf_rn((float)c, sf, zf));
+            }
+            if (live) store8(static_cast<T*>(is_v ? P.v : P.k) + (n * hkv + (h - (is_v ? hkv : 0))) * D + 8 * j, y);
         }
-        T* out = static_cast<T*>(is_v ? P.v : P.k) + (n * hkv + head) * D + 8 * j;
-        store8(out, y);
     }
 }
 
-// Blocks of a token: its rows in as few blocks as still give every SM several.
-int row_chunks(int64_t n, int rows, int rows_at_once, int num_sms) {
-    const int most = (rows + rows_at_once - 1) / rows_at_once;
-    return (int)std::min<int64_t>(most, std::max<int64_t>(1, (8 * (int64_t)num_sms + n - 1) / n));
+// Rows that one group of lanes walks: as many as leave about 1536 threads for every SM.
+int rows_per_group(int64_t n, int lanes, int rows, int num_sms) {
+    const int64_t groups = std::max<int64_t>(1, (int64_t)num_sms * 1536 / lanes);
+    const int chunks = (int)std::min<int64_t>(rows, std::max<int64_t>(1, (groups + n - 1) / n));
+    return (rows + chunks - 1) / chunks;
 }
 
-lq_status launched() { return cudaPeekAtLastError() == cudaSuccess ? LQ_OK : LQ_ERR_CUDA; }
+// A launch that may begin while the kernel before it ends (it waits before it touches memory).
+template <class Params>
+lq_status launch(void (*kernel)(Params), dim3 grid, cudaStream_t stream, const Params& P) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+}
 
 KvView view(const lq_kv_cache& c) {
     return KvView{static_cast<uint8_t*>(c.pages), c.num_pages, c.page_size, c.kv_heads, c.page_size / kKvTile};
@@ -433,10 +554,11 @@ lq_status launch_rope_table(lq_handle h, const lq_rope_config& c, int first, int
         }
         P.step[i] = (uint64_t)nearbyint(f * (keep + (1.0 - keep) / c.factor) / pi2 * 18446744073709551616.0);
     }
-    const int per = 256 / P.half;
-    const int grid = (int)std::min<int64_t>(((int64_t)count + per - 1) / per, (int64_t)h->num_sms * 32);
-    rope_table_kernel<<<grid, 256, 0, stream>>>(P);
-    return launched();
+    // about four blocks for every SM, which hold their tables at once
+    const int64_t steps = ((int64_t)count + kFine - 1) / kFine;
+    P.steps = (int)std::min<int64_t>(kCoarse, (steps + 4 * h->num_sms - 1) / (4 * h->num_sms));
+    const dim3 grid((unsigned)((steps + P.steps - 1) / P.steps));
+    return P.half % 4 == 0 ? launch(rope_table_kernel<4>, grid, stream, P) : launch(rope_table_kernel<1>, grid, stream, P);
 }
 
 lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream) {
@@ -446,7 +568,7 @@ lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream) {
     P.xt = a.x_token_stride, P.xh = a.x_head_stride, P.yt = a.y_token_stride, P.yh = a.y_head_stride;
     P.table = a.table;
     P.positions = a.positions;
-    P.heads = a.heads, P.D = a.head_dim, P.rot = a.rot_dim, P.rows = a.table_rows;
+    P.n = a.n, P.heads = a.heads, P.D = a.head_dim, P.rot = a.rot_dim, P.rows = a.table_rows;
     P.layout = a.layout, P.inverse = a.inverse;
     P.status = h->status_flag;
     const int e = a.dtype == LQ_F32 ? 4 : 2;
@@ -457,34 +579,54 @@ lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream) {
     if (bits % 16 == 0 && P.D % 8 == 0 && P.D <= 256 && P.rot % 16 == 0) {
         P.lanes = 1;
         while (8 * P.lanes < P.D) P.lanes *= 2;
-        const dim3 grid((unsigned)a.n, row_chunks(a.n, P.heads, 256 / P.lanes, h->num_sms));
-        if (a.dtype == LQ_F32) rope_kernel<float><<<grid, 256, 0, stream>>>(P);
-        else if (a.dtype == LQ_F16) rope_kernel<__half><<<grid, 256, 0, stream>>>(P);
-        else rope_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(P);
-    } else {
-        const int64_t work = (int64_t)P.heads * (P.D - P.rot / 2);
-        const dim3 grid((unsigned)a.n, (unsigned)std::min<int64_t>((work + 255) / 256, 64));
-        if (a.dtype == LQ_F32) rope_any_kernel<float><<<grid, 256, 0, stream>>>(P);
-        else if (a.dtype == LQ_F16) rope_any_kernel<__half><<<grid, 256, 0, stream>>>(P);
-        else rope_any_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(P);
+        P.chunk = rows_per_group(P.n, P.lanes, P.heads, h->num_sms);
+        const int at_once = 256 / P.lanes;
+        const dim3 grid((unsigned)((P.n + (int64_t)at_once - 1) / at_once), (P.heads + P.chunk - 1) / P.chunk);
+        if (P.chunk > 1) {
+            if (a.dtype == LQ_F32) return launch(rope_kernel<float, 4>, grid, stream, P);
+            return a.dtype == LQ_F16 ? launch(rope_kernel<__half, 4>, grid, stream, P) : launch(rope_kernel<__nv_bfloat16, 4>, grid, stream, P);
+        }
+        if (a.dtype == LQ_F32) return launch(rope_kernel<float, 1>, grid, stream, P);
+        return a.dtype == LQ_F16 ? launch(rope_kernel<__half, 1>, grid, stream, P) : launch(rope_kernel<__nv_bfloat16, 1>, grid, stream, P);
     }
-    return launched();
+    const int64_t work = (int64_t)P.heads * (P.D - P.rot / 2);
+    const dim3 grid((unsigned)a.n, (unsigned)std::min<int64_t>((work + 255) / 256, 64));
+    if (a.dtype == LQ_F32) return launch(rope_any_kernel<float>, grid, stream, P);
+    return a.dtype == LQ_F16 ? launch(rope_any_kernel<__half>, grid, stream, P) : launch(rope_any_kernel<__nv_bfloat16>, grid, stream, P);
 }
 
 namespace {
 
-template <int BITS, int D>
-void append_typed(int dtype, const AppendParams& P, dim3 grid, cudaStream_t stream) {
-    if (dtype == LQ_F32) kv_append_kernel<BITS, D, float><<<grid, 256, 0, stream>>>(P);
-    else if (dtype == LQ_F16) kv_append_kernel<BITS, D, __half><<<grid, 256, 0, stream>>>(P);
-    else kv_append_kernel<BITS, D, __nv_bfloat16><<<grid, 256, 0, stream>>>(P);
+template <int BITS, int D, int U>
+lq_status append_typed(int dtype, const AppendParams& P, dim3 grid, cudaStream_t stream) {
+    if (dtype == LQ_F32) return launch(kv_append_kernel<BITS, D, float, U>, grid, stream, P);
+    return dtype == LQ_F16 ? launch(kv_append_kernel<BITS, D, __half, U>, grid, stream, P)
+                           : launch(kv_append_kernel<BITS, D, __nv_bfloat16, U>, grid, stream, P);
+}
+
+template <int BITS, int D, int U>
+lq_status read_typed(int dtype, const ReadParams& P, dim3 grid, cudaStream_t stream) {
+    if (dtype == LQ_F32) return launch(kv_read_kernel<BITS, D, float, U>, grid, stream, P);
+    return dtype == LQ_F16 ? launch(kv_read_kernel<BITS, D, __half, U>, grid, stream, P)
+                           : launch(kv_read_kernel<BITS, D, __nv_bfloat16, U>, grid, stream, P);
 }
 
 template <int BITS, int D>
-void read_typed(int dtype, const ReadParams& P, dim3 grid, cudaStream_t stream) {
-    if (dtype == LQ_F32) kv_read_kernel<BITS, D, float><<<grid, 256, 0, stream>>>(P);
-    else if (dtype == LQ_F16) kv_read_kernel<BITS, D, __half><<<grid, 256, 0, stream>>>(P);
-    else kv_read_kernel<BITS, D, __nv_bfloat16><<<grid, 256, 0, stream>>>(P);
+lq_status append_chunked(lq_handle h, int dtype, AppendParams& P, cudaStream_t stream) {
+    constexpr int kLanes = D / 8, kAtOnce = 256 / kLanes;
+    const int rows = P.q_heads + 2 * P.cache.kv_heads;
+    P.chunk = rows_per_group(P.n, kLanes, rows, h->num_sms);
+    const dim3 grid((unsigned)((P.n + (int64_t)kAtOnce - 1) / kAtOnce), (rows + P.chunk - 1) / P.chunk);
+    return P.chunk > 1 ? append_typed<BITS, D, 4>(dtype, P, grid, stream) : append_typed<BITS, D, 1>(dtype, P, grid, stream);
+}
+
+template <int BITS, int D>
+lq_status read_chunked(lq_handle h, int dtype, ReadParams& P, cudaStream_t stream) {
+    constexpr int kLanes = D / 8, kAtOnce = 256 / kLanes;
+    const int rows = ((P.k != nullptr) + (P.v != nullptr)) * P.cache.kv_heads;
+    P.chunk = rows_per_group(P.n, kLanes, rows, h->num_sms);
+    const dim3 grid((unsigned)((P.n + (int64_t)kAtOnce - 1) / kAtOnce), (rows + P.chunk - 1) / P.chunk);
+    return P.chunk > 1 ? read_typed<BITS, D, 4>(dtype, P, grid, stream) : read_typed<BITS, D, 1>(dtype, P, grid, stream);
 }
 
 }  // namespace
@@ -495,13 +637,12 @@ lq_status launch_kv_append(lq_handle h, const lq_kv_cache& c, const lq_kv_append
     P.q = a.q, P.k = a.k, P.v = a.v, P.q_out = a.q_out;
     P.qt = a.q_token_stride, P.kt = a.k_token_stride, P.vt = a.v_token_stride, P.ot = a.q_out_token_stride;
     P.slots = a.slots;
+    P.n = a.n;
     P.table = a.table, P.positions = a.positions;
     P.q_heads = a.q ? a.q_heads : 0, P.rot = a.rot_dim, P.rows = a.table_rows, P.layout = a.layout;
     P.status = h->status_flag;
-    const dim3 grid((unsigned)a.n, row_chunks(a.n, P.q_heads + 2 * c.kv_heads, 256 / (c.head_dim / 8), h->num_sms));
-    if (c.head_dim == 128) c.bits == 4 ? append_typed<4, 128>(a.dtype, P, grid, stream) : append_typed<8, 128>(a.dtype, P, grid, stream);
-    else c.bits == 4 ? append_typed<4, 64>(a.dtype, P, grid, stream) : append_typed<8, 64>(a.dtype, P, grid, stream);
-    return launched();
+    if (c.head_dim == 128) return c.bits == 4 ? append_chunked<4, 128>(h, a.dtype, P, stream) : append_chunked<8, 128>(h, a.dtype, P, stream);
+    return c.bits == 4 ? append_chunked<4, 64>(h, a.dtype, P, stream) : append_chunked<8, 64>(h, a.dtype, P, stream);
 }
 
 lq_status launch_kv_read(lq_handle h, const lq_kv_cache& c, const int64_t* slots, int n, void* k, void* v, int dtype,
@@ -509,13 +650,11 @@ lq_status launch_kv_read(lq_handle h, const lq_kv_cache& c, const int64_t* slots
     ReadParams P;
     P.cache = view(c);
     P.slots = slots;
+    P.n = n;
     P.k = k, P.v = v;
     P.status = h->status_flag;
-    const int rows = ((k != nullptr) + (v != nullptr)) * c.kv_heads;
-    const dim3 grid((unsigned)n, row_chunks(n, rows, 256 / (c.head_dim / 8), h->num_sms));
-    if (c.head_dim == 128) c.bits == 4 ? read_typed<4, 128>(dtype, P, grid, stream) : read_typed<8, 128>(dtype, P, grid, stream);
-    else c.bits == 4 ? read_typed<4, 64>(dtype, P, grid, stream) : read_typed<8, 64>(dtype, P, grid, stream);
-    return launched();
+    if (c.head_dim == 128) return c.bits == 4 ? read_chunked<4, 128>(h, dtype, P, stream) : read_chunked<8, 128>(h, dtype, P, stream);
+    return c.bits == 4 ? read_chunked<4, 64>(h, dtype, P, stream) : read_chunked<8, 64>(h, dtype, P, stream);
 }
 
 }  // namespace lq

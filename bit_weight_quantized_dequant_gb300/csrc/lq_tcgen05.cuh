@@ -7,6 +7,18 @@
 
 namespace lq {
 
+// Allocate `ncols` (power of two >= 32) tensor-memory columns for this CTA; the base address is
+// written to shared memory at `dst`.  Executed by one full warp, as is the release.
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
 // Allocate `ncols` (power of two >= 32) tensor-memory columns for a CTA pair (cta_group::2):
 // one full warp of each of the two CTAs executes it, both receive the same column range, and
 // the base address is written to shared memory at `dst` in each CTA.
@@ -43,6 +55,23 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
            | ((bf16 ? 1u : 0u) << 10)                       // B format
            | ((uint32_t)(N >> 3) << 17)                     // N / 8
            | ((uint32_t)(M >> 4) << 24);                    // M / 16
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T on one CTA (M = 128), issued by one thread.  A sits in tensor
+// memory with row r in lane r and 16-bit elements 2c, 2c + 1 of the row in column c.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
 }
 
 // CTA-pair MMA (M = 256): issued by one thread of the pair's even CTA.  Each CTA holds its
