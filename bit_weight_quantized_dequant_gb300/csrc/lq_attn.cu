@@ -29,7 +29,7 @@
 // synchronisation, and a captured graph serves any lengths.
 //
 // A shared prefix runs first, with every request's rows as one unit list over the prefix pages; its
-// normalised rows and log-sum-exps join at the end of the second run.  Few rows or a short prefix
+// sums join the rows' own at the end of the second run.  Few rows or a short prefix
 // take this kernel for it, many rows the tensor-memory kernel (lq_attn_prefix.cu).
 
 #include <algorithm>
@@ -681,13 +681,15 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
     P.status = h->status_flag;
     if ((int64_t)a.batch * a.tokens * P.group > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     P.all_rows = a.batch * a.tokens * P.group;
-    // workspace: the prefix's rows and log-sum-exps, then partial sums
+    // workspace: what the prefix run leaves, then partial sums
     char* ws = reinterpret_cast<char*>(h->partials);
     const size_t cap = h->partial_floats * sizeof(float), rows = (size_t)c.kv_heads * P.all_rows;
-    const size_t pre = a.prefix_len > 0 ? (rows * (c.head_dim + 1) * sizeof(float) + 255) & ~size_t(255) : 0;
+    const size_t slots = a.prefix_len > 0 ? prefix_tc_bytes(h, c.kv_heads, P.all_rows, a.prefix_len, c.head_dim) : 0;
+    const size_t pre = a.prefix_len == 0 ? 0 : slots ? slots : (rows * (c.head_dim + 1) * sizeof(float) + 255) & ~size_t(255);
     if (pre > cap) return LQ_ERR_WORKSPACE;
     P.pre_o = reinterpret_cast<float*>(ws);
-    P.pre_lse = P.pre_o + rows * c.head_dim;
+    P.pre_m = P.pre_o + rows * c.head_dim;
+    P.pre_rows = 0;
     const bool bf16 = a.dtype == LQ_BF16;
     auto go = [&](AttnParams& p) {
         if (c.head_dim == 128)
@@ -698,9 +700,7 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
         P.prefix = 1;
         P.block_table = a.prefix_table, P.bt_stride = 0, P.lens = nullptr;
         P.requests = 1, P.rows = P.all_rows, P.max_len = a.prefix_len;
-        const lq_status s = prefix_tc_takes(P.all_rows, a.prefix_len)
-                                ? launch_prefix_tc(h, P, c.bits, c.head_dim, bf16, ws + pre, cap - pre, stream)
-                                : go(P);
+        const lq_status s = slots ? launch_prefix_tc(h, P, c.bits, c.head_dim, bf16, ws, stream) : go(P);
         if (s != LQ_OK) return s;
     }
     P.prefix = a.prefix_len > 0 ? 2 : 0;

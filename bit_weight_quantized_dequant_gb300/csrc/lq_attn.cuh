@@ -26,11 +26,23 @@ struct AttnParams {
     float scale_log2;                    // scale * log2(e)
     float* part;                         // partial sums: 2 slots per block
     unsigned* counters;                  // one per unit, zero between calls
-    float *pre_o, *pre_lse;              // the prefix's rows [kv_heads][rows of all requests][D] and log2-sum-exps
+    // The prefix run's sums, which the second run joins with its own.  As records: normalised rows [kv_heads]
+    // [rows of all requests][D] and their reference; as slots (pre_rows > 0): the prefix kernel's partial sums,
+    // two slots of pre_rows rows per block, blocks sharing pre_total key blocks evenly, pre_each per unit.
+    float *pre_o, *pre_m;
+    int pre_rows, pre_tiles, pre_each, pre_total, pre_blocks;
     int all_rows;                        // rows of all requests per kv head
     int prefix;                          // 0: none, 1: this is the prefix run, 2: join the prefix's rows
     int* status;
 };
+
+// n things shared out to c parties in order, the first n % c of them one more: the first of party k, and
+// the party of thing i.
+__device__ __forceinline__ int share_first(int n, int c, int k) { return n / c * k + min(k, n % c); }
+__device__ __forceinline__ int share_of(int n, int c, int i) {
+    const int q = n / c, rem = n % c;
+    return i < rem * (q + 1) ? i / (q + 1) : rem + (i - rem * (q + 1)) / q;
+}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -84,53 +96,86 @@ __device__ __forceinline__ float elem_to_float<__half>(uint16_t bits) { return h
 template <>
 __device__ __forceinline__ float elem_to_float<__nv_bfloat16>(uint16_t bits) { return bf16_bits_to_float(bits); }
 
-// Where a row's result goes, and its factors: out = v * own (+ the prefix's row * pre).
+// Where a row's result goes, and what joins it there: out = (v 2^(m - top) + sum of the prefix's parts) / total.
 template <int D, class T>
 struct RowOut {
     T* out;
-    float *pre, own, shared;
+    float own, top, inv;
+    // the prefix's parts of this row: sums at part + k * stride (the first `lead` floats further), their
+    // (reference, sum of P) the same way from ml
+    const float *part, *ml;
+    int64_t stride;
+    int parts, lead;
+
+    __device__ __forceinline__ const float* at(const float* p, int k) const { return p + (k == 0 ? lead : k * stride); }
+
     // row: of all requests' rows of a kv head; (m, l): reference and sum of P.  One lane (`writes`)
     // stores the log-sum-exp.
     __device__ __forceinline__ RowOut(const AttnParams& P, int row, int head, float m, float l, bool writes) {
-        float s = l == 0.f ? -INFINITY : m + log2f(l) - kPBits;
-        own = l == 0.f ? 0.f : 1.f / l;
-        shared = 0.f;
-        const int64_t at = (int64_t)head * P.all_rows + row;
-        pre = P.pre_o + at * D;
-        if (P.prefix == 1) {
-            if (writes) P.pre_lse[at] = s;
+        parts = 0;
+        top = m;
+        const int64_t rec = (int64_t)head * P.all_rows + row;
+        if (P.prefix == 1) {   // a record: normalised, so its sum of P counts as 1
+            own = l == 0.f ? 0.f : 1.f / l;
+            inv = 1.f;
+            out = reinterpret_cast<T*>(P.pre_o + rec * D);
+            if (writes) P.pre_m[rec] = l == 0.f ? -INFINITY : m + log2f(l);
             return;
         }
         if (P.prefix == 2) {
-            const float s2 = __ldcg(P.pre_lse + at), top = fmaxf(s, s2);
-            if (top != -INFINITY) {
-                const float a = ex2(s - top), c = ex2(s2 - top), f = 1.f / (a + c);
-                own *= a * f;
-                shared = c * f;
-                s = top + log2f(a + c);
+            if (P.pre_rows) {
+                const int rt = row / P.pre_rows, r = row - rt * P.pre_rows, us = (head * P.pre_tiles + rt) * P.pre_each;
+                const int c0 = share_of(P.pre_total, P.pre_blocks, us), c1 = share_of(P.pre_total, P.pre_blocks, us + P.pre_each - 1);
+                const int slot = P.pre_rows * (D + 2);
+                part = P.pre_o + (int64_t)2 * c0 * slot + r * D;
+                ml = P.pre_o + (int64_t)2 * c0 * slot + P.pre_rows * D + 2 * r;
+                stride = 2 * slot, lead = slot, parts = c1 - c0 + 1;
+            } else {
+                part = P.pre_o + rec * D;
+                ml = P.pre_m + rec;
+                stride = 0, lead = 0, parts = 1;
             }
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(at(ml, k)));
         }
+        const float ref = top == -INFINITY ? 0.f : top;
+        own = ex2(m - ref);
+        float total = l * own;
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float* e = at(ml, k);
+            total = fmaf(P.pre_rows ? __ldcg(e + 1) : 1.f, ex2(__ldcg(e) - ref), total);
+        }
+        top = ref;
+        inv = total == 0.f ? 0.f : 1.f / total;
         const int bt = row / P.group, qh = head * P.group + (row - bt * P.group);
         out = static_cast<T*>(P.out) + bt * P.out_stride + (int64_t)qh * D;
-        if (writes && P.lse) P.lse[(int64_t)bt * P.q_heads + qh] = s * 0.6931471805599453f;
+        if (writes && P.lse) P.lse[(int64_t)bt * P.q_heads + qh] = total == 0.f ? -INFINITY : (ref + log2f(total) - kPBits) * 0.6931471805599453f;
     }
     // V dimensions from d on
     template <int V>
     __device__ __forceinline__ void store(const AttnParams& P, int d, float (&v)[V]) const {
-        if (P.prefix == 1) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] *= own;
-            if (V == 4) *reinterpret_cast<float4*>(pre + d) = make_float4(v[0], v[1], v[V - 2], v[V - 1]);
-            else *reinterpret_cast<float2*>(pre + d) = make_float2(v[0], v[1]);
+        for (int i = 0; i < V; ++i) v[i] *= own;
+        if (P.prefix == 1) {
+            float* rec = reinterpret_cast<float*>(out) + d;
+            if (V == 4) *reinterpret_cast<float4*>(rec) = make_float4(v[0], v[1], v[V - 2], v[V - 1]);
+            else *reinterpret_cast<float2*>(rec) = make_float2(v[0], v[1]);
             return;
+        }
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float f = ex2(__ldcg(at(ml, k)) - top);
+            const float* o = at(part, k) + d;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 e = __ldcg(reinterpret_cast<const float2*>(o + i));
+                v[i] = fmaf(e.x, f, v[i]), v[i + 1] = fmaf(e.y, f, v[i + 1]);
+            }
         }
         alignas(4 * V) T o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] *= own;
-            if (P.prefix == 2) v[i] = fmaf(__ldcg(pre + d + i), shared, v[i]);
-            o[i] = (T)v[i];
-        }
+        for (int i = 0; i < V; ++i) o[i] = (T)(v[i] * inv);
         if (V == 4) *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(o);
         else *reinterpret_cast<uint32_t*>(out + d) = *reinterpret_cast<const uint32_t*>(o);
     }
@@ -182,8 +227,9 @@ __device__ __forceinline__ void join(const AttnParams& P, int c0, int c1, int wa
     }
 }
 
-// The shared prefix's run on the tensor-memory tensor cores; scratch holds its partial sums.
-bool prefix_tc_takes(int rows, int prefix_len);
-lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf16, char* scratch, size_t room, cudaStream_t stream);
+// The shared prefix's run on the tensor-memory tensor cores, which leaves partial sums in `scratch`.
+// prefix_tc_bytes: what it needs of that, 0 where the other kernel takes the prefix.
+size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D);
+lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf16, char* scratch, cudaStream_t stream);
 
 }  // namespace lq

@@ -2,11 +2,12 @@
 //
 // A prefix that all requests of a batch share meets all their rows: batch * tokens * group rows
 // per kv head, hundreds of them, so the work is a dense contraction and no longer the cache's
-// bytes.  A block takes 128 rows of one kv head and a range of keys, 64 at a time:
-//   S [128 rows][64 keys] = Q K^T      Q in tensor memory, K in shared memory
-//   P = 2^(S f - m)                    a thread per row, S read from and P written to tensor memory
-//   O [128 rows][D]      += P V        P in tensor memory, V [D][64 keys] in shared memory
-// by one-CTA tcgen05.mma (M 128, N 64 and N D, binary16 operands, fp32 sums).
+// bytes.  A block takes 128 rows of one kv head and a range of keys, 128 at a time:
+//   S [128 rows][128 keys] = Q K^T     Q in tensor memory, K in shared memory
+//   P = 2^(S f - m)                    S read from and P written to tensor memory
+//   O [128 rows][D]       += P V       P in tensor memory, V [D][128 keys] in shared memory
+// by one-CTA tcgen05.mma (M 128, N 128 and N D, binary16 operands, fp32 sums).  An M = 128 MMA
+// takes 62 cycles at N = 64 and 64 at N = 128 (measured), so narrower key blocks waste the pipe.
 //
 // Scores keep fp32 precision.  K's code part S c is the sum of two binary16 values, its rounding
 // and what that left out (one fused multiply-add gives it exactly), each multiplied; its offset
@@ -14,14 +15,16 @@
 // times 2^-2 and V times 2^-1, so that nothing within the cache's range overflows; V is rounded
 // to binary16 (absolute error 2^-24 below 2^-13).
 //
-// Roles (18 warps): one loads tiles by bulk copies; one thread issues the MMAs; eight expand
-// codes (four K, four V: a 16-token tile each); eight do the softmax, as two groups of 128 threads
-// that take the key blocks in turn, each with its own S/P buffer, running maximum and O (two O
-// accumulators need no exchange between the groups until the unit's end).  All MMAs come from one
-// thread and run in its order, so one barrier per buffer and direction suffices: S full (which
-// also frees K's stage and, being later in order, says that P's buffer was read), P full, O done
-// (which frees V's stage).  Every wait is bounded; a role whose wait ran out goes on with what is
-// there, so every loop and barrier still ends, and the status word reports it.
+// Roles (27 warps): two load keys' and values' bytes by bulk copies, each into a ring of its own
+// (values wait for the O before them, keys run two blocks ahead); one issues the MMAs; sixteen expand codes (eight K,
+// eight V, a 16-token tile each); eight do the softmax, two threads per row with half of the keys each,
+// which share the row's reference (one barrier of their two warps per key block tells whether it has
+// to move).  K and S have two stages, so that the next block's scores are computed while this one's
+// softmax runs; V has one: its next block is expanded while those scores are.  All MMAs come from one
+// thread and run in its order, so few barriers suffice: S full (which also frees K's stage and, being
+// later in order, says that P's buffer was read), P full, O done (which frees V's stage).  Every wait
+// is bounded; a role whose wait ran out goes on with what is there, so every loop and barrier still
+// ends, and the status word reports it.
 
 #include <algorithm>
 #include <mutex>
@@ -34,37 +37,39 @@ namespace lq {
 namespace {
 
 constexpr int kRows = 128;          // rows of a unit
-constexpr int kKeys = 64;           // keys of a block
-constexpr int kTiles = kKeys / kKvTile;
-constexpr int kRaw = 3;             // key blocks of cache bytes in flight
-constexpr int kSoftWarps = 8, kDqWarps = 8;
+constexpr int kKeys = 128;          // keys of a block
+constexpr int kHalf = 4;            // tiles of half a block, which are loaded and expanded together
+constexpr int kSoftWarps = 8, kDqWarps = 16;
 constexpr int kSoft0 = 0, kDq0 = kSoft0 + kSoftWarps, kMmaWarp = kDq0 + kDqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kThreads = 32 * (kLoadWarp + 2);
 // tensor memory columns
 constexpr int kTmemCols = 512;
-constexpr int kColS = 0;            // 2 x 64: S, then P in the first 32 of each
-constexpr int kColO = 128;          // 2 x D
+constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
+constexpr int kColO = 256;          // D
 constexpr int kColQ = 384;          // D / 2
 constexpr int kColZ = 448;          // 8 (group sums of q), 32 written
-static_assert(kColO + 2 * 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 32 <= kTmemCols, "tensor memory");
+static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 32 <= kTmemCols, "tensor memory");
 
 template <int BITS, int D>
 struct PreSmem {
     using L = KvLayout<BITS, D>;
     static constexpr int kAtoms = D / 64;                        // 128-byte rows of 64 dimensions
     static constexpr int kAtom = kKeys * 128;                    // one of them for all keys of a block
-    static constexpr int kKStage = (2 * kAtoms + 1) * kAtom;     // K rounded, K's rest, Z
-    static constexpr int kVStage = D * 128;                      // [D][64 keys]
-    static constexpr int kRawStage = (kTiles * L::kBytes + 127) / 128 * 128;
+    static constexpr int kKStage = 2 * kAtoms * kAtom;           // K rounded, K's rest
+    static constexpr int kVAtom = D * 128;                       // [D][64 keys]
+    static constexpr int kRawTile = L::kCodes + 2 * L::kMeta;    // a tile's keys (or values): codes, S, Z
+    static constexpr int kRawStage = kHalf * kRawTile;
+    static constexpr int kRawK = L::kBytes <= 2560 ? 5 : 3, kRawV = L::kBytes <= 2560 ? 4 : 2;   // half blocks in flight
     static constexpr int kK = 0;
-    static constexpr int kV = kK + 2 * kKStage;
-    static constexpr int kRawOff = kV + 2 * kVStage;
-    static constexpr int kMl = kRawOff + kRaw * kRawStage;       // [2 groups][rows] m, l
-    static constexpr int kF = kMl + 2 * kRows * 8;               // [rows] score factors
+    static constexpr int kZ = kK + 2 * kKStage;                  // Z of stage b in chunk 2 b of each key's row
+    static constexpr int kV = kZ + kAtom;
+    static constexpr int kRawOff = kV + 2 * kVAtom;
+    static constexpr int kMl = kRawOff + (kRawK + kRawV) * kRawStage;       // [2 halves][rows] maxima, then sums
+    static constexpr int kF = kMl + 2 * kRows * 4;               // [rows] score factors
     static constexpr int kBars = kF + kRows * 4;
-    static constexpr int kNumBars = 2 * kRaw + 2 * 5 + 1;
+    static constexpr int kNumBars = 2 * (kRawK + kRawV) + 2 * 3 + 3;
     static constexpr int kSize = 1024 + kBars + 8 * kNumBars;
-    static_assert(kSize <= 227 * 1024 && kBars % 8 == 0, "shared memory");
+    static_assert(kSize <= 227 * 1024 && kBars % 8 == 0 && kRawOff % 128 == 0 && kRawStage % 16 == 0, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -77,8 +82,32 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// Two fp32 values at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
+// Whether any thread of a row's two warps says so (and a barrier of the two).
+__device__ __forceinline__ bool pair_any(int pair, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)mine), "r"(2 + pair)
+        : "memory");
+    return any != 0;
+}
 __device__ __forceinline__ void sts128(uint8_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
 }
@@ -96,9 +125,9 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int r) {
 }
 
 // Keys of one tile: [token][dims] rows of the K stage, in the order of the words' pairs (Q's columns
-// follow it).  left: tokens of the prefix from the tile's first on.
+// follow it), and Z.  left: tokens of the prefix from the tile's first on.
 template <int BITS, int D>
-__device__ __forceinline__ void expand_keys(const uint8_t* tile, uint8_t* stage, int tile_no, int left, int lane) {
+__device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, uint8_t* zs, int zchunk, int tile_no, int left, int lane) {
     using L = KvLayout<BITS, D>;
     using M = PreSmem<BITS, D>;
     constexpr int G = D / 32, WK = L::WK, U = WK / G;   // U words of a group (1 or 2)
@@ -118,8 +147,8 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, uint8_t* stage,
         uint32_t s[G / 2], z[G / 2];
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) {
-            s[i] = hmul2(lds32(tile + L::kKs + tok * G * 2 + 4 * i) & keep, 0x34003400u);   // 2^-2
-            z[i] = hmul2(lds32(tile + L::kKz + tok * G * 2 + 4 * i) & keep, 0x34003400u);
+            s[i] = hmul2(lds32(meta + tok * G * 2 + 4 * i) & keep, 0x34003400u);   // 2^-2
+            z[i] = hmul2(lds32(meta + L::kMeta + tok * G * 2 + 4 * i) & keep, 0x34003400u);
         }
         uint8_t* base = stage + row * 128;
 #pragma unroll
@@ -145,7 +174,7 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, uint8_t* stage,
             sts128(at + M::kAtoms * M::kAtom, lo[0], lo[1], lo[2], lo[3]);
         }
         if (t == 0) {   // Z against both terms of the group sums
-            uint8_t* at = base + 2 * M::kAtoms * M::kAtom + (n << 4);
+            uint8_t* at = zs + row * 128 + ((zchunk ^ n) << 4);
             if (G == 4) sts128(at, z[0], z[G / 2 - 1], z[0], z[G / 2 - 1]);
             else sts128(at, z[0], z[0], 0u, 0u);
         }
@@ -154,19 +183,19 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, uint8_t* stage,
 
 // Values of one tile: [dimension][keys] rows of the V stage, two keys per word.
 template <int BITS, int D>
-__device__ __forceinline__ void expand_values(const uint8_t* tile, uint8_t* stage, int tile_no, int left, int lane) {
+__device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, int tile_no, int left, int lane) {
     using L = KvLayout<BITS, D>;
     constexpr int G = D / 32, WV = L::WV;
     const int n = lane >> 2, t = lane & 3;
     alignas(16) uint32_t vw[4 * WV];
 #pragma unroll
     for (int c = 0; c < L::kChunks; ++c)
-        *reinterpret_cast<uint4*>(vw + 4 * c) = lds128(tile + L::kVc + 512 * c + 16 * lane);
+        *reinterpret_cast<uint4*>(vw + 4 * c) = lds128(tile + 512 * c + 16 * lane);
     const uint32_t keep[2] = {(2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u),
                               (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u)};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const uint2 sv = lds64(tile + L::kVs + g * 32 + 8 * t), zv = lds64(tile + L::kVz + g * 32 + 8 * t);
+        const uint2 sv = lds64(meta + g * 32 + 8 * t), zv = lds64(meta + L::kMeta + g * 32 + 8 * t);
         const uint32_t s[2] = {hmul2(sv.x & keep[0], 0x38003800u), hmul2(sv.y & keep[1], 0x38003800u)};   // 2^-1
         const uint32_t z[2] = {hmul2(zv.x & keep[0], 0x38003800u), hmul2(zv.y & keep[1], 0x38003800u)};
 #pragma unroll
@@ -190,46 +219,39 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, uint8_t* stag
     }
 }
 
-// One key block's scores of a row: maximum, reference, P.
-struct RowSum {
-    float m, l, ref;
-};
-
 template <int BITS, int D, class T>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ AttnParams P) {
     using L = KvLayout<BITS, D>;
     using M = PreSmem<BITS, D>;
-    constexpr int G = D / 32;
+    constexpr int G = D / 32, kRawAll = M::kRawK + M::kRawV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms)
-    float2* ml = reinterpret_cast<float2*>(base + M::kMl);
+    float* ml = reinterpret_cast<float*>(base + M::kMl);
     float* factors = reinterpret_cast<float*>(base + M::kF);
     __shared__ uint32_t s_tmem;
-    __shared__ int s_last;
-    __shared__ volatile uint32_t s_there[8];   // a block's tiles that are in the cache (no role is 8 blocks ahead of another)
+    __shared__ volatile uint32_t s_there[2][16];   // a half block's tiles in the cache, keys' and values' (no role is 16 ahead of another)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const uint32_t bars = smem_u32(base + M::kBars);
-    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * kRaw, k_full = raw_empty + 8 * kRaw, v_full = k_full + 16;
-    const uint32_t s_full = v_full + 16, p_full = s_full + 16, o_done = p_full + 16, q_full = o_done + 16;
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * kRawAll, k_full = raw_empty + 8 * kRawAll, s_full = k_full + 16;
+    const uint32_t p_full = s_full + 16, v_full = p_full + 16, o_done = v_full + 8, q_full = o_done + 8;
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) {
+        for (int i = 0; i < kRawAll; ++i) {
             mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, kDqWarps);
+            mbar_init(raw_empty + 8 * i, kHalf);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full + 8 * b, kTiles);
-            mbar_init(v_full + 8 * b, kTiles);
+            mbar_init(k_full + 8 * b, 2 * kHalf);
             mbar_init(s_full + 8 * b, 1);
-            mbar_init(p_full + 8 * b, 4);
-            mbar_init(o_done + 8 * b, 1);
+            mbar_init(p_full + 8 * b, kSoftWarps);
         }
+        mbar_init(v_full, 2 * kHalf);
+        mbar_init(o_done, 1);
         mbar_init(q_full, 4);
         fence_mbar_init();
     }
-    // the Z rows' second 16 bytes multiply nothing: zero for good
-    for (int i = tid; i < 2 * kKeys; i += kThreads)
-        sts128(base + M::kK + (i / kKeys) * M::kKStage + 2 * M::kAtoms * M::kAtom + (i % kKeys) * 128 + ((1 ^ (i & 7)) << 4), 0, 0, 0, 0);
+    // (the odd chunks of the Z rows multiply nothing: zero for good)
+    for (int i = tid; i < M::kAtom / 16; i += kThreads) sts128(base + M::kZ + 16 * i, 0, 0, 0, 0);
     if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
     fence_async_smem();
     tc_fence_before();
@@ -241,21 +263,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
     // this block's key blocks of the sequence of all (kv head, row tile) units' blocks
     const int each = (P.max_len + kKeys - 1) / kKeys;
-    const int total = each * P.cache.kv_heads * P.row_tiles, C = gridDim.x, c = blockIdx.x;
-    const int q = total / C, rem = total - q * C;
-    const int g0 = q * c + min(c, rem), g1 = q * (c + 1) + min(c + 1, rem), blocks = g1 - g0;
+    const int total = each * P.cache.kv_heads * P.row_tiles, c = blockIdx.x;
+    const int g0 = share_first(total, gridDim.x, c), g1 = share_first(total, gridDim.x, c + 1), blocks = g1 - g0;
     int own_abort = 0;
     auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded(bar, parity & 1u, &own_abort, P.status); };
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- tiles into the raw ring
+    if (warp >= kLoadWarp) {
+        // ---------------------------------------------------------------- keys' or values' bytes into their ring
+        const int what = warp - kLoadWarp, ring = what ? M::kRawV : M::kRawK, first = what ? M::kRawK : 0;
+        const uint32_t full = raw_full + 8 * first, empty = raw_empty + 8 * first;
+        const uint32_t dst0 = smem_u32(base + M::kRawOff + first * M::kRawStage);
         const uint8_t* src = nullptr;
-        for (int i = 0; i < blocks; ++i) {
-            if (i % 8 == 0) {   // addresses of eight blocks' tiles, one per lane
-                const int gb = g0 + i + lane / kTiles;
+        int s = 0, turn = -1;
+        for (int i = 0; i < 2 * blocks; ++i) {   // half blocks
+            if (i % 8 == 0) {                    // addresses of four blocks' tiles, one per lane
+                const int gb = g0 + (i + lane / kHalf) / 2;
                 src = nullptr;
                 if (gb < g1) {
-                    const int unit = gb / each, tile = (gb - unit * each) * kTiles + lane % kTiles, head = unit / P.row_tiles;
+                    const int unit = gb / each, head = unit / P.row_tiles;
+                    const int tile = (gb - unit * each) * 2 * kHalf + lane % (2 * kHalf);
                     if (tile * kKvTile < P.max_len) {
                         const int pi = tile / P.cache.tiles_per_page, page = __ldg(P.block_table + pi);
                         if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
@@ -265,95 +291,108 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
                 }
             }
-            const int s = i % kRaw;
-            if (i >= kRaw) wait(raw_empty + 8 * s, i / kRaw - 1);
+            if (turn >= 0) wait(empty + 8 * s, turn);
             __syncwarp();
-            const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (i % 8 * kTiles)) & ((1u << kTiles) - 1u);
+            const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (i % 8 * kHalf)) & ((1u << kHalf) - 1u);
             if (lane == 0) {
-                s_there[i & 7] = there;
-                if (there) mbar_arrive_expect_tx(raw_full + 8 * s, __popc(there) * L::kBytes);
-                else mbar_arrive(raw_full + 8 * s);
+                s_there[what][i & 15] = there;
+                if (there) mbar_arrive_expect_tx(full + 8 * s, __popc(there) * M::kRawTile);
+                else mbar_arrive(full + 8 * s);
             }
             __syncwarp();
-            if (lane / kTiles == i % 8 && src)
-                bulk_load(smem_u32(base + M::kRawOff + s * M::kRawStage) + lane % kTiles * L::kBytes, src, L::kBytes, raw_full + 8 * s);
+            if (lane / kHalf == i % 8 && src) {
+                const uint32_t dst = dst0 + s * M::kRawStage + lane % kHalf * M::kRawTile;
+                bulk_load(dst, src + (what ? L::kVc : 0), L::kCodes, full + 8 * s);
+                bulk_load(dst + L::kCodes, src + (what ? L::kVs : L::kKs), 2 * L::kMeta, full + 8 * s);
+            }
+            if (++s == ring) s = 0, ++turn;
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- all MMAs, one thread
-        if (lane == 0) {
-            const uint32_t idS = idesc_f16(false, kRows, kKeys), idO = idesc_f16(false, kRows, D);
-            const uint32_t ks = smem_u32(base + M::kK), vs = smem_u32(base + M::kV);
-            auto scores = [&](int i) {
-                const int b = i & 1;
-                const uint32_t d = tmem + kColS + kKeys * b, k = ks + b * M::kKStage;
-                wait(k_full + 8 * b, i >> 1);
+        const uint32_t lead = lane == 0;
+        constexpr uint32_t idS = idesc_f16(false, kRows, kKeys), idO = idesc_f16(false, kRows, D);
+        // (descriptors count 16-byte units from their first: a constant each)
+        const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
+        const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
+        auto scores = [&](int i) {
+            const int b = i & 1;
+            const uint32_t d = tmem + kColS + kKeys * b;
+            const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
+            wait(k_full + 8 * b, i >> 1);
+            tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st)
+                    tc_mma_f16_ts(lead, d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16,
+                                  idS, (part | st) != 0);
+            tc_mma_f16_ts(lead, d, tmem + kColZ, zd + 2 * b, idS, 1);
+            tc_commit(lead, s_full + 8 * b);
+        };
+        int done = 0;   // blocks of earlier units
+        for (int u = 0; done < blocks; ++u) {
+            const int unit = (g0 + done) / each, nb = min((unit + 1) * each, g1) - (g0 + done);
+            wait(q_full, u);
+            tc_fence_after();
+            scores(done);
+            for (int j = 0; j < nb; ++j) {
+                const int i = done + j, b = i & 1;
+                if (j + 1 < nb) scores(i + 1);
+                wait(v_full, i);
+                wait(p_full + 8 * b, i >> 1);
                 tc_fence_after();
+                __syncwarp();
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int st = 0; st < D / 16; ++st)
-                        tc_mma_f16_ts(d, tmem + kColQ + 8 * st,
-                                      smem_desc_sw128(k + (part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)), idS, (part | st) != 0);
-                tc_mma_f16_ts(d, tmem + kColZ, smem_desc_sw128(k + 2 * M::kAtoms * M::kAtom), idS, 1);
-                tc_commit(s_full + 8 * b);
-            };
-            int done = 0;   // blocks of earlier units
-            for (int u = 0; done < blocks; ++u) {
-                const int unit = (g0 + done) / each, nb = min((unit + 1) * each, g1) - (g0 + done);
-                wait(q_full, u);
-                tc_fence_after();
-                scores(done);
-                if (nb > 1) scores(done + 1);
-                for (int j = 0; j < nb; ++j) {
-                    const int i = done + j, b = i & 1;
-                    wait(v_full + 8 * b, i >> 1);
-                    wait(p_full + 8 * b, i >> 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int st = 0; st < kKeys / 16; ++st)
-                        tc_mma_f16_ts(tmem + kColO + D * b, tmem + kColS + kKeys * b + 8 * st,
-                                      smem_desc_sw128(vs + b * M::kVStage + 32 * st), idO, j >= 2 || st != 0);
-                    tc_commit(o_done + 8 * b);
-                    if (j + 2 < nb) scores(i + 2);
-                }
-                done += nb;
+                for (int st = 0; st < kKeys / 16; ++st)
+                    tc_mma_f16_ts(lead, tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4),
+                                  vd + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, j != 0 || st != 0);
+                tc_commit(lead, o_done);
             }
+            done += nb;
         }
         __syncwarp();
     } else if (warp >= kDq0) {
         // ---------------------------------------------------------------- codes to operands
-        const int w = warp - kDq0, tile_no = w % kTiles;
-        const bool keys = w < kTiles;
+        const int w = warp - kDq0, tile_no = w % kHalf, half = w / kHalf & 1;   // this warp's tile of every block
+        const bool keys = w < 2 * kHalf;
+        const int ring = keys ? M::kRawK : M::kRawV, first = keys ? 0 : M::kRawK, no = half * kHalf + tile_no;
+        const uint8_t* raw = base + M::kRawOff + first * M::kRawStage + tile_no * M::kRawTile;
+        int s = half % ring, turn = half / ring;   // half block 2 i + half in stage (2 i + half) % ring
         for (int i = 0; i < blocks; ++i) {
-            const int s = i % kRaw, b = i & 1, gb = g0 + i, kb = gb - gb / each * each;
-            wait(raw_full + 8 * s, i / kRaw);
-            if (i >= 2) wait((keys ? s_full : o_done) + 8 * b, (i >> 1) - 1);   // the stage's last MMAs have read it
-            const uint8_t* tile = base + M::kRawOff + s * M::kRawStage + tile_no * L::kBytes;
-            const int left = s_there[i & 7] >> tile_no & 1u ? P.max_len - kb * kKeys - tile_no * kKvTile : 0;
-            if (keys) expand_keys<BITS, D>(tile, base + M::kK + b * M::kKStage, tile_no, left, lane);
-            else expand_values<BITS, D>(tile, base + M::kV + b * M::kVStage, tile_no, left, lane);
+            const int b = i & 1, gb = g0 + i, kb = gb - gb / each * each;
+            wait(raw_full + 8 * (first + s), turn);
+            // the stage's last MMAs have read it
+            if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
+            if (!keys && i >= 1) wait(o_done, i - 1);
+            const uint8_t* tile = raw + s * M::kRawStage;
+            const int left = s_there[keys ? 0 : 1][(2 * i + half) & 15] >> tile_no & 1u ? P.max_len - kb * kKeys - no * kKvTile : 0;
+            if (keys) expand_keys<BITS, D>(tile, tile + L::kCodes, base + M::kK + b * M::kKStage, base + M::kZ, 2 * b, no, left, lane);
+            else expand_values<BITS, D>(tile, tile + L::kCodes, base + M::kV + half * M::kVAtom, tile_no, left, lane);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive((keys ? k_full : v_full) + 8 * b);
-                mbar_arrive(raw_empty + 8 * s);
+                mbar_arrive(keys ? k_full + 8 * b : v_full);
+                mbar_arrive(raw_empty + 8 * (first + s));
             }
+            s += 2;
+            if (s >= ring) s -= ring, ++turn;
         }
     } else {
-        // ---------------------------------------------------------------- softmax: a thread per row
-        const int grp = warp >> 2, r = 32 * (warp & 3) + lane;         // group of the blocks with i & 1 == grp
+        // ---------------------------------------------------------------- softmax: two threads per row
+        const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         int done = 0;
         for (int u = 0; done < blocks; ++u) {
-            const int unit = (g0 + done) / each, us = unit * each, ue = us + each, nb = min(ue, g1) - (g0 + done);
+            const int unit = (g0 + done) / each, us = unit * each, nb = min(us + each, g1) - (g0 + done);
             const int head = unit / P.row_tiles, rt = unit - head * P.row_tiles, rows = min(kRows, P.all_rows - rt * kRows);
-            if (grp == 0) {
+            if (half == 0) {
                 // Q, scaled by a power of two into [2^9, 2^10), its columns in the order of K's rows
                 float top = 0.f;
                 const int row = rt * kRows + r, bt = row / P.group;
                 const uint16_t* src = static_cast<const uint16_t*>(P.q) + bt * P.q_stride + (int64_t)(head * P.group + (row - bt * P.group)) * D;
                 const bool live = r < rows;
-#pragma unroll 4
+#pragma unroll 8
                 for (int k = 0; k < D / 8; ++k) {
                     const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -407,107 +446,99 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             }
             soft_sync();   // the factors
             const float f = factors[r];
-            RowSum A{-INFINITY, 0.f, 0.f};
-            for (int j = (done & 1) == grp ? 0 : 1; j < nb; j += 2) {
-                const int i = done + j;
-                wait(s_full + 8 * grp, i >> 1);
+            float m = -INFINITY, l = 0.f, ref = 0.f;
+            for (int j = 0; j < nb; ++j) {
+                const int i = done + j, b = i & 1;
+                wait(s_full + 8 * b, i >> 1);
                 tc_fence_after();
-                const uint32_t col = lanes + kColS + kKeys * grp;
-                float x[kKeys];
-                tmem_ld32(col, reinterpret_cast<uint32_t(&)[32]>(x[0]));
-                tmem_ld32(col + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
-                const int left = P.max_len - (g0 + i - us) * kKeys;    // keys of the prefix from the block's first on
-                const uint32_t there = s_there[i & 7];
-                if (left < kKeys || there != (1u << kTiles) - 1u) {
+                const uint32_t col = lanes + kColS + kKeys * b + 64 * half;
+                const int left = P.max_len - (g0 + i - us) * kKeys - 64 * half;   // keys of the prefix from this half's first on
+                const uint32_t there = s_there[0][(2 * i + half) & 15];
+                const bool some = left < 64 || there != (1u << kHalf) - 1u;
+                // 32 scores at a time, read twice (for the maximum and for P): registers are what 27 warps leave
+                auto load = [&](int h, float (&x)[32]) {
+                    tmem_ld32(col + 32 * h, reinterpret_cast<uint32_t(&)[32]>(x));
+                    if (some) {
 #pragma unroll
-                    for (int k = 0; k < kKeys; ++k)
-                        if (k >= left || !(there >> (k / kKvTile) & 1u)) x[k] = -INFINITY;
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * h + k >= left || !(there >> ((32 * h + k) / kKvTile) & 1u)) x[k] = -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    load(h, x);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) mx = fmaxf(fmaxf(mx, x[k]), x[k + 1]);
                 }
-                float mx = x[0];
-#pragma unroll
-                for (int k = 1; k < kKeys; ++k) mx = fmaxf(mx, x[k]);
                 mx *= f;
-                const bool move = mx > A.m + kTau;
-                if (__any_sync(0xffffffffu, move)) {
-                    const float now = move ? mx : A.m, a = A.m == now ? 1.f : ex2(A.m - now);
-                    if (j >= 2 && __any_sync(0xffffffffu, A.m != now)) {
-                        // O's last addition was earlier in the MMA thread's order than S, so it is complete
+                if (pair_any(warp & 3, mx > m + kTau)) {
+                    ml[half * kRows + r] = mx;
+                    pair_any(warp & 3, false);
+                    mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
+                    const float now = mx > m + kTau ? mx : m, a = m == now ? 1.f : ex2(m - now);
+                    if (j > 0 && __any_sync(0xffffffffu, m != now)) {   // each thread its half of O's dimensions
+                        wait(o_done, i - 1);
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 32) {
+                        for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
                             uint32_t o[32];
-                            tmem_ld32(lanes + kColO + D * grp + d, o);
+                            tmem_ld32(lanes + kColO + d, o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                            tmem_st32(lanes + kColO + D * grp + d, o);
+                            tmem_st32(lanes + kColO + d, o);
                         }
                     }
-                    A.l *= a;
-                    A.m = now;
-                    A.ref = now == -INFINITY ? 0.f : now - kPBits;
+                    l *= a;
+                    m = now;
+                    ref = now == -INFINITY ? 0.f : now - kPBits;
                 }
-                uint32_t p[kKeys / 2];
-                float l0 = 0.f, l1 = 0.f;
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < kKeys; k += 2) {
-                    const float a = ex2(fmaf(x[k], f, -A.ref)), b = ex2(fmaf(x[k + 1], f, -A.ref));
-                    l0 += a;
-                    l1 += b;
-                    p[k / 2] = pack_half2_rn(a, b);
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    load(h, x);
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 y = fma2(make_float2(x[k], x[k + 1]), make_float2(f, f), make_float2(-ref, -ref));
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum = add2(sum, e);
+                        p[k / 2] = pack_half2_rn(e.x, e.y);
+                    }
+                    tmem_st16(col + 16 * h, p);   // (over scores that have been read)
                 }
-                A.l += l0 + l1;
-                tmem_st32(col, p);
+                l += sum.x + sum.y;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * grp);
+                if (lane == 0) mbar_arrive(p_full + 8 * b);
             }
 
-            // ---- the two groups' sums of the unit: each thread half of its row's dimensions ----
-            ml[grp * kRows + r] = make_float2(A.m, A.l);
+            // ---- the unit's rows: each thread half of its row's dimensions ----
+            soft_sync();   // (the maxima's last readers are done)
+            ml[half * kRows + r] = l;
             soft_sync();
-            const int i1 = done + nb - 1;                              // the unit's last block
-            wait(o_done + 8 * (i1 & 1), i1 >> 1);
-            if (nb > 1) wait(o_done + 8 * ((i1 - 1) & 1), (i1 - 1) >> 1);
+            l = ml[r] + ml[kRows + r];
+            wait(o_done, done + nb - 1);
             tc_fence_after();
-            const float2 e0 = ml[r], e1 = ml[kRows + r];
-            const float top = fmaxf(e0.x, e1.x), ref = top == -INFINITY ? 0.f : top;
-            const float f0 = ex2(e0.x - ref), f1 = ex2(e1.x - ref), l = e0.y * f0 + e1.y * f1;
-            const bool has0 = nb > 1 || (done & 1) == 0, has1 = nb > 1 || (done & 1) == 1;
-            const bool all_here = us >= g0 && ue <= g1;
-            float* slot = P.part + (2 * c + (us >= g0 ? 1 : 0)) * (int64_t)(kRows * (D + 2));
-            const RowOut<D, T> out(P, rt * kRows + min(r, rows - 1), head, top, l, all_here && grp == 0 && r < rows);
+            // into this block's slot of the unit: the second run joins the slots
+            float* slot = P.pre_o + (2 * c + (us >= g0 ? 1 : 0)) * (int64_t)(kRows * (D + 2));
+            if (half == 0 && r < rows) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m, l);
 #pragma unroll 1
-            for (int d = grp * (D / 2); d < (grp + 1) * (D / 2); d += 32) {
-                uint32_t a[32], b[32];
+            for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                uint32_t a[32];
                 tmem_ld32(lanes + kColO + d, a);
-                tmem_ld32(lanes + kColO + D + d, b);
                 if (r < rows) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)                    // (V is held times 2^-1)
-                            v[i] = 2.f * ((has0 ? __uint_as_float(a[k + i]) * f0 : 0.f) + (has1 ? __uint_as_float(b[k + i]) * f1 : 0.f));
-                        if (all_here) out.store(P, d + k, v);
-                        else *reinterpret_cast<float4*>(slot + r * D + d + k) = make_float4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-            }
-            if (!all_here) {
-                if (grp == 0 && r < rows) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(top, l);
-                auto block_of = [&](int at) { return at < rem * (q + 1) ? at / (q + 1) : rem + (at - rem * (q + 1)) / q; };
-                const int c0 = block_of(us), c1 = block_of(ue - 1);
-                __threadfence();
-                soft_sync();
-                if (tid == 0) s_last = atomicAdd(P.counters + unit, 1u) == (unsigned)(c1 - c0);
-                soft_sync();
-                if (s_last) {
-                    __threadfence();
-                    join<D, kRows, kSoftWarps, T>(P, c0, c1, warp, lane, rows, rt * kRows, head);
-                    if (tid == 0) P.counters[unit] = 0;
+                    for (int k = 0; k < 32; k += 4)   // (V is held times 2^-1)
+                        *reinterpret_cast<float4*>(slot + r * D + d + k) =
+                            make_float4(2.f * __uint_as_float(a[k]), 2.f * __uint_as_float(a[k + 1]), 2.f * __uint_as_float(a[k + 2]),
+                                        2.f * __uint_as_float(a[k + 3]));
                 }
             }
             tc_fence_before();
-            soft_sync();   // both groups are done with O, the factors and the sums
+            soft_sync();   // both halves are done with O, the factors and the sums
             done += nb;
         }
     }
@@ -518,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 }
 
 template <int BITS, int D, class T>
-lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream_t stream) {
+lq_status run(lq_handle h, const AttnParams& P, cudaStream_t stream) {
     using M = PreSmem<BITS, D>;
     static std::mutex mu;
     static std::vector<int> ready;   // per device: the shared-memory attribute is set
@@ -532,14 +563,8 @@ lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream
             ready[h->device] = 1;
         }
     }
-    P.row_tiles = (P.all_rows + kRows - 1) / kRows;
-    const int64_t units = (int64_t)P.cache.kv_heads * P.row_tiles, total = units * ((P.max_len + kKeys - 1) / kKeys);
-    if (total > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
-    const int blocks = (int)std::min<int64_t>(h->num_sms, total);
-    if ((size_t)units > h->num_counters || (size_t)blocks * 2 * kRows * (D + 2) * sizeof(float) > room) return LQ_ERR_WORKSPACE;
-    P.part = reinterpret_cast<float*>(scratch);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.gridDim = dim3(P.pre_blocks, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = M::kSize;
     cfg.stream = stream;
@@ -551,17 +576,32 @@ lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream
     return cudaLaunchKernelEx(&cfg, prefix_kernel<BITS, D, T>, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
 }
 
+// Key blocks of all units, and the thread blocks that share them.
+int64_t key_blocks(int kv_heads, int all_rows, int prefix_len) {
+    return (int64_t)kv_heads * ((all_rows + kRows - 1) / kRows) * ((prefix_len + kKeys - 1) / kKeys);
+}
+
 }  // namespace
 
-bool prefix_tc_takes(int rows, int prefix_len) { return rows >= 64 && prefix_len >= 256; }
+size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D) {
+    const int64_t n = key_blocks(kv_heads, all_rows, prefix_len);
+    if (all_rows < 64 || prefix_len < 256 || n > 0x7fffffffLL) return 0;
+    return (size_t)std::min<int64_t>(h->num_sms, n) * 2 * kRows * (D + 2) * sizeof(float);
+}
 
-lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
+lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf16, char* scratch, cudaStream_t stream) {
+    P.pre_o = reinterpret_cast<float*>(scratch);
+    P.pre_rows = kRows;
+    P.row_tiles = P.pre_tiles = (P.all_rows + kRows - 1) / kRows;
+    P.pre_each = (P.max_len + kKeys - 1) / kKeys;
+    P.pre_total = (int)key_blocks(P.cache.kv_heads, P.all_rows, P.max_len);
+    P.pre_blocks = std::min(h->num_sms, P.pre_total);
     if (D == 128) {
-        if (bits == 4) return bf16 ? run<4, 128, __nv_bfloat16>(h, P, scratch, room, stream) : run<4, 128, __half>(h, P, scratch, room, stream);
-        return bf16 ? run<8, 128, __nv_bfloat16>(h, P, scratch, room, stream) : run<8, 128, __half>(h, P, scratch, room, stream);
+        if (bits == 4) return bf16 ? run<4, 128, __nv_bfloat16>(h, P, stream) : run<4, 128, __half>(h, P, stream);
+        return bf16 ? run<8, 128, __nv_bfloat16>(h, P, stream) : run<8, 128, __half>(h, P, stream);
     }
-    if (bits == 4) return bf16 ? run<4, 64, __nv_bfloat16>(h, P, scratch, room, stream) : run<4, 64, __half>(h, P, scratch, room, stream);
-    return bf16 ? run<8, 64, __nv_bfloat16>(h, P, scratch, room, stream) : run<8, 64, __half>(h, P, scratch, room, stream);
+    if (bits == 4) return bf16 ? run<4, 64, __nv_bfloat16>(h, P, stream) : run<4, 64, __half>(h, P, stream);
+    return bf16 ? run<8, 64, __nv_bfloat16>(h, P, stream) : run<8, 64, __half>(h, P, stream);
 }
 
 }  // namespace lq
