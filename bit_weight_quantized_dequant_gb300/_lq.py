@@ -178,6 +178,12 @@ def _dtype_code(t) -> int:
 
 
 @functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
+
+
+@functools.lru_cache(maxsize=None)
 def _code(dtype) -> int:
     import torch
     codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -254,6 +260,12 @@ class KVCache:
             pages.shape[0], page_size, kv_heads, head_dim, bits
         self._c = lq_kv_cache(pages.data_ptr(), self.num_pages, page_size, kv_heads, head_dim, bits)
         self._ref = ctypes.byref(self._c)
+        self._device = pages.get_device()
+
+    def _on(self, device):
+        if self._device != device:
+            raise ValueError(f"the cache must be on cuda:{device}")
+        return self._ref
 
 
 class Handle:
@@ -267,6 +279,7 @@ class Handle:
             raise LQError(st, "lq_create")
         self._h = h
         self.device = device
+        self._device = f"cuda:{device}"
 
     def close(self):
         if getattr(self, "_h", None):
@@ -371,39 +384,34 @@ class Handle:
             raise LQError(st, "lq_selftest_wait")
 
     # ---- rotary positions, the low-bit KV cache and attention over it ----
+    # (A decode step calls these once per layer: their checks are few and cheap.)
 
-    def _out(self, stream, shape, dtype, device):
-        """A result on the current stream's allocator, kept until `stream` (when another) is done with it."""
-        import torch
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            t.record_stream(stream)
-        return t
+    def _raw(self, stream, *made):
+        """The raw stream of a call; results made here on the current stream's allocator are kept until
+        `stream`, when it is another, is done with them."""
+        if stream is None:
+            return _torch()._C._cuda_getCurrentRawStream(self.device)
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
 
-    def _raw(self, stream):
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else int(stream.cuda_stream)
-
-    def _rows(self, name, t, heads, dim, dtype=None):
-        """Token stride of a [n][heads][dim] operand of this device."""
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (dtype is not None and t.dtype != dtype):
-            raise ValueError(f"{name} must be [n][{heads}][{dim}]" + (f" of {dtype}" if dtype is not None else ""))
-        st = t.stride()
-        if (st[2] != 1 or (st[1] != dim and heads > 1)) and t.numel():
+    def _rows(self, name, t, n, heads, dim, dtype):
+        """Token stride of a [n][heads][dim] operand of this device, heads and dimensions contiguous."""
+        if t.shape != (n, heads, dim) or t.dtype is not dtype or t.get_device() != self.device:
+            raise ValueError(f"{name} must be [{n}][{heads}][{dim}] of {dtype} on cuda:{self.device}")
+        s = t.stride()
+        if (s[2] != 1 or (s[1] != dim and heads > 1)) and n:
             raise ValueError(f"{name}'s heads and dimensions must be contiguous")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name} must be on cuda:{self.device}")
-        return st[0] if t.shape[0] > 1 else heads * dim
+        return s[0] if n > 1 else heads * dim
 
     def _indices(self, name, t, dtype, n):
-        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or \
-                t.get_device() != self.device:
+        if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self.device:
             raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype} on cuda:{self.device}")
         return t.data_ptr()
 
     def _table(self, table):
-        import torch
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or \
+        if table.dtype is not _torch().float32 or table.dim() != 2 or not table.is_contiguous() or \
                 table.get_device() != self.device:
             raise ValueError(f"table must be a contiguous fp32 [rows][rot_dim] tensor on cuda:{self.device}")
         return table.data_ptr()
@@ -412,13 +420,13 @@ class Handle:
                    high_rotations=32.0, mscale=1.0, out=None, stream=None):
         """Rows first .. first + count - 1 of the rotation table, fp32 [count][rot_dim]: cosines, then
         sines.  factor stretches the positions: every frequency (original_length 0) or by parts."""
-        import torch
+        torch, made = _torch(), None
         if out is None:
-            out = self._out(stream, (count, rot_dim), torch.float32, torch.device("cuda", self.device))
-        elif tuple(out.shape) != (count, rot_dim):
+            out = made = torch.empty((count, rot_dim), dtype=torch.float32, device=self._device)
+        elif out.shape != (count, rot_dim):
             raise ValueError(f"out must be [{count}][{rot_dim}]")
         c = lq_rope_config(rot_dim, base, factor, original_length, low_rotations, high_rotations, mscale)
-        st = self._lib.lq_rope_table(self._h, ctypes.byref(c), first, count, self._table(out), self._raw(stream))
+        st = self._lib.lq_rope_table(self._h, ctypes.byref(c), first, count, self._table(out), self._raw(stream, made))
         if st != LQ_OK:
             raise LQError(st, "lq_rope_table")
         return out
@@ -426,23 +434,23 @@ class Handle:
     def rope(self, x, positions, table, layout=ROPE_HALF, inverse=False, out=None, stream=None):
         """Rotate the first table.shape[1] dimensions of x [n][heads][dim] (any token and head stride) by
         its int32 positions' table rows; inverse=True applies the transpose (the gradient)."""
-        import torch
-        n, heads, dim = x.shape
+        torch, made = _torch(), None
+        n, heads, dim = shape = x.shape
         if out is None:
-            out = self._out(stream, (n, heads, dim), x.dtype, x.device)
-        elif out.shape != x.shape or out.dtype != x.dtype:
-            raise ValueError("out must have x's shape and dtype")
+            out = made = torch.empty(shape, dtype=x.dtype, device=x.device)
+        elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != self.device:
+            raise ValueError(f"out must have x's shape and dtype on cuda:{self.device}")
         xs, ys = x.stride(), out.stride()
         if (xs[2] != 1 or ys[2] != 1) and dim > 1:
             raise ValueError("dimensions must be contiguous")
-        if x.get_device() != self.device or out.get_device() != self.device:
-            raise ValueError(f"x and out must be on cuda:{self.device}")
-        a = lq_rope_args(x.data_ptr(), out.data_ptr(), _code(x.dtype), n, heads, dim, table.shape[1], xs[0], xs[1], ys[0],
-                         ys[1], self._table(table), table.shape[0], self._indices("positions", positions, torch.int32, n),
-                         layout, bool(inverse))
+        if x.get_device() != self.device:
+            raise ValueError(f"x must be on cuda:{self.device}")
+        rows, rot = table.shape
+        a = lq_rope_args(x.data_ptr(), out.data_ptr(), _code(x.dtype), n, heads, dim, rot, xs[0], xs[1], ys[0], ys[1],
+                         self._table(table), rows, self._indices("positions", positions, torch.int32, n), layout, inverse)
         if n == 0:
             return out
-        st = self._lib.lq_rope(self._h, ctypes.byref(a), self._raw(stream))
+        st = self._lib.lq_rope(self._h, ctypes.byref(a), self._raw(stream, made))
         if st != LQ_OK:
             raise LQError(st, "lq_rope")
         return out
@@ -451,23 +459,20 @@ class Handle:
                   stream=None):
         """Quantise k and v [n][kv_heads][dim] into the cache's int64 slots (negative: skipped).  With a
         table, k is rotated first, and so is q [n][q_heads][dim] when given, into the returned tensor."""
-        import torch
-        dt, n, dim = k.dtype, k.shape[0], cache.head_dim
-        ks, vs = self._rows("k", k, cache.kv_heads, dim), self._rows("v", v, cache.kv_heads, dim, dt)
-        if v.shape[0] != n:
-            raise ValueError("k and v must have the same tokens")
-        qp = op = None
-        hq = qs = os = 0
+        torch, made = _torch(), None
+        dt, n, dim, hkv = k.dtype, k.shape[0], cache.head_dim, cache.kv_heads
+        ks, vs = self._rows("k", k, n, hkv, dim, dt), self._rows("v", v, n, hkv, dim, dt)
+        qp = op = tp = pp = None
+        hq = qs = os = rows = rot = 0
         if q is not None:
             hq = q.shape[1]
+            qs = self._rows("q", q, n, hq, dim, dt)
             if q_out is None:
-                q_out = self._out(stream, (n, hq, dim), dt, q.device)
-            qs, os = self._rows("q", q, hq, dim, dt), self._rows("q_out", q_out, hq, dim, dt)
-            if q.shape[0] != n or q_out.shape[0] != n:
-                raise ValueError("q and q_out must have k's tokens")
+                q_out = made = torch.empty((n, hq, dim), dtype=dt, device=q.device)
+                os = hq * dim
+            else:
+                os = self._rows("q_out", q_out, n, hq, dim, dt)
             qp, op = q.data_ptr(), q_out.data_ptr()
-        tp = pp = None
-        rows = rot = 0
         if table is not None:
             rows, rot = table.shape
             tp, pp = self._table(table), self._indices("positions", positions, torch.int32, n)
@@ -475,21 +480,22 @@ class Handle:
                               self._indices("slots", slots, torch.int64, n), tp, rows, pp, rot, layout)
         if n == 0:
             return q_out
-        st = self._lib.lq_kv_append(self._h, cache._ref, ctypes.byref(a), self._raw(stream))
+        st = self._lib.lq_kv_append(self._h, cache._on(self.device), ctypes.byref(a), self._raw(stream, made))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_append")
         return q_out
 
     def kv_read(self, cache: KVCache, slots, dtype=None, stream=None):
         """The cached keys and values of int64 slots [n], dense [n][kv_heads][dim] (default bfloat16)."""
-        import torch
+        torch = _torch()
         dt, n = dtype or torch.bfloat16, slots.shape[0]
-        shape = (n, cache.kv_heads, cache.head_dim)
-        k, v = self._out(stream, shape, dt, slots.device), self._out(stream, shape, dt, slots.device)
+        shape, dev = (n, cache.kv_heads, cache.head_dim), slots.device
+        k, v = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
         sp = self._indices("slots", slots, torch.int64, n)
         if n == 0:
             return k, v
-        st = self._lib.lq_kv_read(self._h, cache._ref, sp, n, k.data_ptr(), v.data_ptr(), _code(dt), self._raw(stream))
+        st = self._lib.lq_kv_read(self._h, cache._on(self.device), sp, n, k.data_ptr(), v.data_ptr(), _code(dt),
+                                  self._raw(stream, k, v))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_read")
         return k, v
@@ -500,42 +506,48 @@ class Handle:
         over the cache: request b's own tokens in the pages block_table[b] (int32), lens[b] (int32) of
         them, after the prefix_len tokens of prefix_table's pages, which all requests share.  Returns
         out (q's shape and dtype) and the fp32 log-sum-exp [batch][tokens][q_heads]."""
-        import torch
-        B, T, hq, dim = q.shape
-        qs, dt = q.stride(), q.dtype
-        if out is None:
-            out = self._out(stream, (B, T, hq, dim), dt, q.device)
-        if lse is None:
-            lse = self._out(stream, (B, T, hq), torch.float32, q.device)
-        os = out.stride()
-        if dim != cache.head_dim or out.shape != q.shape or out.dtype != dt or lse.shape != q.shape[:3]:
-            raise ValueError(f"q and out must be [batch][tokens][heads][{cache.head_dim}] of one dtype, lse [batch][tokens][heads]")
-        for name, s in (("q", qs), ("out", os)):
+        torch, dev, mo, ml = _torch(), self.device, None, None
+        B, T, hq, dim = shape = q.shape
+        dt, row = q.dtype, hq * dim
+
+        def token_stride(name, t):
+            if t.shape != shape or t.dtype is not dt or t.get_device() != dev or dim != cache.head_dim:
+                raise ValueError(f"q and out must be [batch][tokens][heads][{cache.head_dim}] of one dtype on cuda:{dev}")
+            s = t.stride()
             if s[3] != 1 or (s[2] != dim and hq > 1) or (B > 1 and T > 1 and s[0] != T * s[1]):
                 raise ValueError(f"{name} must be rows of contiguous heads with one token stride")
-        if lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse must be contiguous fp32")
-        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
-                (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+            return s[1] if T > 1 else s[0] if B > 1 else row
+
+        qs = token_stride("q", q)
+        if out is None:
+            out = mo = torch.empty(shape, dtype=dt, device=q.device)
+            os = row
+        else:
+            os = token_stride("out", out)
+        if lse is None:
+            lse = ml = torch.empty((B, T, hq), dtype=torch.float32, device=q.device)
+        elif lse.shape != (B, T, hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError(f"lse must be contiguous fp32 [batch][tokens][heads] on cuda:{dev}")
+        if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.get_device() != dev:
+            raise ValueError(f"block_table must be int32 [{B}][pages] on cuda:{dev}")
+        rows, pages = block_table.shape
+        bs = block_table.stride()
+        if rows != B or (bs[1] != 1 and pages > 1):
             raise ValueError(f"block_table must be int32 [{B}][pages], rows contiguous")
-        dev = self.device
-        if q.get_device() != dev or out.get_device() != dev or lse.get_device() != dev or block_table.get_device() != dev:
-            raise ValueError(f"q, out, lse and block_table must be on cuda:{dev}")
-        pages = block_table.shape[1]
         pp = None
         if prefix_table is not None:
-            pp = self._indices("prefix_table", prefix_table, torch.int32, prefix_table.shape[0])
-            room = prefix_table.shape[0] * cache.page_size
-            prefix_len = room if prefix_len is None else prefix_len
-            if prefix_len > room:
+            n = prefix_table.shape[0]
+            pp = self._indices("prefix_table", prefix_table, torch.int32, n)
+            room = n * cache.page_size
+            if prefix_len is None:
+                prefix_len = room
+            elif prefix_len > room:
                 raise ValueError("prefix_table has too few pages for prefix_len")
-        a = lq_kv_attention_args(q.data_ptr(), out.data_ptr(), lse.data_ptr(), _code(dt), B, T, hq,
-                                 qs[1] if T > 1 else (qs[0] if B > 1 else hq * dim),
-                                 os[1] if T > 1 else (os[0] if B > 1 else hq * dim), block_table.data_ptr(),
-                                 block_table.stride(0) if B > 1 else pages, pages,
+        a = lq_kv_attention_args(q.data_ptr(), out.data_ptr(), lse.data_ptr(), _code(dt), B, T, hq, qs, os,
+                                 block_table.data_ptr(), bs[0] if B > 1 else pages, pages,
                                  self._indices("lens", lens, torch.int32, B), pp, prefix_len or 0,
                                  dim ** -0.5 if scale is None else scale)
-        st = self._lib.lq_kv_attention(self._h, cache._ref, ctypes.byref(a), self._raw(stream))
+        st = self._lib.lq_kv_attention(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream, mo, ml))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_attention")
         return out, lse

@@ -388,8 +388,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
     const int c = blockIdx.x, C = gridDim.x;
     const bool pieces = (int64_t)cum[P.requests].y * per <= C;
     // (a share counts kUnitCost tiles before each unit's own, for what a unit costs a block besides them)
-    const int total = (cum[P.requests].x + kUnitCost * P.requests) * per, q = total / C, rem = total - q * C;
-    auto last = [&](auto start, int at) {             // last request b with per * start(b) <= at
+    const int total = (cum[P.requests].x + kUnitCost * P.requests) * per;
+    const int q = (int)(((uint64_t)(uint32_t)total * P.grid_inverse) >> 42), rem = total - q * C;   // (total / C)
+    // last request b with per * start(b) <= at: for the warp together, and for each lane its own
+    auto last = [&](auto start, int at) {
+        int lo = 0;
+        for (int step = P.requests > 32 ? 32 : 1; step; step = step == 32 ? 1 : 0) {
+            const int i = lo + step * lane;
+            const uint32_t in = __ballot_sync(0xffffffffu, i < P.requests && start(min(i, P.requests - 1)) * per <= at);
+            lo += step * (31 - __clz((int)in));
+        }
+        return lo;
+    };
+    auto last_lane = [&](auto start, int at) {
         int lo = 0, hi = P.requests - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -398,13 +409,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         }
         return lo;
     };
-    auto request_of = [&](int gt) { return last([&](int i) { return cum[i].x; }, gt); };
+    auto tiles_to = [&](int i) { return cum[i].x; };
     auto costly = [&](int i) { return cum[i].x + kUnitCost * i; };
     auto block_of = [&](int at) { return at < rem * (q + 1) ? at / (q + 1) : rem + (at - rem * (q + 1)) / q; };
     auto tile_at = [&](int at) {                      // first tile at or after a place of the shares' sequence
         if (at >= total) return cum[P.requests].x * per;
         const int i = last(costly, at), tiles = cum[i + 1].x - cum[i].x, in = at - costly(i) * per;
-        const int u = in / (tiles + kUnitCost);
+        const int u = quick_div(in, tiles + kUnitCost);
         return cum[i].x * per + u * tiles + max(0, in - u * (tiles + kUnitCost) - kUnitCost);
     };
     int g0, g1, b, unit, piece = 0, of = 1;
@@ -412,18 +423,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         if (c >= cum[P.requests].y * per) return;
         b = last([&](int i) { return cum[i].y; }, c);
         of = cum[b + 1].y - cum[b].y;
-        unit = (c - cum[b].y * per) / of;
+        unit = quick_div(c - cum[b].y * per, of);
         piece = c - cum[b].y * per - unit * of;
         const int each = cum[b + 1].x - cum[b].x, us = cum[b].x * per + unit * each;
-        const int pq = each / of, pr = each - pq * of;
+        const int pq = quick_div(each, of), pr = each - pq * of;
         g0 = us + pq * piece + min(piece, pr);
         g1 = us + pq * (piece + 1) + min(piece + 1, pr);
     } else {
         g0 = tile_at(q * c + min(c, rem));
         g1 = tile_at(q * (c + 1) + min(c + 1, rem));
         if (g0 >= g1) return;
-        b = request_of(g0);
-        unit = (g0 - cum[b].x * per) / (cum[b + 1].x - cum[b].x);
+        b = last(tiles_to, g0);
+        unit = quick_div(g0 - cum[b].x * per, cum[b + 1].x - cum[b].x);
     }
 
     // ---- this warp's tiles: 32 addresses at a time, one per lane, issued S ahead ----
@@ -439,11 +450,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
             const int gt = g0 + warp + kWarps * (issued + lane);
             src = nullptr;
             if (gt < g1) {
-                const int bb = pieces ? b : request_of(gt);
+                const int bb = pieces ? b : last_lane(tiles_to, gt);
                 const int in = gt - cum[bb].x * per, each = cum[bb + 1].x - cum[bb].x;
-                const int u = in / each, tile = in - u * each, head = u / P.row_tiles;
+                const int u = quick_div(in, each), tile = in - u * each, head = P.row_tiles == 1 ? u : u / P.row_tiles;
                 if (tile * kKvTile < len_of(bb)) {
-                    const int pi = tile / P.cache.tiles_per_page;
+                    const int pi = P.page_shift >= 0 ? tile >> P.page_shift : tile / P.cache.tiles_per_page;
                     const int page = __ldg(P.block_table + bb * P.bt_stride + pi);
                     if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
                     else
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
 #pragma unroll 1
     for (;;) {
         const int us = first + unit * each, ue = us + each;
-        const int head = unit / P.row_tiles, rt = unit - head * P.row_tiles;
+        const int head = P.row_tiles == 1 ? unit : unit / P.row_tiles, rt = unit - head * P.row_tiles;
         const int rows = min(R, P.rows - rt * R);                    // live rows of this unit
         const int row0 = b * P.rows + rt * R;
         const int len = len_of(b);
@@ -576,7 +587,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
                 v[i] = (a[0] + a[R * M::kPitch]) + (a[2 * R * M::kPitch] + a[3 * R * M::kPitch]);
             }
             if (all_here) {
-                RowOut<D, T>(P, row0 + r, head, total_ml[r].x, total_ml[r].y, lane == 0).store(P, V * lane, v);
+                finish_row<D, T>(P, row0 + r, head, total_ml[r].x, total_ml[r].y, v, lane);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) slot[r * D + V * lane + i] = v[i];
@@ -588,12 +599,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
             const int from = costly(b) * per + unit * (each + kUnitCost) + kUnitCost;
             const int c0 = pieces ? c - piece : block_of(from), c1 = pieces ? c0 + of - 1 : block_of(from + each - 1);
             unsigned* count = P.counters + (int64_t)b * per + unit;
-            __threadfence();
             __syncthreads();
-            if (tid == 0) s_last = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
+            // (release of what the block wrote before the barrier, acquire of what the others did)
+            if (tid == 0) s_last = arrive_gpu(count) == (unsigned)(c1 - c0);
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 join<D, R, kWarps, T>(P, c0, c1, warp, lane, rows, row0, head);
                 if (tid == 0) *count = 0;
             }
@@ -647,6 +657,8 @@ lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream
     // (tile indices are 32-bit)
     if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     P.part = reinterpret_cast<float*>(scratch);
+    if (blocks > 1024 || (int64_t)P.cache.kv_heads * P.row_tiles >= (1 << 20)) return LQ_ERR_UNSUPPORTED;
+    P.grid_inverse = ((uint64_t)1 << 42) / blocks + 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks, 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
@@ -681,6 +693,9 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
     P.status = h->status_flag;
     if ((int64_t)a.batch * a.tokens * P.group > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     P.all_rows = a.batch * a.tokens * P.group;
+    P.page_shift = -1;
+    for (int i = 0; i < 27; ++i)
+        if (P.cache.tiles_per_page == 1 << i) P.page_shift = i;
     // workspace: what the prefix run leaves, then partial sums
     char* ws = reinterpret_cast<char*>(h->partials);
     const size_t cap = h->partial_floats * sizeof(float), rows = (size_t)c.kv_heads * P.all_rows;

@@ -12,6 +12,7 @@ namespace lq {
 
 constexpr float kTau = 3.f;      // a row's reference moves when a score passes it by 2^3
 constexpr float kPBits = 11.f;   // P = 2^11 p
+constexpr int kPreUnitCost = 6;  // what a unit costs a block of the prefix kernel, in its key blocks
 
 struct AttnParams {
     KvView cache;
@@ -23,18 +24,28 @@ struct AttnParams {
     int requests, rows;                  // units' outer count and rows of each per kv head
     int tokens, group, q_heads;
     int max_len, row_tiles;
+    int page_shift;                      // log2 of the tiles of a page, -1 when that is not whole
+    uint64_t grid_inverse;               // 2^42 / blocks, rounded up: n * this >> 42 is n / blocks for n < 2^31, blocks <= 1024
     float scale_log2;                    // scale * log2(e)
     float* part;                         // partial sums: 2 slots per block
     unsigned* counters;                  // one per unit, zero between calls
     // The prefix run's sums, which the second run joins with its own.  As records: normalised rows [kv_heads]
     // [rows of all requests][D] and their reference; as slots (pre_rows > 0): the prefix kernel's partial sums,
-    // two slots of pre_rows rows per block, blocks sharing pre_total key blocks evenly, pre_each per unit.
+    // two slots of pre_rows rows per block, pre_blocks blocks sharing pre_total places evenly: for each unit
+    // kPreUnitCost places for what it costs a block besides its key blocks, then pre_each key blocks.
     float *pre_o, *pre_m;
     int pre_rows, pre_tiles, pre_each, pre_total, pre_blocks;
     int all_rows;                        // rows of all requests per kv head
     int prefix;                          // 0: none, 1: this is the prefix run, 2: join the prefix's rows
     int* status;
 };
+
+// n / d for a quotient below 2^20 (n, d > 0): a reciprocal and one correction.
+__device__ __forceinline__ int quick_div(int n, int d) {
+    int q = __float2int_rz(__fdividef((float)n, (float)d));
+    const int r = n - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
 
 // n things shared out to c parties in order, the first n % c of them one more: the first of party k, and
 // the party of thing i.
@@ -64,6 +75,11 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ unsigned arrive_gpu(unsigned* count) {
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
+    return old;
+}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -96,134 +112,142 @@ __device__ __forceinline__ float elem_to_float<__half>(uint16_t bits) { return h
 template <>
 __device__ __forceinline__ float elem_to_float<__nv_bfloat16>(uint16_t bits) { return bf16_bits_to_float(bits); }
 
-// Where a row's result goes, and what joins it there: out = (v 2^(m - top) + sum of the prefix's parts) / total.
-template <int D, class T>
-struct RowOut {
-    T* out;
-    float own, top, inv;
-    // the prefix's parts of this row: sums at part + k * stride (the first `lead` floats further), their
-    // (reference, sum of P) the same way from ml
-    const float *part, *ml;
-    int64_t stride;
-    int parts, lead;
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    return v;
+}
 
-    __device__ __forceinline__ const float* at(const float* p, int k) const { return p + (k == 0 ? lead : k * stride); }
-
-    // row: of all requests' rows of a kv head; (m, l): reference and sum of P.  One lane (`writes`)
-    // stores the log-sum-exp.
-    __device__ __forceinline__ RowOut(const AttnParams& P, int row, int head, float m, float l, bool writes) {
-        parts = 0;
-        top = m;
-        const int64_t rec = (int64_t)head * P.all_rows + row;
-        if (P.prefix == 1) {   // a record: normalised, so its sum of P counts as 1
-            own = l == 0.f ? 0.f : 1.f / l;
-            inv = 1.f;
-            out = reinterpret_cast<T*>(P.pre_o + rec * D);
-            if (writes) P.pre_m[rec] = l == 0.f ? -INFINITY : m + log2f(l);
-            return;
-        }
-        if (P.prefix == 2) {
-            if (P.pre_rows) {
-                const int rt = row / P.pre_rows, r = row - rt * P.pre_rows, us = (head * P.pre_tiles + rt) * P.pre_each;
-                const int c0 = share_of(P.pre_total, P.pre_blocks, us), c1 = share_of(P.pre_total, P.pre_blocks, us + P.pre_each - 1);
-                const int slot = P.pre_rows * (D + 2);
-                part = P.pre_o + (int64_t)2 * c0 * slot + r * D;
-                ml = P.pre_o + (int64_t)2 * c0 * slot + P.pre_rows * D + 2 * r;
-                stride = 2 * slot, lead = slot, parts = c1 - c0 + 1;
+// Partial sums of one row, n of them, that a warp joins: V dimensions per lane from part(k), (reference,
+// sum of P) from ml(k), the first 32 in a lane's register each.  B parts' loads are in flight at a time, the
+// first B from the start on.
+template <int V, int B, class Part, class Ml>
+struct RowParts {
+    Part part;
+    Ml ml;
+    int n, lane;
+    float2 mine;   // part `lane`'s reference and sum
+    float f;       // its factor
+    float o[B][V];
+    __device__ __forceinline__ void load(int k0) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const float* a = part(min(k0 + j, n - 1)) + V * lane;
+            if (V == 4) {
+                const float4 e = __ldcg(reinterpret_cast<const float4*>(a));
+                o[j][0] = e.x, o[j][1] = e.y, o[j][V - 2] = e.z, o[j][V - 1] = e.w;
             } else {
-                part = P.pre_o + rec * D;
-                ml = P.pre_m + rec;
-                stride = 0, lead = 0, parts = 1;
+                const float2 e = __ldcg(reinterpret_cast<const float2*>(a));
+                o[j][0] = e.x, o[j][1] = e.y;
             }
-#pragma unroll 4
-            for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(at(ml, k)));
         }
-        const float ref = top == -INFINITY ? 0.f : top;
-        own = ex2(m - ref);
-        float total = l * own;
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float* e = at(ml, k);
-            total = fmaf(P.pre_rows ? __ldcg(e + 1) : 1.f, ex2(__ldcg(e) - ref), total);
-        }
-        top = ref;
-        inv = total == 0.f ? 0.f : 1.f / total;
-        const int bt = row / P.group, qh = head * P.group + (row - bt * P.group);
-        out = static_cast<T*>(P.out) + bt * P.out_stride + (int64_t)qh * D;
-        if (writes && P.lse) P.lse[(int64_t)bt * P.q_heads + qh] = total == 0.f ? -INFINITY : (ref + log2f(total) - kPBits) * 0.6931471805599453f;
     }
-    // V dimensions from d on
-    template <int V>
-    __device__ __forceinline__ void store(const AttnParams& P, int d, float (&v)[V]) const {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= own;
-        if (P.prefix == 1) {
-            float* rec = reinterpret_cast<float*>(out) + d;
-            if (V == 4) *reinterpret_cast<float4*>(rec) = make_float4(v[0], v[1], v[V - 2], v[V - 1]);
-            else *reinterpret_cast<float2*>(rec) = make_float2(v[0], v[1]);
-            return;
+    __device__ __forceinline__ RowParts(int count, int lane_, Part p, Ml m) : part(p), ml(m), n(count), lane(lane_) {
+        mine = lane < n ? ml(lane) : make_float2(-INFINITY, 0.f);
+        load(0);
+    }
+    __device__ __forceinline__ float top() const {
+        float t = mine.x;
+        for (int k = 32 + lane; k < n; k += 32) t = fmaxf(t, ml(k).x);
+        return warp_max(t);
+    }
+    // sums of P relative to `ref`
+    __device__ __forceinline__ float total(float ref) {
+        f = ex2(mine.x - ref);
+        float l = mine.y * f;
+        for (int k = 32 + lane; k < n; k += 32) {
+            const float2 e = ml(k);
+            l = fmaf(e.y, ex2(e.x - ref), l);
         }
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float f = ex2(__ldcg(at(ml, k)) - top);
-            const float* o = at(part, k) + d;
+        return warp_sum(l);
+    }
+    // v += the parts, in order
+    __device__ __forceinline__ void add(float ref, float (&v)[V]) {
+        for (int k0 = 0; k0 < n; k0 += B) {
+            if (k0) load(k0);
+            if (k0 && k0 % 32 == 0) f = k0 + lane < n ? ex2(ml(k0 + lane).x - ref) : 0.f;
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 e = __ldcg(reinterpret_cast<const float2*>(o + i));
-                v[i] = fmaf(e.x, f, v[i]), v[i + 1] = fmaf(e.y, f, v[i + 1]);
+            for (int j = 0; j < B; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, (k0 + j) & 31);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (k0 + j < n) v[i] = fmaf(o[j][i], fj, v[i]);
             }
         }
-        alignas(4 * V) T o[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = (T)(v[i] * inv);
-        if (V == 4) *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(o);
-        else *reinterpret_cast<uint32_t*>(out + d) = *reinterpret_cast<const uint32_t*>(o);
     }
 };
+template <int V, int B, class Part, class Ml>
+__device__ __forceinline__ RowParts<V, B, Part, Ml> row_parts(int n, int lane, Part p, Ml m) { return RowParts<V, B, Part, Ml>(n, lane, p, m); }
 
-// A unit's partial sums of blocks c0 .. c1, joined in block order: a warp per row, D / 32
-// dimensions per lane, the blocks' factors 32 at a time (one per lane).
+// A finished row, by one warp: V dimensions per lane in v, relative to reference m, and sum of P l.  The prefix
+// run leaves a record (normalised, so its sum of P counts as 1); the second run joins the prefix's parts and
+// writes out and the log-sum-exp.  row: of all requests' rows of a kv head.
+template <int D, class T>
+__device__ __forceinline__ void finish_row(const AttnParams& P, int row, int head, float m, float l, float (&v)[D / 32], int lane) {
+    constexpr int V = D / 32;
+    const int64_t rec = (int64_t)head * P.all_rows + row;
+    if (P.prefix == 1) {
+        const float own = l == 0.f ? 0.f : 1.f / l;
+        float* o = P.pre_o + rec * D + V * lane;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) *reinterpret_cast<float2*>(o + i) = make_float2(v[i] * own, v[i + 1] * own);
+        if (lane == 0) P.pre_m[rec] = l == 0.f ? -INFINITY : m + log2f(l);
+        return;
+    }
+    float top = m, total = l;
+    if (P.prefix == 2) {
+        auto join = [&](auto&& parts) {
+            top = fmaxf(m, parts.top());
+            const float ref = top == -INFINITY ? 0.f : top, own = ex2(m - ref);
+            total = fmaf(l, own, parts.total(ref));
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] *= own;
+            parts.add(ref, v);
+        };
+        if (P.pre_rows) {
+            const int rt = row / P.pre_rows, r = row - rt * P.pre_rows, us = (head * P.pre_tiles + rt) * (P.pre_each + kPreUnitCost) + kPreUnitCost;
+            const int c0 = share_of(P.pre_total, P.pre_blocks, us), c1 = share_of(P.pre_total, P.pre_blocks, us + P.pre_each - 1);
+            const int slot = P.pre_rows * (D + 2);
+            // (the first block's slot of the unit is its second, the others' their first)
+            const float* base = P.pre_o + (int64_t)2 * c0 * slot;
+            auto at = [=](int k) { return base + (int64_t)(2 * k + (k == 0 ? 1 : 0)) * slot; };
+            join(row_parts<V, 8>(c1 - c0 + 1, lane, [=](int k) { return at(k) + r * D; },
+                              [=](int k) { return __ldcg(reinterpret_cast<const float2*>(at(k) + (slot / (D + 2)) * D + 2 * r)); }));
+        } else {
+            const float *o = P.pre_o + rec * D, *pm = P.pre_m + rec;
+            join(row_parts<V, 1>(1, lane, [=](int) { return o; }, [=](int) { return make_float2(__ldcg(pm), 1.f); }));
+        }
+    }
+    const int bt = row / P.group, qh = head * P.group + (row - bt * P.group);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    alignas(4 * V) T o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = (T)(v[i] * inv);
+    T* out = static_cast<T*>(P.out) + bt * P.out_stride + (int64_t)qh * D + V * lane;
+    if (V == 4) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+    else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(o);
+    if (lane == 0 && P.lse)
+        P.lse[(int64_t)bt * P.q_heads + qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPBits) * 0.6931471805599453f;
+}
+
+// A unit's partial sums of blocks c0 .. c1, joined in block order: a warp per row.
 template <int D, int R, int kWarps, class T>
 __device__ __forceinline__ void join(const AttnParams& P, int c0, int c1, int warp, int lane, int rows, int row0, int head) {
-    constexpr int V = D / 32;
-    constexpr int kSlot = R * (D + 2);   // (slots of all blocks together: within 32 bits)
-    auto from = [&](int k) { return P.part + (unsigned)(2 * k + (k == c0 ? 1 : 0)) * kSlot; };
+    constexpr int V = D / 32, kSlot = R * (D + 2);   // (slots of all blocks together: within 32 bits)
+    const float* base = P.part + (unsigned)(2 * c0) * kSlot;
     for (int r = warp; r < rows; r += kWarps) {
-        float top = -INFINITY, l = 0.f, v[V] = {};
-        for (int k = c0 + lane; k <= c1; k += 32) top = fmaxf(top, __ldcg(from(k) + R * D + 2 * r));
-        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        const float ref = top == -INFINITY ? 0.f : top;
-        for (int k0 = c0; k0 <= c1; k0 += 32) {
-            const int m = min(32, c1 + 1 - k0);
-            float f = 0.f;
-            if (lane < m) {
-                const float2 e = __ldcg(reinterpret_cast<const float2*>(from(k0 + lane) + R * D + 2 * r));
-                f = ex2(e.x - ref);
-                l = fmaf(e.y, f, l);
-            }
-            // sixteen blocks' values in flight at a time
-            for (int j0 = 0; j0 < m; j0 += 16) {
-                float o[16][V];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float* a = from(k0 + min(j0 + j, m - 1)) + r * D + V * lane;
-#pragma unroll
-                    for (int i = 0; i < V; i += 2) {
-                        const float2 e = __ldcg(reinterpret_cast<const float2*>(a + i));
-                        o[j][i] = e.x, o[j][i + 1] = e.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (j0 + j < m) v[i] = fmaf(o[j][i], fj, v[i]);
-                }
-            }
-        }
-        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-        RowOut<D, T>(P, row0 + r, head, top, l, lane == 0).store(P, V * lane, v);
+        auto at = [=](int k) { return base + (unsigned)(2 * k + (k == 0 ? 1 : 0)) * kSlot; };
+        auto parts = row_parts<V, 16>(c1 - c0 + 1, lane, [=](int k) { return at(k) + r * D; },
+                                  [=](int k) { return __ldcg(reinterpret_cast<const float2*>(at(k) + R * D + 2 * r)); });
+        const float top = parts.top(), ref = top == -INFINITY ? 0.f : top, l = parts.total(ref);
+        float v[V] = {};
+        parts.add(ref, v);
+        finish_row<D, T>(P, row0 + r, head, top, l, v, lane);
     }
 }
 

@@ -15,7 +15,7 @@
 // times 2^-2 and V times 2^-1, so that nothing within the cache's range overflows; V is rounded
 // to binary16 (absolute error 2^-24 below 2^-13).
 //
-// Roles (27 warps): two load keys' and values' bytes by bulk copies, each into a ring of its own
+// Roles (27 warps of 28): two load keys' and values' bytes by bulk copies, each into a ring of its own
 // (values wait for the O before them, keys run two blocks ahead); one issues the MMAs; sixteen expand codes (eight K,
 // eight V, a 16-token tile each); eight do the softmax, two threads per row with half of the keys each,
 // which share the row's reference (one barrier of their two warps per key block tells whether it has
@@ -40,8 +40,16 @@ constexpr int kRows = 128;          // rows of a unit
 constexpr int kKeys = 128;          // keys of a block
 constexpr int kHalf = 4;            // tiles of half a block, which are loaded and expanded together
 constexpr int kSoftWarps = 8, kDqWarps = 16;
-constexpr int kSoft0 = 0, kDq0 = kSoft0 + kSoftWarps, kMmaWarp = kDq0 + kDqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + 2);
+// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those
+// of one scheduler (number mod 4 = 0) issue MMAs, load and expand one tile, so that the MMA warp, whose few
+// instructions feed the tensor cores, shares its scheduler with little; the other three schedulers' expand.
+constexpr int kMmaWarp = 8, kLoadWarp = 12, kDqLast = 20, kWarpsAll = 28;   // (the load warps: 12 and 16)
+constexpr int kThreads = 32 * kWarpsAll;
+__device__ __forceinline__ int dq_index(int warp) {   // which expanding warp, -1: none
+    if (warp < kSoftWarps) return -1;
+    if (warp % 4 == 0) return warp == kDqLast ? kDqWarps - 1 : -1;
+    return (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
+}
 // tensor memory columns
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
@@ -263,14 +271,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
     // this block's key blocks of the sequence of all (kv head, row tile) units' blocks
     const int each = (P.max_len + kKeys - 1) / kKeys;
-    const int total = each * P.cache.kv_heads * P.row_tiles, c = blockIdx.x;
-    const int g0 = share_first(total, gridDim.x, c), g1 = share_first(total, gridDim.x, c + 1), blocks = g1 - g0;
+    const int c = blockIdx.x;
+    auto block_at = [&](int place) {   // first key block at or after a place of the shares' sequence
+        const int u = place / (each + kPreUnitCost), in = place - u * (each + kPreUnitCost);
+        return u * each + max(0, in - kPreUnitCost);
+    };
+    const int g0 = block_at(share_first(P.pre_total, gridDim.x, c)), g1 = block_at(share_first(P.pre_total, gridDim.x, c + 1));
+    const int blocks = g1 - g0;        // (none: nothing to do, and the second run expects nothing)
     int own_abort = 0;
     auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded(bar, parity & 1u, &own_abort, P.status); };
 
-    if (warp >= kLoadWarp) {
+    if (warp == kLoadWarp || warp == kLoadWarp + 4) {
         // ---------------------------------------------------------------- keys' or values' bytes into their ring
-        const int what = warp - kLoadWarp, ring = what ? M::kRawV : M::kRawK, first = what ? M::kRawK : 0;
+        const int what = warp != kLoadWarp, ring = what ? M::kRawV : M::kRawK, first = what ? M::kRawK : 0;
         const uint32_t full = raw_full + 8 * first, empty = raw_empty + 8 * first;
         const uint32_t dst0 = smem_u32(base + M::kRawOff + first * M::kRawStage);
         const uint8_t* src = nullptr;
@@ -352,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             done += nb;
         }
         __syncwarp();
-    } else if (warp >= kDq0) {
+    } else if (dq_index(warp) >= 0) {
         // ---------------------------------------------------------------- codes to operands
-        const int w = warp - kDq0, tile_no = w % kHalf, half = w / kHalf & 1;   // this warp's tile of every block
+        const int w = dq_index(warp), tile_no = w % kHalf, half = w / kHalf & 1;   // this warp's tile of every block
         const bool keys = w < 2 * kHalf;
         const int ring = keys ? M::kRawK : M::kRawV, first = keys ? 0 : M::kRawK, no = half * kHalf + tile_no;
         const uint8_t* raw = base + M::kRawOff + first * M::kRawStage + tile_no * M::kRawTile;
@@ -378,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             s += 2;
             if (s >= ring) s -= ring, ++turn;
         }
-    } else {
+    } else if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax: two threads per row
         const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -455,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 const int left = P.max_len - (g0 + i - us) * kKeys - 64 * half;   // keys of the prefix from this half's first on
                 const uint32_t there = s_there[0][(2 * i + half) & 15];
                 const bool some = left < 64 || there != (1u << kHalf) - 1u;
-                // 32 scores at a time, read twice (for the maximum and for P): registers are what 27 warps leave
+                // 32 scores at a time, read twice (for the maximum and for P): registers are what 28 warps leave
                 auto load = [&](int h, float (&x)[32]) {
                     tmem_ld32(col + 32 * h, reinterpret_cast<uint32_t(&)[32]>(x));
                     if (some) {
@@ -576,15 +589,15 @@ lq_status run(lq_handle h, const AttnParams& P, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, prefix_kernel<BITS, D, T>, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
 }
 
-// Key blocks of all units, and the thread blocks that share them.
-int64_t key_blocks(int kv_heads, int all_rows, int prefix_len) {
-    return (int64_t)kv_heads * ((all_rows + kRows - 1) / kRows) * ((prefix_len + kKeys - 1) / kKeys);
+// Places of all units' key blocks, with each unit's fixed cost before them, which the thread blocks share.
+int64_t key_places(int kv_heads, int all_rows, int prefix_len) {
+    return (int64_t)kv_heads * ((all_rows + kRows - 1) / kRows) * ((prefix_len + kKeys - 1) / kKeys + kPreUnitCost);
 }
 
 }  // namespace
 
 size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D) {
-    const int64_t n = key_blocks(kv_heads, all_rows, prefix_len);
+    const int64_t n = key_places(kv_heads, all_rows, prefix_len);
     if (all_rows < 64 || prefix_len < 256 || n > 0x7fffffffLL) return 0;
     return (size_t)std::min<int64_t>(h->num_sms, n) * 2 * kRows * (D + 2) * sizeof(float);
 }
@@ -594,7 +607,7 @@ lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf1
     P.pre_rows = kRows;
     P.row_tiles = P.pre_tiles = (P.all_rows + kRows - 1) / kRows;
     P.pre_each = (P.max_len + kKeys - 1) / kKeys;
-    P.pre_total = (int)key_blocks(P.cache.kv_heads, P.all_rows, P.max_len);
+    P.pre_total = (int)key_places(P.cache.kv_heads, P.all_rows, P.max_len);
     P.pre_blocks = std::min(h->num_sms, P.pre_total);
     if (D == 128) {
         if (bits == 4) return bf16 ? run<4, 128, __nv_bfloat16>(h, P, stream) : run<4, 128, __half>(h, P, stream);

@@ -20,7 +20,7 @@
 namespace lq {
 namespace {
 
-// ---- 8 values of a row ----------------------------------------------------------------
+// ---- 8 values of a row, as pairs ----------------------------------------------------------
 
 template <class T>
 __device__ __forceinline__ float to_f(T v);
@@ -39,39 +39,68 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+
+// Words of 8 values: pair i in word i (16-bit types) or in words 2 i, 2 i + 1.
 template <class T>
-struct alignas(16) Vec8 {
-    T v[8];
+struct Row8 {
+    uint32_t w[8 * sizeof(T) / 4];
+
+    __device__ __forceinline__ static Row8 load(const T* p) {
+        Row8 r;
+        *reinterpret_cast<uint4*>(r.w) = *reinterpret_cast<const uint4*>(p);
+        if (sizeof(T) == 4) reinterpret_cast<uint4*>(r.w)[sizeof(T) / 4] = reinterpret_cast<const uint4*>(p)[sizeof(T) / 4];
+        return r;
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+        if (sizeof(T) == 4) reinterpret_cast<uint4*>(p)[sizeof(T) / 4] = reinterpret_cast<const uint4*>(w)[sizeof(T) / 4];
+    }
+    __device__ __forceinline__ float2 get(int i) const;
+    __device__ __forceinline__ void set(int i, float2 v);
 };
-
-template <class T>
-__device__ __forceinline__ Vec8<T> load8(const T* p) {
-    Vec8<T> r;
-    if (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(p);
-    } else {
-        reinterpret_cast<uint4*>(&r)[0] = reinterpret_cast<const uint4*>(p)[0];
-        reinterpret_cast<uint4*>(&r)[sizeof(T) / 4] = reinterpret_cast<const uint4*>(p)[sizeof(T) / 4];
-    }
-    return r;
+template <>
+__device__ __forceinline__ float2 Row8<float>::get(int i) const { return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])); }
+template <>
+__device__ __forceinline__ void Row8<float>::set(int i, float2 v) { w[2 * i] = bits(v.x), w[2 * i + 1] = bits(v.y); }
+template <>
+__device__ __forceinline__ float2 Row8<__half>::get(int i) const {
+    return make_float2(half_bits_to_float((uint16_t)w[i]), half_bits_to_float((uint16_t)(w[i] >> 16)));
 }
-template <class T>
-__device__ __forceinline__ void store8(T* p, const Vec8<T>& r) {
-    if (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
-    } else {
-        reinterpret_cast<uint4*>(p)[0] = reinterpret_cast<const uint4*>(&r)[0];
-        reinterpret_cast<uint4*>(p)[sizeof(T) / 4] = reinterpret_cast<const uint4*>(&r)[sizeof(T) / 4];
-    }
+template <>
+__device__ __forceinline__ void Row8<__half>::set(int i, float2 v) { w[i] = pack_half2_rn(v.x, v.y); }
+template <>
+__device__ __forceinline__ float2 Row8<__nv_bfloat16>::get(int i) const {
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ void Row8<__nv_bfloat16>::set(int i, float2 v) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v.y), "f"(v.x));
 }
 
+// Two fp32 operations at a time.  (Not for a product and a sum that are to be rounded each: the assembler
+// makes a packed multiplication and the addition of its product one operation, .rn or not, and the same of
+// a fused operation with -0.  Scalar __fmul_rn and __fadd_rn stay two.)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
 // ---- rotation ---------------------------------------------------------------------------
 
 // The rotation of the 8 dimensions 8 j .. 8 j + 7 that a lane holds: y = x c + p s with p the
 // pair's other member (sign in s), products and sum rounded to fp32 each.  Half layout: pairs
 // (i, i + rot / 2), the other member on the lane `src`; interleaved: pairs (2 i, 2 i + 1).
 struct Turn {
-    float c[8], s[8];
+    float2 c[4], s[4];
     int src;          // lane of the warp with the pairs' other members (half layout)
     bool on, inter;   // whether these dimensions turn at all
 };
@@ -82,7 +111,7 @@ __device__ __forceinline__ Turn turn_for(const float* row, int j, int lane, int 
     u.on = row != nullptr && 8 * j < rot;
     u.src = lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u.c[i] = 1.f, u.s[i] = 0.f;
+    for (int i = 0; i < 4; ++i) u.c[i] = make_float2(1.f, 1.f), u.s[i] = make_float2(0.f, 0.f);
     if (!u.on) return u;
     if (u.inter) {
         const float4 c = *reinterpret_cast<const float4*>(row + 4 * j);
@@ -90,9 +119,8 @@ __device__ __forceinline__ Turn turn_for(const float* row, int j, int lane, int 
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            u.c[2 * i] = u.c[2 * i + 1] = cc[i];
-            u.s[2 * i] = inverse ? ss[i] : -ss[i];
-            u.s[2 * i + 1] = inverse ? -ss[i] : ss[i];
+            u.c[i] = make_float2(cc[i], cc[i]);
+            u.s[i] = inverse ? make_float2(ss[i], -ss[i]) : make_float2(-ss[i], ss[i]);
         }
     } else {
         const int hv = rot / 16;             // vectors of a half
@@ -104,8 +132,8 @@ __device__ __forceinline__ Turn turn_for(const float* row, int j, int lane, int 
         for (int q = 0; q < 2; ++q) {
             const float4 c = *reinterpret_cast<const float4*>(row + i0 + 4 * q);
             const float4 s = *reinterpret_cast<const float4*>(row + rot / 2 + i0 + 4 * q);
-            u.c[4 * q] = c.x, u.c[4 * q + 1] = c.y, u.c[4 * q + 2] = c.z, u.c[4 * q + 3] = c.w;
-            u.s[4 * q] = sign * s.x, u.s[4 * q + 1] = sign * s.y, u.s[4 * q + 2] = sign * s.z, u.s[4 * q + 3] = sign * s.w;
+            u.c[2 * q] = make_float2(c.x, c.y), u.c[2 * q + 1] = make_float2(c.z, c.w);
+            u.s[2 * q] = make_float2(sign * s.x, sign * s.y), u.s[2 * q + 1] = make_float2(sign * s.z, sign * s.w);
         }
     }
     return u;
@@ -113,22 +141,20 @@ __device__ __forceinline__ Turn turn_for(const float* row, int j, int lane, int 
 
 // (All 32 lanes call this together.)
 template <class T>
-__device__ __forceinline__ Vec8<T> turned(const Vec8<T>& x, const Turn& u) {
-    Vec8<T> p = x;
-    if (u.inter) {
+__device__ __forceinline__ Row8<T> turned(const Row8<T>& x, const Turn& u) {
+    Row8<T> p = x;
+    if (!u.inter) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p.v[i] = x.v[i ^ 1];
-    } else {
-        constexpr int W = 8 * sizeof(T) / 4;
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            reinterpret_cast<uint32_t*>(&p)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(&x)[w], u.src);
+        for (int w = 0; w < (int)(8 * sizeof(T) / 4); ++w) p.w[w] = __shfl_sync(0xffffffffu, x.w[w], u.src);
     }
     if (!u.on) return x;
-    Vec8<T> y;
+    Row8<T> y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y.v[i] = from_f<T>(__fadd_rn(__fmul_rn(to_f(x.v[i]), u.c[i]), __fmul_rn(to_f(p.v[i]), u.s[i])));
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = x.get(i), o = u.inter ? make_float2(a.y, a.x) : p.get(i);
+        y.set(i, make_float2(__fadd_rn(__fmul_rn(a.x, u.c[i].x), __fmul_rn(o.x, u.s[i].x)),
+                             __fadd_rn(__fmul_rn(a.y, u.c[i].y), __fmul_rn(o.y, u.s[i].y))));
+    }
     return y;
 }
 
@@ -158,7 +184,7 @@ struct RopeParams {
 
 // blockIdx.x: 256 / lanes neighbouring tokens; blockIdx.y: a chunk of their heads.
 template <class T, int U>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeParams P) {
     pdl_launch_dependents();
     pdl_wait();
     const int j = threadIdx.x & (P.lanes - 1);
@@ -169,18 +195,18 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
     const int h0 = blockIdx.y * P.chunk, h1 = min(P.heads, h0 + P.chunk);
     Turn u;
     for (int hb = h0; hb < h1; hb += U) {   // (uniform over the block: the shuffles need all lanes)
-        Vec8<T> v[U] = {};
+        Row8<T> v[U] = {};
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (live && hb + k < h1) v[k] = load8(x + (hb + k) * P.xh);
+            if (live && hb + k < h1) v[k] = Row8<T>::load(x + (hb + k) * P.xh);
         if (hb == h0) {                     // after the first rows' loads are on their way
             const float* row = n < P.n ? table_row(P.table, P.positions, n, P.rows, P.rot, P.status, j == 0) : nullptr;
             u = turn_for(row, j, threadIdx.x & 31, P.rot, P.layout, P.inverse != 0);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const Vec8<T> r = turned(v[k], u);
-            if (live && hb + k < h1) store8(y + (hb + k) * P.yh, r);
+            const Row8<T> r = turned(v[k], u);
+            if (live && hb + k < h1) r.store(y + (hb + k) * P.yh);
         }
     }
 }
@@ -237,7 +263,7 @@ constexpr int kFine = 32, kCoarse = 16;   // positions of a step, steps of a blo
 // A position is a multiple of kFine (from the block's first) plus the rest: its angle's cosine and
 // sine are the product of two unit numbers, each evaluated as above once per block.  That leaves
 // one evaluation per 11 outputs and two products and two sums each, which the stores hide; direct
-// evaluation was bound by its arithmetic (131072 x 128: 18.7 us, and FIGURE this way).
+// evaluation was bound by its arithmetic (131072 x 128: 18.7 us, and 11.7 this way).
 template <int V>
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableParams P) {
     __shared__ float2 fine[kFine][kMaxRot / 2], coarse[kCoarse][kMaxRot / 2];   // [coarse: times mscale]
@@ -295,6 +321,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
+// (three operands at once)
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 struct AppendParams {
     KvView cache;
     const void *q, *k, *v;
@@ -330,8 +368,8 @@ __device__ __forceinline__ Place place_of(const KvView& c, const int64_t* slots,
 
 // A key or value row's group of 32 is four lanes: its range by two shuffles, its codes by the
 // definition's fp32 operations (correctly rounded each, so the stored bits are one and the same
-// everywhere).  blockIdx.x: neighbouring tokens; blockIdx.y: a chunk of their rows (q heads, then
-// k, then v), the same for the whole block.
+// everywhere).  blockIdx.x: neighbouring tokens; blockIdx.y: a chunk of their rows (k heads, then
+// v, then q: the costlier first), the same for the whole block.
 template <int BITS, int D, class T, int U>
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams P) {
     using L = KvLayout<BITS, D>;
@@ -347,22 +385,22 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     Place at{nullptr, 0, 0};
     Turn u;
     for (int hb = h0; hb < h1; hb += U) {
-        Vec8<T> x[U] = {};
+        Row8<T> x[U] = {};
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int h = hb + k;
             if (live && h < h1) {
-                const T* src = h < hq         ? static_cast<const T*>(P.q) + n * P.qt + h * D
-                               : h < hq + hkv ? static_cast<const T*>(P.k) + n * P.kt + (h - hq) * D
-                                              : static_cast<const T*>(P.v) + n * P.vt + (h - hq - hkv) * D;
-                x[k] = load8(src + 8 * j);
+                const T* src = h < hkv       ? static_cast<const T*>(P.k) + n * P.kt + h * D
+                               : h < 2 * hkv ? static_cast<const T*>(P.v) + n * P.vt + (h - hkv) * D
+                                             : static_cast<const T*>(P.q) + n * P.qt + (h - 2 * hkv) * D;
+                x[k] = Row8<T>::load(src + 8 * j);
             }
         }
         if (hb == h0) {   // after the first rows' loads are on their way
             const float* row = nullptr;
             if (live) {
-                if (h1 > hq) at = place_of(P.cache, P.slots, n, L::kBytes, P.status, j == 0);
-                if (h0 < hq + hkv) row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status, j == 0);
+                if (h0 < 2 * hkv) at = place_of(P.cache, P.slots, n, L::kBytes, P.status, j == 0);
+                if (h0 < hkv || h1 > 2 * hkv) row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status, j == 0);
             }
             u = turn_for(row, j, lane, P.rot, P.layout, false);
         }
@@ -370,41 +408,64 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         for (int k = 0; k < U; ++k) {
             const int h = hb + k;
             if (h >= h1) break;
-            const bool is_v = h >= hq + hkv;
-            Vec8<T> y = is_v ? x[k] : turned(x[k], u);
-            if (h < hq) {
-                if (live) store8(static_cast<T*>(P.q_out) + n * P.ot + h * D + 8 * j, y);
+            const bool is_v = h >= hkv && h < 2 * hkv;
+            const Row8<T> y = is_v ? x[k] : turned(x[k], u);
+            if (h >= 2 * hkv) {
+                if (live) y.store(static_cast<T*>(P.q_out) + n * P.ot + (h - 2 * hkv) * D + 8 * j);
                 continue;
             }
-            float f[8], lo, hi;
+            float2 f[4];
+            float lo = 0.f, hi = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] = max_nan(min_nan(to_f(y.v[i]), 65504.f), -65504.f);
-                lo = i ? min_nan(lo, f[i]) : f[0];
-                hi = i ? max_nan(hi, f[i]) : f[0];
-            }
+            for (int i = 0; i < 4; ++i) f[i] = y.get(i);
+            auto range = [&] {   // of the group: four lanes
+                lo = min_nan(f[0].x, f[0].y), hi = max_nan(f[0].x, f[0].y);
 #pragma unroll
-            for (int s = 1; s <= 2; s <<= 1) {
-                lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-                hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+                for (int i = 1; i < 4; ++i) lo = min_nan(lo, f[i].x, f[i].y), hi = max_nan(hi, f[i].x, f[i].y);
+#pragma unroll
+                for (int s = 1; s <= 2; s <<= 1) {
+                    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+                    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+                }
+            };
+            range();
+            if (__any_sync(0xffffffffu, !(lo >= -65504.f && hi <= 65504.f))) {   // clamped only where it matters
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] = make_float2(max_nan(min_nan(f[i].x, 65504.f), -65504.f), max_nan(min_nan(f[i].y, 65504.f), -65504.f));
+                range();
             }
             const __half S = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / kTop)), Z = __float2half_rn(lo);
             const float s = __half2float(S), z = __half2float(Z);
             // rint of the rounded quotient, without a division per value: a product with 1 / s is off
             // by at most 255 * 2^-22.4 = 4.6e-5, so it has the same nearest whole number unless it lies
-            // within 1e-4 of a half
-            const float inv = __fdiv_rn(1.f, s);
+            // within 1e-4 of a half.  Sums with 1.5 * 2^23 round to it and hold it in their low bits.
+            constexpr float kRound = 12582912.f;
+            const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+            uint32_t c[8];
+            float off = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = add2(f[i], make_float2(-z, -z)), t = fma2(d, make_float2(inv, inv), make_float2(kRound, kRound));
+                const float2 e = fma2(d, make_float2(inv, inv), add2(make_float2(kRound, kRound), make_float2(-t.x, -t.y)));
+                off = max_nan(off, fabsf(e.x), fabsf(e.y));
+                c[2 * i] = bits(fminf(fmaxf(t.x, kRound), kRound + kTop)) & 255u;
+                c[2 * i + 1] = bits(fminf(fmaxf(t.y, kRound), kRound + kTop)) & 255u;
+            }
+            if (!(off <= 0.4999f)) {   // close to a half, or no number
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float r = rintf(__fdiv_rn(__fsub_rn(i & 1 ? f[i >> 1].y : f[i >> 1].x, z), s));
+                    c[i] = s > 0.f ? (uint32_t)fminf(fmaxf(r, 0.f), kTop) : 0u;
+                }
+            }
             uint32_t w[2] = {0u, 0u};   // the row's 8 codes, dimension order
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = __fsub_rn(f[i], z);
-                float r = d * inv, c = rintf(r);
-                if (fabsf(r - c) > 0.4999f) c = rintf(__fdiv_rn(d, s));
-                const uint32_t code = s > 0.f ? (uint32_t)fminf(fmaxf(c, 0.f), kTop) : 0u;
-                if (BITS == 4) w[0] |= code << (4 * i);
-                else w[i >> 2] |= code << (8 * (i & 3));
+                if (BITS == 4) w[0] |= c[i] << (4 * i);
+                else w[i >> 2] |= c[i] << (8 * (i & 3));
             }
-            uint8_t* t = at.tile + (h - hq - (is_v ? hkv : 0)) * at.head_bytes;
+            uint8_t* t = at.tile + (h - (is_v ? hkv : 0)) * at.head_bytes;
             const bool kept = live && at.tile != nullptr;
             const int tok = at.tok;
             if (!is_v) {
@@ -498,22 +559,27 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
                 }
             }
             const float sf = __half2float(s[k]), zf = __half2float(z[k]);
-            Vec8<T> y;
+            Row8<T> y;
+            auto code = [&](int i) {   // 2^23 + code
+                if (BITS == 8) return __uint_as_float(prmt(w[k][i >> 2], 0x4b000000u, 0x7440 + (i & 3)));
+                return __uint_as_float(((w[k][0] >> (4 * i)) & 15u) | 0x4b000000u);
+            };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t c = BITS == 4 ? (w[k][0] >> (4 * i)) & 15u : (w[k][i >> 2] >> (8 * (i & 3))) & 255u;
-                y.v[i] = from_f<T>(__fmaf_rn((float)c, sf, zf));
-            }
-            if (live) store8(static_cast<T*>(is_v ? P.v : P.k) + (n * hkv + (h - (is_v ? hkv : 0))) * D + 8 * j, y);
+            for (int i = 0; i < 4; ++i)
+                y.set(i, fma2(add2(make_float2(code(2 * i), code(2 * i + 1)), make_float2(-8388608.f, -8388608.f)), make_float2(sf, sf),
+                              make_float2(zf, zf)));
+            if (live) y.store(static_cast<T*>(is_v ? P.v : P.k) + (n * hkv + (h - (is_v ? hkv : 0))) * D + 8 * j);
         }
     }
 }
 
-// Rows that one group of lanes walks: as many as leave about 1536 threads for every SM.
+// Rows that one group of lanes walks: one where all rows then still fit the device at once (about 1536
+// threads an SM), otherwise a multiple of the four that are loaded together.
 int rows_per_group(int64_t n, int lanes, int rows, int num_sms) {
     const int64_t groups = std::max<int64_t>(1, (int64_t)num_sms * 1536 / lanes);
     const int chunks = (int)std::min<int64_t>(rows, std::max<int64_t>(1, (groups + n - 1) / n));
-    return (rows + chunks - 1) / chunks;
+    const int each = (rows + chunks - 1) / chunks;
+    return each == 1 ? 1 : (each + 3) / 4 * 4;
 }
 
 // A launch that may begin while the kernel before it ends (it waits before it touches memory).
