@@ -21,7 +21,7 @@
 //           keeps 11 bits down to 2^-27 of the largest.  Sums and statistics are fp32.
 //
 // The grid is persistent: all (request, kv head, row tile) units' 16-token tiles form one
-// sequence, and block c of C takes the range [total c / C, total (c + 1) / C); its 8 warps take
+// sequence, and block c of C takes the range [total c / C, total (c + 1) / C); its warps take
 // that range's tiles in turn, each with its own ring of bulk copies (a tile is one contiguous
 // 1.3 .. 4.6 KB block).  A unit inside one range is finished there; a unit over several leaves
 // partial sums in the workspace, and the block that arrives last joins them in block order
@@ -32,36 +32,40 @@
 // sums join the rows' own at the end of the second run.  Few rows or a short prefix
 // take this kernel for it, many rows the tensor-memory kernel (lq_attn_prefix.cu).
 
-#include <algorithm>
 #include <mutex>
-#include <vector>
 
 #include "lq_attn.cuh"
 
 namespace lq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kUnitCost = 28;    // what a unit costs a block besides its tiles, in tiles
+// Blocks of 8 warps, two on an SM, where units are few and long (fewer partial sums to join); of 4 warps, four
+// on an SM, where there are more units than blocks, so that more of them are in flight: what a unit costs
+// besides its tiles (its queries, the joining of its warps, its output) is latency.  Measured with
+// 64 requests of 50 .. 200 tokens, 40 kv heads, 8 bits: 56 us with 8 warps, 40 with 4; one request of 128 Ki
+// tokens, 8 kv heads, 4 bits: 49 and 59.
+// What a unit costs a block besides its tiles, in tiles:
+template <int W>
+constexpr int kUnitCost = W == 8 ? 28 : 20;
 constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
 // S 2^ks stays at or below kMostS (2^14 times that is finite); ks = 0 where the first tile's largest S lies
 // between the two, so that the multiplication is skipped; otherwise it brings the largest into [1, 2)
 constexpr float kMostS = 3.9f, kLeastS = 0x1p-8f;
 constexpr int kUnset = 99;
 
-template <int BITS, int D, int NT>
+template <int BITS, int D, int NT, int W>
 struct AttnSmem {
     using L = KvLayout<BITS, D>;
     static constexpr int kRows = 8 * NT;
-    // ring stages per warp: what lets two blocks share an SM, 4 at most
+    // ring stages per warp: what lets 16 warps share an SM, 4 at most
     static constexpr int kStages = L::kBytes <= 2560 ? (NT == 1 || D == 64 ? 4 : 3) : 2;
     static constexpr int kPitch = D + 4;                                   // floats of a row of the sums
     static constexpr int kRing = 0;
-    static constexpr int kRed = kRing + kWarps * kStages * L::kBytes;      // 4 x [rows][pitch] fp32
-    static constexpr int kMl = kRed + 4 * kRows * kPitch * 4;              // [warps][rows] m, l
-    static constexpr int kTot = kMl + kWarps * kRows * 8;                  // [rows] m, l of the unit
+    static constexpr int kRed = kRing + W * kStages * L::kBytes;           // W / 2 x [rows][pitch] fp32
+    static constexpr int kMl = kRed + W / 2 * kRows * kPitch * 4;          // [warps][rows] m, l
+    static constexpr int kTot = kMl + W * kRows * 8;                  // [rows] m, l of the unit
     static constexpr int kBars = kTot + kRows * 8;
-    static constexpr int kCum = kBars + kWarps * kStages * 8;              // then [requests + 1] int2
+    static constexpr int kCum = kBars + W * kStages * 8;              // then [requests + 1] int2
 };
 
 // The rows' sums of one warp.
@@ -339,10 +343,11 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
     }
 }
 
-template <int BITS, int D, int NT, class T>
-__global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_constant__ AttnParams P) {
+template <int BITS, int D, int NT, int W, class T>
+__global__ void __launch_bounds__(32 * W, 16 / W) attn_kernel(const __grid_constant__ AttnParams P) {
     using L = KvLayout<BITS, D>;
-    using M = AttnSmem<BITS, D, NT>;
+    using M = AttnSmem<BITS, D, NT, W>;
+    constexpr int kCost = kUnitCost<W>;
     constexpr int R = M::kRows, S = M::kStages, MT = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     float* red = reinterpret_cast<float*>(smem + M::kRed);
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
     pdl_wait();
     auto len_of = [&](int b) { return P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len; };
     // a unit has one tile at least, so that every unit is somebody's
-    for (int b = tid; b < P.requests; b += 32 * kWarps) {
+    for (int b = tid; b < P.requests; b += 32 * W) {
         const int tiles = max(1, (len_of(b) + kKvTile - 1) / kKvTile);
         cum[b + 1] = make_int2(tiles, (tiles + kPiece - 1) / kPiece);
     }
@@ -387,8 +392,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
     const int per = P.cache.kv_heads * P.row_tiles;   // units of a request
     const int c = blockIdx.x, C = gridDim.x;
     const bool pieces = (int64_t)cum[P.requests].y * per <= C;
-    // (a share counts kUnitCost tiles before each unit's own, for what a unit costs a block besides them)
-    const int total = (cum[P.requests].x + kUnitCost * P.requests) * per;
+    // (a share counts kCost tiles before each unit's own, for what a unit costs a block besides them)
+    const int total = (cum[P.requests].x + kCost * P.requests) * per;
     const int q = (int)(((uint64_t)(uint32_t)total * P.grid_inverse) >> 42), rem = total - q * C;   // (total / C)
     // last request b with per * start(b) <= at: for the warp together, and for each lane its own
     auto last = [&](auto start, int at) {
@@ -410,13 +415,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         return lo;
     };
     auto tiles_to = [&](int i) { return cum[i].x; };
-    auto costly = [&](int i) { return cum[i].x + kUnitCost * i; };
+    auto costly = [&](int i) { return cum[i].x + kCost * i; };
     auto block_of = [&](int at) { return at < rem * (q + 1) ? at / (q + 1) : rem + (at - rem * (q + 1)) / q; };
     auto tile_at = [&](int at) {                      // first tile at or after a place of the shares' sequence
         if (at >= total) return cum[P.requests].x * per;
         const int i = last(costly, at), tiles = cum[i + 1].x - cum[i].x, in = at - costly(i) * per;
-        const int u = quick_div(in, tiles + kUnitCost);
-        return cum[i].x * per + u * tiles + max(0, in - u * (tiles + kUnitCost) - kUnitCost);
+        const int u = quick_div(in, tiles + kCost);
+        return cum[i].x * per + u * tiles + max(0, in - u * (tiles + kCost) - kCost);
     };
     int g0, g1, b, unit, piece = 0, of = 1;
     if (pieces) {
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
 
     // ---- this warp's tiles: 32 addresses at a time, one per lane, issued S ahead ----
     const uint32_t ring = smem_u32(smem) + warp * S * L::kBytes;
-    const int mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+    const int mine = g1 - g0 > warp ? (g1 - g0 - warp + W - 1) / W : 0;
     int issued = 0, is = 0;               // tiles issued, the stage of the next
     uint32_t known = 0, there = 0;        // bit per lane: tile in the cache; bit per stage: the same
     const uint8_t* src = nullptr;
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         if (issued >= mine) return;
         const int who = issued & 31;
         if (who == 0) {
-            const int gt = g0 + warp + kWarps * (issued + lane);
+            const int gt = g0 + warp + W * (issued + lane);
             src = nullptr;
             if (gt < g1) {
                 const int bb = pieces ? b : last_lane(tiles_to, gt);
@@ -514,10 +519,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         }
         const int whole = (P.prefix == 1 ? len : len - P.tokens + 1) - kKvTile;   // later tiles: not every row sees all
 
-        const int upto = min(ue, g1) - g0 - warp;   // tiles of this warp: kWarps * done < upto
-        int j0 = (g0 + warp + kWarps * done - us) * kKvTile;
+        const int upto = min(ue, g1) - g0 - warp;   // tiles of this warp: W * done < upto
+        int j0 = (g0 + warp + W * done - us) * kKvTile;
 #pragma unroll 1
-        for (; kWarps * done < upto; ++done, j0 += kWarps * kKvTile) {
+        for (; W * done < upto; ++done, j0 += W * kKvTile) {
             mbar_wait_bounded(bars + 8 * ds, parity, &own_abort, P.status);
             if (there >> ds & 1u) {
                 const uint8_t* tile = smem + (warp * S + ds) * L::kBytes;
@@ -546,15 +551,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
             for (int i = 0; i < 2; ++i) {
                 const int r = 8 * nt + 2 * t + i;
                 float top = -INFINITY, l = 0.f;
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * R + r].x);
+                for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * R + r].x);
                 const float ref = top == -INFINITY ? 0.f : top;
-                for (int w = 0; w < kWarps; ++w) l += ml[w * R + r].y * ex2(ml[w * R + r].x - ref);
+                for (int w = 0; w < W; ++w) l += ml[w * R + r].y * ex2(ml[w * R + r].x - ref);
                 fac[nt][i] = ex2(A.m[nt][i] - ref);
                 if (warp == 0 && n == 0) total_ml[r] = make_float2(top, l);
             }
         const float up = pow2i(24 - (A.ks == kUnset ? 0 : A.ks));
-        auto put = [&](bool add) {   // this warp's rows into (or onto) slot warp % 4
-            float* dst = red + (warp & 3) * R * M::kPitch;
+        auto put = [&](bool add) {   // this warp's rows into (or onto) slot warp % (W / 2)
+            float* dst = red + (warp % (W / 2)) * R * M::kPitch;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -571,20 +576,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
                     }
                 }
         };
-        if (warp >= 4) put(false);
+        if (warp >= W / 2) put(false);
         __syncthreads();
-        if (warp < 4) put(true);
+        if (warp < W / 2) put(true);
         __syncthreads();
 
         const bool all_here = us >= g0 && ue <= g1;
         float* slot = P.part + (2 * c + (us >= g0 ? 1 : 0)) * (int64_t)(R * (D + 2));
         constexpr int V = D / 32;   // a warp per row
-        for (int r = warp; r < rows; r += kWarps) {
+        for (int r = warp; r < rows; r += W) {
             float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float* a = red + r * M::kPitch + V * lane + i;
-                v[i] = (a[0] + a[R * M::kPitch]) + (a[2 * R * M::kPitch] + a[3 * R * M::kPitch]);
+                v[i] = a[0] + a[R * M::kPitch];
+                if (W == 8) v[i] += a[2 * R * M::kPitch] + a[3 * R * M::kPitch];
             }
             if (all_here) {
                 finish_row<D, T>(P, row0 + r, head, total_ml[r].x, total_ml[r].y, v, lane);
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
         if (!all_here) {
             if (tid < rows) *reinterpret_cast<float2*>(slot + R * D + 2 * tid) = total_ml[tid];
             // the blocks that share the unit
-            const int from = costly(b) * per + unit * (each + kUnitCost) + kUnitCost;
+            const int from = costly(b) * per + unit * (each + kCost) + kCost;
             const int c0 = pieces ? c - piece : block_of(from), c1 = pieces ? c0 + of - 1 : block_of(from + each - 1);
             unsigned* count = P.counters + (int64_t)b * per + unit;
             __syncthreads();
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
             if (tid == 0) s_last = arrive_gpu(count) == (unsigned)(c1 - c0);
             __syncthreads();
             if (s_last) {
-                join<D, R, kWarps, T>(P, c0, c1, warp, lane, rows, row0, head);
+                join<D, R, W, T>(P, c0, c1, warp, lane, rows, row0, head);
                 if (tid == 0) *count = 0;
             }
         }
@@ -619,65 +625,61 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_kernel(const __grid_const
     }
 }
 
-// Blocks of a kernel that fit on the device at once (0 on error); sets its shared-memory
-// attribute, which only rises.  Kept per kernel and device.
-template <int BITS, int D, int NT, class T>
-int attn_blocks(int device, int num_sms, int smem) {
-    struct Slot {
-        int smem = 0, most = 0;
-    };
+// Requests that the shared memory of a launch has room for: a few sizes, so that few are ever asked about.
+int cum_room(int requests) { return requests <= 64 ? 64 : requests <= 256 ? 256 : kMaxAttnBatch; }
+
+// Blocks of a kernel that fit on the device at once (0 on error); sets its shared-memory attribute,
+// which only rises.  Kept per kernel, device and size.
+template <int BITS, int D, int NT, int W, class T>
+int attn_blocks(int device, int num_sms, int requests) {
     static std::mutex mu;
-    static std::vector<Slot> slots;
-    std::lock_guard<std::mutex> lock(mu);
-    if ((int)slots.size() <= device) slots.resize(device + 1);
-    Slot& s = slots[device];
-    if (smem > s.most) {
-        if (cudaFuncSetAttribute(attn_kernel<BITS, D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return 0;
-        s.most = smem;
+    static int known[kMaxDevices][3] = {}, most[kMaxDevices] = {};
+    if (device < 0 || device >= kMaxDevices) return 0;
+    const int room = cum_room(requests), smem = AttnSmem<BITS, D, NT, W>::kCum + 8 * (room + 1);
+    const std::lock_guard<std::mutex> lock(mu);
+    int& blocks = known[device][room == 64 ? 0 : room == 256 ? 1 : 2];
+    if (blocks == 0) {
+        if (smem > most[device]) {
+            if (cudaFuncSetAttribute(attn_kernel<BITS, D, NT, W, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return 0;
+            most[device] = smem;
+        }
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<BITS, D, NT, W, T>, 32 * W, smem) != cudaSuccess) return 0;
+        blocks = n * num_sms;
     }
-    static std::vector<std::pair<int, int>> known;   // (shared memory, blocks per SM), the same on every GB300
-    for (const auto& k : known)
-        if (k.first == smem) return k.second * num_sms;
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<BITS, D, NT, T>, 32 * kWarps, smem) != cudaSuccess) return 0;
-    known.push_back({smem, n});
-    return n * num_sms;
+    return blocks;
 }
 
-template <int BITS, int D, int NT, class T>
+template <int BITS, int D, int NT, int W, class T>
 lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream_t stream) {
     constexpr int R = 8 * NT;
     P.row_tiles = (P.rows + R - 1) / R;
-    const int smem = AttnSmem<BITS, D, NT>::kCum + 8 * (P.requests + 1);
-    const int blocks = smem <= h->max_smem_optin ? attn_blocks<BITS, D, NT, T>(h->device, h->num_sms, smem) : 0;
+    const int blocks = attn_blocks<BITS, D, NT, W, T>(h->device, h->num_sms, P.requests);
     if (blocks < 1) return LQ_ERR_CUDA;
     if ((size_t)P.requests * P.cache.kv_heads * P.row_tiles > h->num_counters) return LQ_ERR_WORKSPACE;
     if ((size_t)blocks * 2 * R * (D + 2) * sizeof(float) > room) return LQ_ERR_WORKSPACE;
-    // (tile indices are 32-bit)
-    if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
-    P.part = reinterpret_cast<float*>(scratch);
+    // (tile indices are 32-bit, quotients of units below 2^20)
+    if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost<W>) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     if (blocks > 1024 || (int64_t)P.cache.kv_heads * P.row_tiles >= (1 << 20)) return LQ_ERR_UNSUPPORTED;
+    P.part = reinterpret_cast<float*>(scratch);
     P.grid_inverse = ((uint64_t)1 << 42) / blocks + 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, 1, 1);
-    cfg.blockDim = dim3(32 * kWarps, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kernel<BITS, D, NT, T>, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+    return launch_overlapped(attn_kernel<BITS, D, NT, W, T>, blocks, 32 * W,
+                             AttnSmem<BITS, D, NT, W>::kCum + 8 * (cum_room(P.requests) + 1), stream, P);
+}
+
+template <int BITS, int D, int NT>
+lq_status run_typed(lq_handle h, AttnParams& P, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
+    const int64_t units = (int64_t)P.requests * P.cache.kv_heads * ((P.rows + 8 * NT - 1) / (8 * NT));
+    if (units > 2 * h->num_sms)
+        return bf16 ? run<BITS, D, NT, 4, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, NT, 4, __half>(h, P, scratch, room, stream);
+    return bf16 ? run<BITS, D, NT, 8, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, NT, 8, __half>(h, P, scratch, room, stream);
 }
 
 template <int BITS, int D>
-lq_status run_typed(lq_handle h, AttnParams& P, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
+lq_status run_rows(lq_handle h, AttnParams& P, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
     // one n = 8 tile of rows where 8 hold them, two otherwise (a second tile costs a third more issue slots per key)
-    if (P.rows <= 8)
-        return bf16 ? run<BITS, D, 1, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, 1, __half>(h, P, scratch, room, stream);
-    return bf16 ? run<BITS, D, 2, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, 2, __half>(h, P, scratch, room, stream);
+    return P.rows <= 8 ? run_typed<BITS, D, 1>(h, P, bf16, scratch, room, stream) : run_typed<BITS, D, 2>(h, P, bf16, scratch, room, stream);
 }
 
 }  // namespace
@@ -708,8 +710,8 @@ lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_att
     const bool bf16 = a.dtype == LQ_BF16;
     auto go = [&](AttnParams& p) {
         if (c.head_dim == 128)
-            return c.bits == 4 ? run_typed<4, 128>(h, p, bf16, ws + pre, cap - pre, stream) : run_typed<8, 128>(h, p, bf16, ws + pre, cap - pre, stream);
-        return c.bits == 4 ? run_typed<4, 64>(h, p, bf16, ws + pre, cap - pre, stream) : run_typed<8, 64>(h, p, bf16, ws + pre, cap - pre, stream);
+            return c.bits == 4 ? run_rows<4, 128>(h, p, bf16, ws + pre, cap - pre, stream) : run_rows<8, 128>(h, p, bf16, ws + pre, cap - pre, stream);
+        return c.bits == 4 ? run_rows<4, 64>(h, p, bf16, ws + pre, cap - pre, stream) : run_rows<8, 64>(h, p, bf16, ws + pre, cap - pre, stream);
     };
     if (a.prefix_len > 0) {
         P.prefix = 1;

@@ -10,6 +10,7 @@
 
 namespace lq {
 
+constexpr int kMaxDevices = 64;  // devices whose kernel settings are kept
 constexpr float kTau = 3.f;      // a row's reference moves when a score passes it by 2^3
 constexpr float kPBits = 11.f;   // P = 2^11 p
 constexpr int kPreUnitCost = 6;  // what a unit costs a block of the prefix kernel, in its key blocks

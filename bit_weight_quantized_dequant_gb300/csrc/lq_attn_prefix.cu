@@ -28,7 +28,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <vector>
 
 #include "lq_attn.cuh"
 #include "lq_tcgen05.cuh"
@@ -322,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- all MMAs, one thread
-        const uint32_t lead = lane == 0;
         constexpr uint32_t idS = idesc_f16(false, kRows, kKeys), idO = idesc_f16(false, kRows, D);
         // (descriptors count 16-byte units from their first: a constant each)
         const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
@@ -333,15 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
             wait(k_full + 8 * b, i >> 1);
             tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int st = 0; st < D / 16; ++st)
+                        tc_mma_f16_ts(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS,
+                                      (part | st) != 0);
+                tc_mma_f16_ts(d, tmem + kColZ, zd + 2 * b, idS, 1);
+                tc_commit(s_full + 8 * b);
+            }
             __syncwarp();
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int st = 0; st < D / 16; ++st)
-                    tc_mma_f16_ts(lead, d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16,
-                                  idS, (part | st) != 0);
-            tc_mma_f16_ts(lead, d, tmem + kColZ, zd + 2 * b, idS, 1);
-            tc_commit(lead, s_full + 8 * b);
         };
         int done = 0;   // blocks of earlier units
         for (int u = 0; done < blocks; ++u) {
@@ -355,12 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 wait(v_full, i);
                 wait(p_full + 8 * b, i >> 1);
                 tc_fence_after();
-                __syncwarp();
+                if (lane == 0) {
 #pragma unroll
-                for (int st = 0; st < kKeys / 16; ++st)
-                    tc_mma_f16_ts(lead, tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4),
-                                  vd + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, j != 0 || st != 0);
-                tc_commit(lead, o_done);
+                    for (int st = 0; st < kKeys / 16; ++st)
+                        tc_mma_f16_ts(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4),
+                                      vd + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, j != 0 || st != 0);
+                    tc_commit(o_done);
+                }
+                __syncwarp();
             }
             done += nb;
         }
@@ -565,28 +567,17 @@ template <int BITS, int D, class T>
 lq_status run(lq_handle h, const AttnParams& P, cudaStream_t stream) {
     using M = PreSmem<BITS, D>;
     static std::mutex mu;
-    static std::vector<int> ready;   // per device: the shared-memory attribute is set
+    static bool ready[kMaxDevices] = {};   // the shared-memory attribute is set
+    if (h->device < 0 || h->device >= kMaxDevices || M::kSize > h->max_smem_optin) return LQ_ERR_UNSUPPORTED;
     {
-        std::lock_guard<std::mutex> lock(mu);
-        if ((int)ready.size() <= h->device) ready.resize(h->device + 1, 0);
+        const std::lock_guard<std::mutex> lock(mu);
         if (!ready[h->device]) {
-            if (M::kSize > h->max_smem_optin ||
-                cudaFuncSetAttribute(prefix_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSize) != cudaSuccess)
+            if (cudaFuncSetAttribute(prefix_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSize) != cudaSuccess)
                 return LQ_ERR_CUDA;
-            ready[h->device] = 1;
+            ready[h->device] = true;
         }
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P.pre_blocks, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = M::kSize;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_kernel<BITS, D, T>, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+    return launch_overlapped(prefix_kernel<BITS, D, T>, P.pre_blocks, kThreads, M::kSize, stream, P);
 }
 
 // Places of all units' key blocks, with each unit's fixed cost before them, which the thread blocks share.

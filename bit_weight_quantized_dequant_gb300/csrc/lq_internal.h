@@ -111,6 +111,23 @@ constexpr int kStatusIndex = 4;         // status word: a position, slot or page
 constexpr int kMaxAttnBatch = 1024;     // requests of one attention call
 constexpr int kMaxAttnTokens = 64;      // query tokens of a request
 
+// A launch that may begin while the kernel before it in the stream ends (programmatic dependent launch: the
+// kernel waits, with griddepcontrol.wait, before it touches memory).
+template <class Params>
+lq_status launch_overlapped(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Params& P) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+}
+
 lq_status launch_rope_table(lq_handle h, const lq_rope_config& c, int first, int count, float* table, cudaStream_t stream);
 lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream);
 lq_status launch_kv_append(lq_handle h, const lq_kv_cache& c, const lq_kv_append_args& a, cudaStream_t stream);

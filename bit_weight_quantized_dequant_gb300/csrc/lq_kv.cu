@@ -582,19 +582,9 @@ int rows_per_group(int64_t n, int lanes, int rows, int num_sms) {
     return each == 1 ? 1 : (each + 3) / 4 * 4;
 }
 
-// A launch that may begin while the kernel before it ends (it waits before it touches memory).
 template <class Params>
 lq_status launch(void (*kernel)(Params), dim3 grid, cudaStream_t stream, const Params& P) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? LQ_OK : LQ_ERR_CUDA;
+    return launch_overlapped(kernel, grid, 256, 0, stream, P);
 }
 
 KvView view(const lq_kv_cache& c) {

@@ -57,24 +57,21 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
            | ((uint32_t)(M >> 4) << 24);                    // M / 16
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T on one CTA (M = 128).  A sits in tensor memory with row r in lane r
-// and 16-bit elements 2c, 2c + 1 of the row in column c.  A whole warp runs this and the next with the
-// same operands; the one thread with `lead` issues (the operands then stay in uniform registers).
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A[tmem] * B[smem]^T on one CTA (M = 128), issued by one thread.  A sits in tensor
+// memory with row r in lane r and 16-bit elements 2c, 2c + 1 of the row in column c.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// Arrive on `bar` once every MMA issued so far by the thread with `lead` has completed.
-__device__ __forceinline__ void tc_commit(uint32_t lead, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
-        : "memory");
+// Arrive on `bar` once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
 }
 
 // CTA-pair MMA (M = 256): issued by one thread of the pair's even CTA.  Each CTA holds its
