@@ -96,6 +96,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// What the rounding of a b to p left out, exactly.
+__device__ __forceinline__ uint32_t hmul2_rest(uint32_t a, uint32_t b, uint32_t p) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 m;\n\tneg.f16x2 m, %3;\n\tfma.rn.f16x2 %0, %1, %2, m;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(p));
+    return d;
+}
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -105,6 +111,15 @@ __device__ __forceinline__ float2 unpack2(uint32_t h) {
     return make_float2(half_bits_to_float((uint16_t)h), half_bits_to_float((uint16_t)(h >> 16)));
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+template <class T>
+struct IsHalf {
+    static constexpr bool value = false;
+};
+template <>
+struct IsHalf<__half> {
+    static constexpr bool value = true;
+};
 
 template <class T>
 __device__ __forceinline__ float elem_to_float(uint16_t bits);

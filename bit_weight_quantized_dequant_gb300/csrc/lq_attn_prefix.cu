@@ -79,16 +79,8 @@ struct PreSmem {
     static_assert(kSize <= 227 * 1024 && kBars % 8 == 0 && kRawOff % 128 == 0 && kRawStage % 16 == 0, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return reinterpret_cast<__half2&>(v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return reinterpret_cast<uint32_t&>(v); }
 // Two fp32 values at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     unsigned long long d;
@@ -119,16 +111,19 @@ __device__ __forceinline__ void sts128(uint8_t* p, uint32_t a, uint32_t b, uint3
     *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
 }
 
+// A masked code as a whole number: it stands in the low bits of 1024 (or, 4 bits up, of 64).
+__device__ __forceinline__ __half2 less_1024(uint32_t v) { return __hadd2(as_half2(v | 0x64006400u), as_half2(0xe400e400u)); }
+__device__ __forceinline__ __half2 less_64(uint32_t v) { return __hadd2(as_half2(v | 0x54005400u), as_half2(0xd400d400u)); }
+
 // Whole numbers (binary16 pairs) of a word's codes: 4-bit r = 0..3: nibbles (r, r + 4); 8-bit
 // r = 0, 1: bytes (r, r + 2).
 template <int BITS>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int r) {
+__device__ __forceinline__ __half2 code_pair(uint32_t w, int r) {
     if (BITS == 4) {
         const uint32_t y = r & 2 ? w >> 8 : w;
-        if (r & 1) return hadd2((y & 0x00f000f0u) | 0x54005400u, 0xd400d400u);   // 64 + c, less 64
-        return hadd2((y & 0x000f000fu) | 0x64006400u, 0xe400e400u);              // 1024 + c, less 1024
+        return r & 1 ? less_64(y & 0x00f000f0u) : less_1024(y & 0x000f000fu);
     }
-    return hadd2(prmt(w, 0x64646464u, r ? 0x4341 : 0x4240), 0xe400e400u);
+    return __hadd2(as_half2(prmt(w, 0x64646464u, r ? 0x4341 : 0x4240)), as_half2(0xe400e400u));
 }
 
 // Keys of one tile: [token][dims] rows of the K stage, in the order of the words' pairs (Q's columns
@@ -138,7 +133,10 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
     using L = KvLayout<BITS, D>;
     using M = PreSmem<BITS, D>;
     constexpr int G = D / 32, WK = L::WK, U = WK / G;   // U words of a group (1 or 2)
-    const int n = lane >> 2, t = lane & 3;
+    const int n = lane >> 2, t = lane & 3, odd = n & 1;
+    // Odd tokens take their groups two by two in the other order (below: group st ^ odd at step st), so that
+    // eight lanes write to eight places.
+    const int even_at = ((4 * odd + t) ^ n) << 4, odd_at = ((4 * (odd ^ 1) + t) ^ n) << 4;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         const int tok = n + 8 * hf, row = 16 * tile_no + tok;   // row & 7 == n
@@ -151,32 +149,31 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
             *reinterpret_cast<uint2*>(kw) = lds64(tile + kv_word_at(lane, hf * WK));
         }
         const uint32_t keep = tok < left ? 0xffffffffu : 0u;     // past the end: zeros, whatever lies there
-        uint32_t s[G / 2], z[G / 2];
+        uint32_t s[G / 2], z[G / 2];                             // groups (2 i, 2 i + 1), times 2^-2
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) {
-            s[i] = hmul2(lds32(meta + tok * G * 2 + 4 * i) & keep, 0x34003400u);   // 2^-2
+            const uint32_t v = hmul2(lds32(meta + tok * G * 2 + 4 * i) & keep, 0x34003400u);
+            s[i] = odd ? prmt(v, v, 0x1032) : v;
             z[i] = hmul2(lds32(meta + L::kMeta + tok * G * 2 + 4 * i) & keep, 0x34003400u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t x = kw[U * 2 * i + u], y = kw[U * (2 * i + 1) + u];
+                kw[U * 2 * i + u] = odd ? y : x;
+                kw[U * (2 * i + 1) + u] = odd ? x : y;
+            }
         }
         uint8_t* base = stage + row * 128;
 #pragma unroll
         for (int st = 0; st < G; ++st) {
-            // odd tokens take their groups in the other order, so that eight lanes write to eight places
-            const int g = st ^ (n & 1);
-            const uint32_t pair = s[st >> 1], s2 = prmt(pair, 0, g & 1 ? 0x3232 : 0x1010);
+            const __half2 s2 = st & 1 ? __high2half2(as_half2(s[st >> 1])) : __low2half2(as_half2(s[st >> 1]));
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t w0 = kw[U * st + u], w1 = kw[U * (st ^ 1) + u], w = n & 1 ? w1 : w0;
-#pragma unroll
-                for (int r = 0; r < 4 / U; ++r) {
-                    const uint32_t c = code_pair<BITS>(w, r);
-                    const uint32_t p = hmul2(c, s2);
-                    hi[u * (4 / U) + r] = p;
-                    lo[u * (4 / U) + r] = hfma2(c, s2, p ^ 0x80008000u);   // c S - p, exactly
-                }
+            for (int i = 0; i < 4; ++i) {
+                const __half2 c = code_pair<BITS>(kw[U * st + i / (4 / U)], i % (4 / U)), p = __hmul2(c, s2);
+                hi[i] = as_bits(p);
+                lo[i] = as_bits(__hfma2(c, s2, __hneg2(p)));     // c S - p, exactly
             }
-            const int ch = 4 * g + t;
-            uint8_t* at = base + (ch >> 3) * M::kAtom + (((ch & 7) ^ n) << 4);
+            uint8_t* at = base + (st & 1 ? odd_at : even_at) + (st >> 1) * M::kAtom;
             sts128(at, hi[0], hi[1], hi[2], hi[3]);
             sts128(at + M::kAtoms * M::kAtom, lo[0], lo[1], lo[2], lo[3]);
         }
@@ -200,6 +197,7 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
         *reinterpret_cast<uint4*>(vw + 4 * c) = lds128(tile + 512 * c + 16 * lane);
     const uint32_t keep[2] = {(2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u),
                               (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u)};
+    uint8_t* at[2] = {stage + n * 128 + (((2 * tile_no) ^ n) << 4) + 4 * t, stage + n * 128 + (((2 * tile_no + 1) ^ n) << 4) + 4 * t};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const uint2 sv = lds64(meta + g * 32 + 8 * t), zv = lds64(meta + L::kMeta + g * 32 + 8 * t);
@@ -207,20 +205,19 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
         const uint32_t z[2] = {hmul2(zv.x & keep[0], 0x38003800u), hmul2(zv.y & keep[1], 0x38003800u)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int slab = 4 * g + k, wi = slab % WV, e = slab / WV, d = 8 * slab + n;   // (d & 7 == n)
+            const int slab = 4 * g + k, wi = slab % WV, e = slab / WV;   // dimension 8 slab + n
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint32_t wa = vw[2 * half * WV + wi], wb = vw[(2 * half + 1) * WV + wi];
-                uint32_t c;
+                __half2 c;
                 if (BITS == 4) {
                     const uint32_t y = prmt(wa, wb, e < 4 ? 0x5410 : 0x7632), w = (e & 2) ? y >> 8 : y;
-                    c = (e & 1) ? hadd2((w & 0x00f000f0u) | 0x54005400u, 0xd400d400u)
-                                : hadd2((w & 0x000f000fu) | 0x64006400u, 0xe400e400u);
+                    c = (e & 1) ? less_64(w & 0x00f000f0u) : less_1024(w & 0x000f000fu);
                 } else {
                     const uint32_t y = prmt(wa, wb, e < 2 ? 0x5410 : 0x7632), w = (e & 1) ? y >> 8 : y;
-                    c = hadd2((w & 0x00ff00ffu) | 0x64006400u, 0xe400e400u);
+                    c = less_1024(w & 0x00ff00ffu);
                 }
-                *reinterpret_cast<uint32_t*>(stage + d * 128 + (((2 * tile_no + half) ^ n) << 4) + 4 * t) = hfma2(c, s[half], z[half]);
+                *reinterpret_cast<uint32_t*>(at[half] + slab * 1024) = as_bits(__hfma2(c, as_half2(s[half]), as_half2(z[half])));
             }
         }
     }
