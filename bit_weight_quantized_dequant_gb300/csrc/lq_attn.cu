@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) attn_kernel(const __grid_const
     }
     pdl_launch_dependents();
     pdl_wait();
-    auto len_of = [&](int b) { return P.lens ? min(max(__ldg(P.lens + b), 0), P.max_len) : P.max_len; };
+    auto len_of = [&](int b) { return P.lens ? min(max(P.lens[b], 0), P.max_len) : P.max_len; };
     // a unit has one tile at least, so that every unit is somebody's
     for (int b = tid; b < P.requests; b += 32 * W) {
         const int tiles = max(1, (len_of(b) + kKvTile - 1) / kKvTile);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) attn_kernel(const __grid_const
                 const int u = quick_div(in, each), tile = in - u * each, head = P.row_tiles == 1 ? u : u / P.row_tiles;
                 if (tile * kKvTile < len_of(bb)) {
                     const int pi = P.page_shift >= 0 ? tile >> P.page_shift : tile / P.cache.tiles_per_page;
-                    const int page = __ldg(P.block_table + bb * P.bt_stride + pi);
+                    const int page = P.block_table[bb * P.bt_stride + pi];
                     if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
                     else
                         src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + head) * P.cache.tiles_per_page +

@@ -112,7 +112,8 @@ constexpr int kMaxAttnBatch = 1024;     // requests of one attention call
 constexpr int kMaxAttnTokens = 64;      // query tokens of a request
 
 // A launch that may begin while the kernel before it in the stream ends (programmatic dependent launch: the
-// kernel waits, with griddepcontrol.wait, before it touches memory).
+// kernel waits, with griddepcontrol.wait, before it touches memory).  Such a kernel reads what an earlier one
+// may have written with ordinary loads, not through the read-only path: the data changes while it is resident.
 template <class Params>
 lq_status launch_overlapped(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Params& P) {
     cudaLaunchConfig_t cfg = {};

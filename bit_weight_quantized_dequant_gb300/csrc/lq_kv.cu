@@ -162,7 +162,7 @@ __device__ __forceinline__ Row8<T> turned(const Row8<T>& x, const Turn& u) {
 __device__ __forceinline__ const float* table_row(const float* table, const int* positions, int64_t n, int rows, int rot,
                                                   int* status, bool report) {
     if (!table) return nullptr;
-    const int p = __ldg(positions + n);
+    const int p = positions[n];
     if (p < 0 || p >= rows) {
         if (report) atomicOr(status, kStatusIndex);
         return nullptr;
@@ -354,7 +354,7 @@ struct Place {
     int tok;
 };
 __device__ __forceinline__ Place place_of(const KvView& c, const int64_t* slots, int64_t n, int tile_bytes, int* status, bool report) {
-    const int64_t slot = __ldg(slots + n);
+    const int64_t slot = slots[n];
     Place p{nullptr, (int64_t)c.tiles_per_page * tile_bytes, (int)(slot & 15)};
     const int64_t tile = slot >> 4;   // (pages are whole tiles)
     if (slot < 0 || tile >= c.num_pages * c.tiles_per_page) {
