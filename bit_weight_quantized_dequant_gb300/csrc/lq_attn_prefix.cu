@@ -11,9 +11,11 @@
 //
 // Scores keep fp32 precision.  K's code part S c is the sum of two binary16 values, its rounding
 // and what that left out (one fused multiply-add gives it exactly), each multiplied; its offset
-// part is one more MMA of 16 columns, Z by the group sums of q in two binary16 terms.  K is held
-// times 2^-2 and V times 2^-1, so that nothing within the cache's range overflows; V is rounded
-// to binary16 (absolute error 2^-24 below 2^-13).
+// part is one more MMA of 16 columns, Z by the group sums of q in two binary16 terms.  V is rounded
+// to binary16 (absolute error 2^-25 below 2^-14).  A group that spans all of binary16's range (clamped
+// infinities) has terms past its end.  They are clamped, two instructions per pair of keys' terms and
+// one per pair of values (3 us of 107); a branch around them cost 5, and scaling S down instead
+// costs it bits where it is small.
 //
 // Roles (27 warps of 28): two load keys' and values' bytes by bulk copies, each into a ring of its own
 // (values wait for the O before them, keys run two blocks ahead); one issues the MMAs; sixteen expand codes (eight K,
@@ -126,6 +128,9 @@ __device__ __forceinline__ __half2 code_pair(uint32_t w, int r) {
     return __hadd2(as_half2(prmt(w, 0x64646464u, r ? 0x4341 : 0x4240)), as_half2(0xe400e400u));
 }
 
+// Not past the end of binary16's range (NaN stays).
+__device__ __forceinline__ __half2 clamp_top(__half2 v) { return __hmin2_nan(v, __float2half2_rn(65504.f)); }
+
 // Keys of one tile: [token][dims] rows of the K stage, in the order of the words' pairs (Q's columns
 // follow it), and Z.  left: tokens of the prefix from the tile's first on.
 template <int BITS, int D>
@@ -149,12 +154,12 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
             *reinterpret_cast<uint2*>(kw) = lds64(tile + kv_word_at(lane, hf * WK));
         }
         const uint32_t keep = tok < left ? 0xffffffffu : 0u;     // past the end: zeros, whatever lies there
-        uint32_t s[G / 2], z[G / 2];                             // groups (2 i, 2 i + 1), times 2^-2
+        uint32_t s[G / 2], z[G / 2];                             // groups (2 i, 2 i + 1)
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) {
-            const uint32_t v = hmul2(lds32(meta + tok * G * 2 + 4 * i) & keep, 0x34003400u);
+            const uint32_t v = lds32(meta + tok * G * 2 + 4 * i) & keep;
             s[i] = odd ? prmt(v, v, 0x1032) : v;
-            z[i] = hmul2(lds32(meta + L::kMeta + tok * G * 2 + 4 * i) & keep, 0x34003400u);
+            z[i] = lds32(meta + L::kMeta + tok * G * 2 + 4 * i) & keep;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t x = kw[U * 2 * i + u], y = kw[U * (2 * i + 1) + u];
@@ -169,9 +174,9 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2 c = code_pair<BITS>(kw[U * st + i / (4 / U)], i % (4 / U)), p = __hmul2(c, s2);
+                const __half2 c = code_pair<BITS>(kw[U * st + i / (4 / U)], i % (4 / U)), p = clamp_top(__hmul2(c, s2));
                 hi[i] = as_bits(p);
-                lo[i] = as_bits(__hfma2(c, s2, __hneg2(p)));     // c S - p, exactly
+                lo[i] = as_bits(clamp_top(__hfma2(c, s2, __hneg2(p))));     // c S - p, exactly (unless p was clamped)
             }
             uint8_t* at = base + (st & 1 ? odd_at : even_at) + (st >> 1) * M::kAtom;
             sts128(at, hi[0], hi[1], hi[2], hi[3]);
@@ -201,8 +206,7 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const uint2 sv = lds64(meta + g * 32 + 8 * t), zv = lds64(meta + L::kMeta + g * 32 + 8 * t);
-        const uint32_t s[2] = {hmul2(sv.x & keep[0], 0x38003800u), hmul2(sv.y & keep[1], 0x38003800u)};   // 2^-1
-        const uint32_t z[2] = {hmul2(zv.x & keep[0], 0x38003800u), hmul2(zv.y & keep[1], 0x38003800u)};
+        const uint32_t s[2] = {sv.x & keep[0], sv.y & keep[1]}, z[2] = {zv.x & keep[0], zv.y & keep[1]};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int slab = 4 * g + k, wi = slab % WV, e = slab / WV;   // dimension 8 slab + n
@@ -217,7 +221,8 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
                     const uint32_t y = prmt(wa, wb, e < 2 ? 0x5410 : 0x7632), w = (e & 1) ? y >> 8 : y;
                     c = less_1024(w & 0x00ff00ffu);
                 }
-                *reinterpret_cast<uint32_t*>(at[half] + slab * 1024) = as_bits(__hfma2(c, as_half2(s[half]), as_half2(z[half])));
+                const __half2 v = clamp_top(__hfma2(c, as_half2(s[half]), as_half2(z[half])));   // (S rounded up may pass it)
+                *reinterpret_cast<uint32_t*>(at[half] + slab * 1024) = as_bits(v);
             }
         }
     }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     const int unit = gb / each, head = unit / P.row_tiles;
                     const int tile = (gb - unit * each) * 2 * kHalf + lane % (2 * kHalf);
                     if (tile * kKvTile < P.max_len) {
-                        const int pi = tile / P.cache.tiles_per_page, page = __ldg(P.block_table + pi);
+                        const int pi = tile / P.cache.tiles_per_page, page = P.block_table[pi];
                         if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
                         else
                             src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + head) * P.cache.tiles_per_page +
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 int e = top > 0.f ? 9 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
                 e = min(max(e, -120), 120);
                 const float up = pow2i(e);
-                factors[r] = P.scale_log2 * pow2i(-e) * 4.f;           // (K is held times 2^-2)
+                factors[r] = P.scale_log2 * pow2i(-e);
                 uint32_t z[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -543,10 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 tmem_ld32(lanes + kColO + d, a);
                 if (r < rows) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)   // (V is held times 2^-1)
-                        *reinterpret_cast<float4*>(slot + r * D + d + k) =
-                            make_float4(2.f * __uint_as_float(a[k]), 2.f * __uint_as_float(a[k + 1]), 2.f * __uint_as_float(a[k + 2]),
-                                        2.f * __uint_as_float(a[k + 3]));
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4*>(slot + r * D + d + k) = make_uint4(a[k], a[k + 1], a[k + 2], a[k + 3]);
                 }
             }
             tc_fence_before();

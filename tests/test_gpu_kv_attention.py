@@ -165,6 +165,40 @@ def test_shared_prefix_many_rows(lqm, handle, bits, B, T, hq, hkv, prefix):
     c.check(*c.run(handle), requests=list(g.integers(0, B, 6)) + [0, B - 1])
 
 
+@pytest.mark.parametrize("bits,D", SHAPES)
+@pytest.mark.parametrize("spread,vscale,mult", [(0.01, 1.0, 100.0), (1e-4, 1.0, 1e4), (1.0, 0.02, 1.0), (1.0, 2e-3, 1.0),
+                                               (3000.0, 3000.0, 1e-3)])
+def test_shared_prefix_scales_far_from_one(lqm, handle, bits, D, spread, vscale, mult):
+    """Small keys under large queries (scales of the keys down to binary16's subnormals), small and large values."""
+    c = Case(lqm, [5] * 20, hq=8, hkv=2, D=D, bits=bits, prefix=600, spread=spread, vscale=vscale, seed=17, page=48)
+    c.q = (c.q.float() * mult).to(torch.bfloat16)
+    c.check(*c.run(handle), requests=[0, 7, 19])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_shared_prefix_groups_that_span_the_range(lqm, handle, bits):
+    """Keys and values of which a group holds both infinities (clamped when cached): the dense product stays finite."""
+    hkv, D, n, B = 1, 128, 320, 70
+    cache = lqm.KVCache(num_pages=n // 64 + B, page_size=64, kv_heads=hkv, head_dim=D, bits=bits)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(n, hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k[9, 0, 32], k[9, 0, 40], v[77, 0, 0], v[77, 0, 1] = float("inf"), -float("inf"), -float("inf"), float("inf")
+    at = torch.arange(n, device="cuda")
+    handle.kv_append(cache, k, v, at)
+    q = torch.randn(B, 1, 1, D, generator=g, device="cuda").bfloat16() * 1e-4
+    bt = torch.arange(n // 64, n // 64 + B, device="cuda", dtype=torch.int32)[:, None]
+    out, lse = handle.kv_attention(q, cache, bt, torch.zeros(B, dtype=torch.int32, device="cuda"),
+                                   prefix_table=torch.arange(n // 64, device="cuda", dtype=torch.int32), prefix_len=n)
+    kk, vv = handle.kv_read(cache, at, dtype=torch.float32)
+    kk, vv = kk[:, 0].cpu().numpy(), vv[:, 0].cpu().numpy()
+    for b in (0, 35, 69):
+        o, s, mass, size = R.attend(q[b].float().cpu().numpy(), kk, vv, [n], D ** -0.5)
+        # the group's keys are c S / 2 twice, each rounded by 2^-11: an error of 2^-11 of its share of the score
+        tol = 2.0 ** -11 * size[0] * D ** -0.5 + 2.0 ** -19
+        assert abs(float(lse[b, 0, 0]) - s[0, 0]) <= tol
+        assert np.all(np.abs(out[b, 0].float().cpu().numpy() - o[0]) <= (2.0 ** -10 + 2 * tol) * mass[0] + 2.0 ** -8 * np.abs(o[0]) + 2.0 ** -11 * 65504 / n)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("B", [33, 200, 1024])
 def test_many_requests(lqm, handle, bits, B):
