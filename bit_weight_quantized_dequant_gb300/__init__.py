@@ -8,6 +8,9 @@ Weight formats (see ``include/lq.h``):
   * 2-bit Lloyd-Max codes, group 32, binary16 scale/offset, binary16 anchor columns
     (otf-llm 4.0.1 README, sections 2-4);
   * NF4, block 64, fp32 absmax (AirQuant README, NF4 block-wise).
+
+Attention block: ``Handle.rope_table``, ``rope``, ``kv_append``, ``kv_read`` and
+``kv_attention`` over a paged ``KVCache`` in 4 or 8 bits.
 """
 from __future__ import annotations
 

@@ -31,6 +31,12 @@
 // A shared prefix runs first, with every request's rows as one unit list over the prefix pages; its
 // sums join the rows' own at the end of the second run.  Few rows or a short prefix
 // take this kernel for it, many rows the tensor-memory kernel (lq_attn_prefix.cu).
+//
+// Measured (128 dimensions, bf16): 24 requests of 1 .. 4001 tokens, 40 heads, 8 bits: 577 MB in 95 us,
+// 6.1 TB/s of a copy's 6.7.  One request of 128 Ki tokens, 64 query heads over 8, 4 bits: 168 MB in 49 us;
+// there the loop runs at 5.4 to 5.6 TB/s (ALU pipe 53 %, issue 54 %: 390 instructions per tile and warp),
+// and 3 us of start and 8 us from the last tile to the joined output come on top.  333 tokens, 32 heads:
+// 8.7 us, all latency.
 
 #include <mutex>
 

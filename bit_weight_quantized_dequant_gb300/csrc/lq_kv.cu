@@ -7,6 +7,11 @@
 // and written once.  A group of lanes stays with its token, whose cosines and sines it holds in
 // registers, and walks a chunk of its rows, four loads at a time; neighbouring groups have
 // neighbouring tokens, which lie in the same cache tiles.
+//
+// Measured (from a graph): rotation of 2048 x 40 x 128 bf16, 43 MB in 8.5 us, 5.1 TB/s; in f16, 1111 x 64 x
+// 64 of which 32 rotate, strided rows, 4.0 us.  Rotation, 8-bit cache write and reading back of
+// 2048 tokens, 64 query and 8 kv heads: 94 MB in 24.4 us, where the append is bound by its instructions
+// (issue 66 %, 21 per value: each product and sum of a rotation is rounded by itself).
 
 #include <math.h>
 #include <string.h>
