@@ -50,9 +50,15 @@ namespace {
 // besides its tiles (its queries, the joining of its warps, its output) is latency.  Measured with
 // 64 requests of 50 .. 200 tokens, 40 kv heads, 8 bits: 56 us with 8 warps, 40 with 4; one request of 128 Ki
 // tokens, 8 kv heads, 4 bits: 49 and 59.
-// What a unit costs a block besides its tiles, in tiles:
+// What a unit costs a block besides its tiles, in tiles (16 requests of 100 .. 4000 tokens, 8 kv heads, 16 rows: 37.3
+// us with 28 for 8 warps, 35.1 with 40; 26.0 and 27.5 for 24 requests of 8 rows with 40 and 60):
 template <int W>
-constexpr int kUnitCost = W == 8 ? 28 : 20;
+constexpr int kUnitCost = W == 8 ? 40 : 20;
+// Warps that share an SM's registers: 16, with 128 each.  16 rows of 128 dimensions do not fit that (600 bytes a
+// thread spilled): 8, with 255.  Measured with 16 rows: 64 Ki tokens, 8 kv heads, 4 bits, 62.9 us with 16 warps and
+// 40.5 with 8; in 8 bits 70.8 and 41.7.  8 rows and 64 dimensions: 32.3 with 16, 38.1 with 8.
+template <int D, int NT>
+constexpr int kWarpsPerSm = NT == 2 && D == 128 ? 8 : 16;
 constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
 // S 2^ks stays at or below kMostS (2^14 times that is finite); ks = 0 where the first tile's largest S lies
 // between the two, so that the multiplication is skipped; otherwise it brings the largest into [1, 2)
@@ -63,7 +69,7 @@ template <int BITS, int D, int NT, int W>
 struct AttnSmem {
     using L = KvLayout<BITS, D>;
     static constexpr int kRows = 8 * NT;
-    // ring stages per warp: what lets 16 warps share an SM, 4 at most
+    // ring stages per warp: what lets 16 warps share an SM, 4 at most (8 warps gain nothing from more)
     static constexpr int kStages = L::kBytes <= 2560 ? (NT == 1 || D == 64 ? 4 : 3) : 2;
     static constexpr int kPitch = D + 4;                                   // floats of a row of the sums
     static constexpr int kRing = 0;
@@ -361,7 +367,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
 }
 
 template <int BITS, int D, int NT, int W, class T>
-__global__ void __launch_bounds__(32 * W, 16 / W) attn_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(const __grid_constant__ AttnParams P) {
     using L = KvLayout<BITS, D>;
     using M = AttnSmem<BITS, D, NT, W>;
     constexpr int kCost = kUnitCost<W>;
