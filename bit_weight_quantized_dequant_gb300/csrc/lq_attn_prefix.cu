@@ -591,12 +591,15 @@ int64_t key_places(int kv_heads, int all_rows, int prefix_len) {
 
 }  // namespace
 
-// Taken from 32 rows per kv head and 512 shared tokens on.  Measured (whole call, 8 kv heads of 128 dimensions, 4 bits; this
-// kernel and the other, us): 32 rows over 256 / 1000 / 16000 tokens 15.1, 16.0 / 16.4, 20.7 / 29.9, 33.4; 64 rows
-// 17.4, 16.2 / 18.4, 21.0 / 31.0, 46.7; 128 rows 20.9, 16.5 / 20.9, 24.5 / 34.2, 71.8.  8 bits: the same within 10 %.
+// Taken from 17 rows per kv head (where the other kernel reads the prefix once per 16 rows) and 385 shared tokens
+// on (where the other cuts a unit into pieces and joins them).  Measured (whole call, 128 dimensions, 4 bits; this
+// kernel and the other, us), 8 kv heads over 256 / 1000 / 16000 tokens: 20 rows, 1000 and 16000: 15.2, 20.3 / 28.0,
+// 32.7; 32 rows 15.1, 16.0 / 16.4, 20.7 / 29.9, 33.4; 64 rows 17.4, 16.2 / 18.4, 21.0 / 31.0, 46.7; 128 rows 20.9,
+// 16.5 / 20.9, 24.5 / 34.2, 71.8.  16 rows: 15.0, 20.2 over 1000 tokens with 8 heads, but 29.3, 27.9 over 16000 and
+// 64.9, 51.5 with 32 heads.  8 bits: the same within 10 %.
 size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D) {
     const int64_t n = key_places(kv_heads, all_rows, prefix_len);
-    if (all_rows < 32 || prefix_len < 512 || n > 0x7fffffffLL) return 0;
+    if (all_rows <= 16 || prefix_len <= 384 || n > 0x7fffffffLL) return 0;
     return (size_t)std::min<int64_t>(h->num_sms, n) * 2 * kRows * (D + 2) * sizeof(float);
 }
 

@@ -538,8 +538,8 @@ LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t
  *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
  * over kv head h / (q_heads / kv_heads) and these keys j, in 32-bit statistics:
  *   - the prefix_len tokens of the pages prefix_table[], which all requests share: their
- *     part is computed once for all requests' rows together (from 32 rows per kv head and
- *     512 tokens on as a dense product whose values are rounded to binary16);
+ *     part is computed once for all requests' rows together (from 17 rows per kv head and
+ *     385 tokens on as a dense product whose values are rounded to binary16);
  *   - the request's own tokens j < lens[b] - tokens + 1 + t (lens counts the query tokens,
  *     which are in the cache already), token j in slot block_table[b][j / page_size] *
  *     page_size + j % page_size.
