@@ -6,6 +6,7 @@
 
 #include "lq_internal.h"
 #include "lq_kv.cuh"
+#include "lq_share.h"
 #include "lq_tma.cuh"
 
 namespace lq {
@@ -13,7 +14,6 @@ namespace lq {
 constexpr int kMaxDevices = 64;  // devices whose kernel settings are kept
 constexpr float kTau = 3.f;      // a row's reference moves when a score passes it by 2^3
 constexpr float kPBits = 11.f;   // P = 2^11 p
-constexpr int kPreUnitCost = 6;  // what a unit costs a block of the prefix kernel, in its key blocks
 
 struct AttnParams {
     KvView cache;
@@ -32,10 +32,9 @@ struct AttnParams {
     unsigned* counters;                  // one per unit, zero between calls
     // The prefix run's sums, which the second run joins with its own.  As records: normalised rows [kv_heads]
     // [rows of all requests][D] and their reference; as slots (pre_rows > 0): the prefix kernel's partial sums,
-    // two slots of pre_rows rows per block, pre_blocks blocks sharing pre_total places evenly: for each unit
-    // kPreUnitCost places for what it costs a block besides its key blocks, then pre_each key blocks.
+    // pre_slots slots of pre_rows rows per block, pre_blocks blocks sharing pre_total places evenly (lq_share.h).
     float *pre_o, *pre_m;
-    int pre_rows, pre_tiles, pre_each, pre_total, pre_blocks;
+    int pre_rows, pre_tiles, pre_each, pre_total, pre_blocks, pre_slots;
     int all_rows;                        // rows of all requests per kv head
     int prefix;                          // 0: none, 1: this is the prefix run, 2: join the prefix's rows
     int* status;
@@ -46,14 +45,6 @@ __device__ __forceinline__ int quick_div(int n, int d) {
     int q = __float2int_rz(__fdividef((float)n, (float)d));
     const int r = n - q * d;
     return r < 0 ? q - 1 : r >= d ? q + 1 : q;
-}
-
-// n things shared out to c parties in order, the first n % c of them one more: the first of party k, and
-// the party of thing i.
-__device__ __forceinline__ int share_first(int n, int c, int k) { return n / c * k + min(k, n % c); }
-__device__ __forceinline__ int share_of(int n, int c, int i) {
-    const int q = n / c, rem = n % c;
-    return i < rem * (q + 1) ? i / (q + 1) : rem + (i - rem * (q + 1)) / q;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -226,12 +217,12 @@ __device__ __forceinline__ void finish_row(const AttnParams& P, int row, int hea
             parts.add(ref, v);
         };
         if (P.pre_rows) {
-            const int rt = row / P.pre_rows, r = row - rt * P.pre_rows, us = (head * P.pre_tiles + rt) * (P.pre_each + kPreUnitCost) + kPreUnitCost;
-            const int c0 = share_of(P.pre_total, P.pre_blocks, us), c1 = share_of(P.pre_total, P.pre_blocks, us + P.pre_each - 1);
-            const int slot = P.pre_rows * (D + 2);
-            // (the first block's slot of the unit is its second, the others' their first)
-            const float* base = P.pre_o + (int64_t)2 * c0 * slot;
-            auto at = [=](int k) { return base + (int64_t)(2 * k + (k == 0 ? 1 : 0)) * slot; };
+            const int rt = row / P.pre_rows, r = row - rt * P.pre_rows, unit = head * P.pre_tiles + rt;
+            const Shares shares(P.pre_total, P.pre_blocks);
+            const int us = prefix_unit_place(P.pre_each, unit), c0 = shares.of(us), c1 = shares.of(us + P.pre_each - 1);
+            const int slot = P.pre_rows * (D + 2), s0 = prefix_slot(shares, P.pre_each, c0, unit);
+            // (every later block of the unit starts with it)
+            auto at = [=](int k) { return P.pre_o + (int64_t)((c0 + k) * P.pre_slots + (k == 0 ? s0 : 0)) * slot; };
             join(row_parts<V, 8>(c1 - c0 + 1, lane, [=](int k) { return at(k) + r * D; },
                               [=](int k) { return __ldcg(reinterpret_cast<const float2*>(at(k) + (slot / (D + 2)) * D + 2 * r)); }));
         } else {

@@ -277,11 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     // this block's key blocks of the sequence of all (kv head, row tile) units' blocks
     const int each = (P.max_len + kKeys - 1) / kKeys;
     const int c = blockIdx.x;
-    auto block_at = [&](int place) {   // first key block at or after a place of the shares' sequence
-        const int u = place / (each + kPreUnitCost), in = place - u * (each + kPreUnitCost);
-        return u * each + max(0, in - kPreUnitCost);
-    };
-    const int g0 = block_at(share_first(P.pre_total, gridDim.x, c)), g1 = block_at(share_first(P.pre_total, gridDim.x, c + 1));
+    const Shares shares(P.pre_total, gridDim.x);
+    const int g0 = prefix_block_at(each, shares.first(c)), g1 = prefix_block_at(each, shares.first(c + 1));
     const int blocks = g1 - g0;        // (none: nothing to do, and the second run expects nothing)
     int own_abort = 0;
     auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded(bar, parity & 1u, &own_abort, P.status); };
@@ -544,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             wait(o_done, done + nb - 1);
             tc_fence_after();
             // into this block's slot of the unit: the second run joins the slots
-            float* slot = P.pre_o + (2 * c + (us >= g0 ? 1 : 0)) * (int64_t)(kRows * (D + 2));
+            float* slot = P.pre_o + (int64_t)(c * P.pre_slots + prefix_slot(shares, each, c, unit)) * (kRows * (D + 2));
             if (half == 0 && r < rows) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m, l);
 #pragma unroll 1
             for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
@@ -600,7 +597,8 @@ int64_t key_places(int kv_heads, int all_rows, int prefix_len) {
 size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D) {
     const int64_t n = key_places(kv_heads, all_rows, prefix_len);
     if (all_rows <= 16 || prefix_len <= 384 || n > 0x7fffffffLL) return 0;
-    return (size_t)std::min<int64_t>(h->num_sms, n) * 2 * kRows * (D + 2) * sizeof(float);
+    const int blocks = (int)std::min<int64_t>(h->num_sms, n);
+    return (size_t)blocks * prefix_slots((prefix_len + kKeys - 1) / kKeys, (int)n, blocks) * kRows * (D + 2) * sizeof(float);
 }
 
 lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf16, char* scratch, cudaStream_t stream) {
@@ -610,6 +608,7 @@ lq_status launch_prefix_tc(lq_handle h, AttnParams& P, int bits, int D, bool bf1
     P.pre_each = (P.max_len + kKeys - 1) / kKeys;
     P.pre_total = (int)key_places(P.cache.kv_heads, P.all_rows, P.max_len);
     P.pre_blocks = std::min(h->num_sms, P.pre_total);
+    P.pre_slots = prefix_slots(P.pre_each, P.pre_total, P.pre_blocks);
     if (D == 128) {
         if (bits == 4) return bf16 ? run<4, 128, __nv_bfloat16>(h, P, stream) : run<4, 128, __half>(h, P, stream);
         return bf16 ? run<8, 128, __nv_bfloat16>(h, P, stream) : run<8, 128, __half>(h, P, stream);
