@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
     const bool pieces = (int64_t)cum[P.requests].y * per <= C;
     // (a share counts kCost tiles before each unit's own, for what a unit costs a block besides them)
     const int total = (cum[P.requests].x + kCost * P.requests) * per;
-    const int q = (int)(((uint64_t)(uint32_t)total * P.grid_inverse) >> 42), rem = total - q * C;   // (total / C)
+    const Shares shares(total, C);
     // last request b with per * start(b) <= at: for the warp together, and for each lane its own
     auto last = [&](auto start, int at) {
         int lo = 0;
@@ -439,7 +439,6 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
     };
     auto tiles_to = [&](int i) { return cum[i].x; };
     auto costly = [&](int i) { return cum[i].x + kCost * i; };
-    auto block_of = [&](int at) { return at < rem * (q + 1) ? at / (q + 1) : rem + (at - rem * (q + 1)) / q; };
     auto tile_at = [&](int at) {                      // first tile at or after a place of the shares' sequence
         if (at >= total) return cum[P.requests].x * per;
         const int i = last(costly, at), tiles = cum[i + 1].x - cum[i].x, in = at - costly(i) * per;
@@ -458,8 +457,8 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
         g0 = us + pq * piece + min(piece, pr);
         g1 = us + pq * (piece + 1) + min(piece + 1, pr);
     } else {
-        g0 = tile_at(q * c + min(c, rem));
-        g1 = tile_at(q * (c + 1) + min(c + 1, rem));
+        g0 = tile_at(shares.first(c));
+        g1 = tile_at(shares.first(c + 1));
         if (g0 >= g1) return;
         b = last(tiles_to, g0);
         unit = quick_div(g0 - cum[b].x * per, cum[b + 1].x - cum[b].x);
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
             if (tid < rows) *reinterpret_cast<float2*>(slot + R * D + 2 * tid) = total_ml[tid];
             // the blocks that share the unit
             const int from = costly(b) * per + unit * (each + kCost) + kCost;
-            const int c0 = pieces ? c - piece : block_of(from), c1 = pieces ? c0 + of - 1 : block_of(from + each - 1);
+            const int c0 = pieces ? c - piece : shares.of(from), c1 = pieces ? c0 + of - 1 : shares.of(from + each - 1);
             unsigned* count = P.counters + (int64_t)b * per + unit;
             __syncthreads();
             // (release of what the block wrote before the barrier, acquire of what the others did)
@@ -687,7 +686,6 @@ lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream
     if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost<W>) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     if (blocks > 1024 || (int64_t)P.cache.kv_heads * P.row_tiles >= (1 << 20)) return LQ_ERR_UNSUPPORTED;
     P.part = reinterpret_cast<float*>(scratch);
-    P.grid_inverse = ((uint64_t)1 << 42) / blocks + 1;
     return launch_overlapped(attn_kernel<BITS, D, NT, W, T>, blocks, 32 * W,
                              AttnSmem<BITS, D, NT, W>::kCum + 8 * (cum_room(P.requests) + 1), stream, P);
 }

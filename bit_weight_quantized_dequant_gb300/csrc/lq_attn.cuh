@@ -26,7 +26,6 @@ struct AttnParams {
     int tokens, group, q_heads;
     int max_len, row_tiles;
     int page_shift;                      // log2 of the tiles of a page, -1 when that is not whole
-    uint64_t grid_inverse;               // 2^42 / blocks, rounded up: n * this >> 42 is n / blocks for n < 2^31, blocks <= 1024
     float scale_log2;                    // scale * log2(e)
     float* part;                         // partial sums: 2 slots per block
     unsigned* counters;                  // one per unit, zero between calls

@@ -49,6 +49,18 @@ extern "C" int walk_prefix(int units, int each, int sms) {
     }
     return 0;
 }
+
+// n things over c parties: consecutive ranges that differ by one at most, and every thing's party.
+extern "C" int walk_shares(int n, int c) {
+    const Shares s(n, c);
+    if (s.first(0) != 0 || s.first(c) != n) return 1;
+    for (int k = 0; k < c; ++k) {
+        const int a = s.first(k), b = s.first(k + 1), size = b - a;
+        if (size != n / c && size != n / c + 1) return 2;
+        if (size > 0 && (s.of(a) != k || s.of(b - 1) != k)) return 3;
+    }
+    return 0;
+}
 """
 
 
@@ -68,3 +80,11 @@ def shares(tmp_path_factory):
 def test_every_unit_of_the_prefix_kernel_has_slots_of_its_own(shares, sms, each):
     for units in list(range(1, 601)) + [1024, 4097]:
         assert shares.walk_prefix(units, each, sms) == 0, (units, each, sms)
+
+
+@pytest.mark.parametrize("blocks", [1, 148, 152, 304, 456, 608, 1024])
+def test_shares_up_to_the_limit_of_a_call(shares, blocks):
+    """A call's places go up to 2^31 - 1 (the host refuses more); blocks are one to four per SM."""
+    for n in (1, blocks - 1, blocks, blocks + 1, 39916801, 2 ** 29 + 11, 640000003, 1300000000, 2147483547, 2 ** 31 - 1):
+        if n > 0:
+            assert shares.walk_shares(n, blocks) == 0, n
