@@ -16,9 +16,10 @@
 //           per row by a power of two into [2^9, 2^10) first, exact for both types.
 //   values  sum_j p_j (S_gj c_j + Z_gj): P S_g as the B operand of group g's MMAs, sum p Z as one
 //           more MMA (groups as M).  P = 2^11 p is rounded to binary16 (p up to 2^3 before the
-//           running maximum moves), then P S 2^ks, with ks a power of two held per warp so that
-//           S 2^ks stays below 3.9: the product spans 2^16 down to 2^-24, so a probability
-//           keeps 11 bits down to 2^-27 of the largest.  Sums and statistics are fp32.
+//           running maximum moves), then P S 2^ks, with ks held per warp and group so that
+//           S 2^ks stays below 3.9: the product keeps 11 bits down to p S 2^ks = 2^-25 and is off by
+//           2^-36 at least, in units of a code (S 2^ks is 2^-8 or more at the group's largest S, so for its
+//           tokens 11 bits down to p = 2^-17).  Sums and statistics are fp32.
 //
 // The grid is persistent: all (request, kv head, row tile) units' 16-token tiles form one
 // sequence, and block c of C takes the range [total c / C, total (c + 1) / C); its warps take
@@ -60,10 +61,15 @@ constexpr int kUnitCost = W == 8 ? 40 : 20;
 template <int D, int NT>
 constexpr int kWarpsPerSm = NT == 2 && D == 128 ? 8 : 16;
 constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
-// S 2^ks stays at or below kMostS (2^14 times that is finite); ks = 0 where the first tile's largest S lies
-// between the two, so that the multiplication is skipped; otherwise it brings the largest into [1, 2)
-constexpr float kMostS = 3.9f, kLeastS = 0x1p-8f;
-constexpr int kUnset = 99;
+// S 2^ks of a group stays at or below kMostS (2^14 times that is finite).  ks is 0 where the first tile's largest S is
+// kLeastS or more, so that the multiplication is skipped; otherwise it brings the largest into [1, 2), and goes down
+// when a larger one comes.  S 2^ks is exact, and P S 2^ks off by 2^-25 at most.  An S above kMostS among others
+// below, as a wide value group has it (a clamped infinity: 513 in 8 bits), moves no power of two, which would cost
+// every other token its bits: such products are taken one by one, in fp32.  (128 Ki tokens, 4 bits: 51 us, 283 if
+// all were taken so; where all of a group's are wide together, ks is below 0 and it takes 63.)
+constexpr float kMostS = 3.875f, kLeastS = 0x1p-8f;
+constexpr uint32_t kMostS2 = 0x43c043c0u, kLeastS2 = 0x1c001c00u;   // (two of each in binary16)
+constexpr uint32_t kUnset = 1u << 31, kNoScales = 0x0e0e0e0eu;
 
 template <int BITS, int D, int NT, int W>
 struct AttnSmem {
@@ -87,8 +93,9 @@ struct State {
     float oz[NT][4];          // sum p Z: group n x rows
     float m[NT][2], l[NT][2]; // rows' references and sums of P
     float ref[NT][2];         // what scores lose before 2^x: m - 11, 0 while m is -inf
-    int ks;
+    uint32_t ks;              // 14 + ks of group g in bits 8 g .. 8 g + 4; kUnset before the first tile, kNoScales where all are 0
 };
+__device__ __forceinline__ int ks_of(uint32_t ks, int g) { return (int)(ks >> (8 * g) & 31u) - 14; }
 
 template <int BITS, int D, int NT>
 struct QFrag {
@@ -164,6 +171,67 @@ __device__ __forceinline__ void load_q(const AttnParams& P, QFrag<BITS, D, NT>& 
         Q.z[nt][0] = hi;
         Q.z[nt][1] = lo;
     }
+}
+
+// The powers of two of a tile's groups, and its values' scales times them in vs; the sums keep step.  Returns the tokens
+// that have a wide group (S > kMostS where ks >= 0), whose scale is 0 in vs.  Seldom called, and short.
+//   A group's first tile: 0, or what brings its largest S into [1, 2) where that is below kLeastS.  Below 0 only where all
+//   of the group's S are wide together, within a factor that leaves S 2^ks in [kLeastS, kMostS]; at the first that is not,
+//   ks is 0 from then on.  Later tiles: down, not below 0, where S 2^ks would pass kMostS.
+template <int BITS, int D, int NT>
+__device__ __forceinline__ uint32_t choose_scales(const uint8_t* tile, State<D, NT>& A, uint32_t k0, uint32_t k1, uint32_t (&vs)[D / 32][2], int t) {
+    using L = KvLayout<BITS, D>;
+    constexpr int G = D / 32;
+    const uint32_t had = A.ks;
+    uint32_t ks = G == 2 ? kNoScales & 0xffff0000u : 0u, wide = 0;
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+        const uint2 v = lds64(tile + L::kVs + g * 32 + 8 * t);
+        float S[4], most = 0.f, least = INFINITY, fit = 0.f;   // fit: the largest that is not wide
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2((i & 2 ? v.y & k1 : v.x & k0));
+            S[i] = i & 1 ? f.y : f.x;
+            most = fmaxf(most, S[i]);
+            if (S[i] > 0.f) least = fminf(least, S[i]);
+            if (S[i] <= kMostS) fit = fmaxf(fit, S[i]);
+        }
+#pragma unroll
+        for (int s = 1; s <= 2; s <<= 1) {
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, s));
+            fit = fmaxf(fit, __shfl_xor_sync(0xffffffffu, fit, s));
+        }
+        auto to_one = [](float top) { return 127 - (int)(__float_as_uint(top) >> 23); };
+        int k = ks_of(had, g);
+        if ((int)had < 0 && most > kMostS) k = max(to_one(most), -14);
+        if (k < 0 && (most * pow2i(k) > kMostS || least * pow2i(k) < kLeastS)) k = 0;
+        if (k >= 0) {
+            if (k == 0 && (int)had < 0 ? fit < kLeastS : fit * pow2i(k) > kMostS) k = min(max(to_one(fit), 0), 15);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (S[i] > kMostS) wide |= 1u << (2 * t + (i & 1) + 4 * (i & 2));
+        }
+        ks |= (uint32_t)(k + 14) << (8 * g);
+    }
+    wide |= __shfl_xor_sync(0xffffffffu, wide, 1);
+    wide |= __shfl_xor_sync(0xffffffffu, wide, 2);
+    A.ks = ks;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint2 v = lds64(tile + L::kVs + g * 32 + 8 * t);
+        const int k = ks_of(ks, g);
+        vs[g][0] = v.x & k0, vs[g][1] = v.y & k1;
+        if (k >= 0) vs[g][0] &= ~hgt2_mask(vs[g][0], kMostS2), vs[g][1] &= ~hgt2_mask(vs[g][1], kMostS2);
+        const uint32_t k2 = (uint32_t)(k + 15) * 0x04000400u;
+        vs[g][0] = hmul2(vs[g][0], k2), vs[g][1] = hmul2(vs[g][1], k2);
+        const float down = pow2i(k - ks_of(had, g));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) A.o[nt][2 * g + (i >> 2)][i & 3] *= down;
+    }
+    return wide;
 }
 
 // One 16-token tile in shared memory at `tile`, its first token j0: scores, new statistics, O.
@@ -258,39 +326,45 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
     load_scales();
     if (n < G) *reinterpret_cast<uint2*>(zz) = lds64(tile + L::kVz + n * 32 + 8 * t);
     if (kEdge) zz[0] &= k0, zz[1] &= k1;
-    // S 2^ks: below 3.9, so that P S stays finite, and not tiny; S as it is (ks = 0) in between
-    auto largest = [&] {
+    auto scale_by = [&](int g, int e) {
+        const uint32_t k2 = (uint32_t)(e + 15) * 0x04000400u;   // binary16 2^e, twice
+        vs[g][0] = hmul2(vs[g][0], k2), vs[g][1] = hmul2(vs[g][1], k2);
+    };
+    bool scales = false;
+    if (A.ks != kNoScales) {
+        scales = (int)A.ks < 0;   // (kUnset)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int k = ks_of(A.ks, g);
+            scale_by(g, k);
+            if (k < 0) scales |= ((hgt2_mask(kLeastS2, vs[g][0]) & hgt2_mask(vs[g][0], 0u)) | (hgt2_mask(kLeastS2, vs[g][1]) & hgt2_mask(vs[g][1], 0u))) != 0;
+        }
+    }
+    {   // S 2^ks has to stay below kMostS so that P S stays finite
         uint32_t m = hmax2(vs[0][0], vs[0][1]);
 #pragma unroll
         for (int g = 1; g < G; ++g) m = hmax2(m, hmax2(vs[g][0], vs[g][1]));
-        return m;
-    };
-    auto scale_by = [&](int e) {
-        const uint32_t k2 = (uint32_t)(e + 15) * 0x04000400u;   // binary16 2^e, twice
-#pragma unroll
-        for (int g = 0; g < G; ++g) vs[g][0] = hmul2(vs[g][0], k2), vs[g][1] = hmul2(vs[g][1], k2);
-    };
-    if (A.ks != 0 && A.ks != kUnset) scale_by(A.ks);
-    const uint32_t big = largest();
-    const float2 bf = unpack2(big);
-    bool move = fmaxf(bf.x, bf.y) > kMostS || A.ks == kUnset;
+        const float2 f = unpack2(m);
+        scales |= fmaxf(f.x, f.y) > kMostS;
+    }
+    bool move = scales;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) move |= fmaxf(x[nt][i], x[nt][i + 2]) > A.m[nt][i] + kTau;
     if (__any_sync(0xffffffffu, move)) {
-        const int had = A.ks == kUnset ? 0 : A.ks;
-        if (had != 0) load_scales();   // (S as stored: times 2^had it may have overflowed)
-        const float2 raw = unpack2(largest());
-        float top = fmaxf(raw.x, raw.y);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int ks = had;
-        if (top * pow2i(had) > kMostS || (A.ks == kUnset && top < kLeastS))
-            ks = min(max(127 - (int)(__float_as_uint(top) >> 23), -14), 15);
-        if (ks != 0) scale_by(ks);
-        const float down = pow2i(ks - had);
-        A.ks = ks;
+        uint32_t wide = 0;   // tokens with a wide value group
+        if (__any_sync(0xffffffffu, scales)) {
+            // A first tile of ordinary scales, with no group's largest below kLeastS or above kMostS, needs no powers.
+            uint32_t enough = (int)A.ks < 0 ? 0u : 1u << G;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float2 f = unpack2(hmax2(vs[g][0], vs[g][1]));
+                enough |= (fmaxf(f.x, f.y) >= kLeastS) << g | (fmaxf(f.x, f.y) > kMostS) << G;
+            }
+            if (__reduce_or_sync(0xffffffffu, enough) == (1u << G) - 1u) A.ks = kNoScales;
+            else wide = choose_scales<BITS, D, NT>(tile, A, kEdge ? k0 : 0xffffffffu, kEdge ? k1 : 0xffffffffu, vs, t);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float a[2];
@@ -310,7 +384,37 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
 #pragma unroll
             for (int k = 0; k < MT; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) A.o[nt][k][i] *= a[i & 1] * down;
+                for (int i = 0; i < 4; ++i) A.o[nt][k][i] *= a[i & 1];
+        }
+        if (wide) {   // seldom: the products of these tokens' wide groups one by one, in fp32, in the units of the sums
+#pragma unroll 1
+            for (uint32_t rest = wide; rest; rest &= rest - 1) {
+                const int j = __ffs((int)rest) - 1;
+                float f[NT][2];   // P of rows 2 t, 2 t + 1
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        f[nt][i] = __shfl_sync(0xffffffffu, ex2((j & 8 ? x[nt][i + 2] : x[nt][i]) - A.ref[nt][i]), 4 * (j & 7) + t);
+                uint32_t w[WV];
+#pragma unroll
+                for (int i = 0; i < WV; ++i) w[i] = lds32(tile + L::kVc + kv_word_at(4 * n + ((j & 7) >> 1), ((j & 1) + 2 * (j >> 3)) * WV + i));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float S = __half2float(*reinterpret_cast<const __half*>(tile + L::kVs + 2 * (g * kKvTile + kv_vmeta_pos(j))));
+                    if (!(S > kMostS) || ks_of(A.ks, g) < 0) continue;
+                    const float u = S * pow2i(ks_of(A.ks, g) - 24);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = 2 * g + (i >> 2), s = 2 * k + (i >> 1 & 1);
+                            const uint32_t c = (w[s % WV] >> (BITS * (s / WV))) & ((1u << BITS) - 1u);
+                            const float fu = f[nt][i & 1] * (BITS == 4 && (s / WV & 1) ? 16.f * u : u);
+                            A.o[nt][k][i & 3] = fmaf((float)c, fu, A.o[nt][k][i & 3]);
+                        }
+                }
+            }
         }
     }
 
@@ -522,7 +626,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
         load_q<BITS, D, NT, T>(P, Q, row0, rows, head, n, t);
         State<D, NT> A;
         int seen[NT][2];   // tokens that rows 2 t, 2 t + 1 see
-        A.ks = kUnset;
+        A.ks = kUnset | kNoScales;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -580,13 +684,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm<D, NT> / W) attn_kernel(co
                 fac[nt][i] = ex2(A.m[nt][i] - ref);
                 if (warp == 0 && n == 0) total_ml[r] = make_float2(top, l);
             }
-        const float up = pow2i(24 - (A.ks == kUnset ? 0 : A.ks));
         auto put = [&](bool add) {   // this warp's rows into (or onto) slot warp % (W / 2)
             float* dst = red + (warp % (W / 2)) * R * M::kPitch;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < MT; ++k) {
+                    const float up = pow2i(24 - ks_of(A.ks, k >> 1));
                     const float z0 = __shfl_sync(0xffffffffu, A.oz[nt][0], 4 * (k >> 1) + t);
                     const float z1 = __shfl_sync(0xffffffffu, A.oz[nt][1], 4 * (k >> 1) + t);
 #pragma unroll

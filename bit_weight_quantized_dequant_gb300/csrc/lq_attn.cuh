@@ -97,6 +97,15 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
     asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// Each half all ones where a > b (not where one is NaN).
+__device__ __forceinline__ uint32_t hgt2_mask(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("{\n\t.reg .pred p, q;\n\t.reg .b16 l, h;\n\tsetp.gt.f16x2 p|q, %1, %2;\n\tselp.b16 l, 0xffff, 0, p;\n\t"
+        "selp.b16 h, 0xffff, 0, q;\n\tmov.b32 %0, {l, h};\n\t}"
+        : "=r"(d)
+        : "r"(a), "r"(b));
+    return d;
+}
 __device__ __forceinline__ float2 unpack2(uint32_t h) {
     return make_float2(half_bits_to_float((uint16_t)h), half_bits_to_float((uint16_t)(h >> 16)));
 }
