@@ -410,11 +410,38 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
                         for (int i = 0; i < 8; ++i) {
                             const int k = 2 * g + (i >> 2), s = 2 * k + (i >> 1 & 1);
                             const uint32_t c = (w[s % WV] >> (BITS * (s / WV))) & ((1u << BITS) - 1u);
-                            const float fu = f[nt][i & 1] * (BITS == 4 && (s / WV & 1) ? 16.f * u : u);
+                            const float fu = f[nt][i & 1] == 0.f ? 0.f : f[nt][i & 1] * (BITS == 4 && (s / WV & 1) ? 16.f * u : u);
                             A.o[nt][k][i & 3] = fmaf((float)c, fu, A.o[nt][k][i & 3]);
                         }
                 }
             }
+        }
+    }
+
+    // A NaN or infinity of a value is for the rows that see its token.  P is 0 in the others, but 0 times it is not: P S
+    // is cleared there, and a Z that is no number leaves the sums' operand and makes S one instead, which stays in
+    // its group of dimensions as Z does.
+    uint32_t row_sees[NT][2];
+    if (kEdge) {
+        auto odd = [](uint32_t z, int h) { return (z >> (16 * h) & 0x7c00u) == 0x7c00u; };
+        const bool any_odd = odd(zz[0], 0) || odd(zz[0], 1) || odd(zz[1], 0) || odd(zz[1], 1);
+        if (__any_sync(0xffffffffu, any_odd)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = q >> 1, shift = 16 * (q & 1);
+                const uint32_t m = __ballot_sync(0xffffffffu, odd(zz[i], q & 1));   // bit 4 g + t: group g, this lane's token q
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    if (m >> (4 * g + t) & 1u) vs[g][i] |= 0x7fffu << shift;
+                if (odd(zz[i], q & 1)) zz[i] &= ~(0xffffu << shift);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {   // (row n's count lies in lane n / 2)
+            const int even = __shfl_sync(0xffffffffu, seen[nt][0], n >> 1), other = __shfl_sync(0xffffffffu, seen[nt][1], n >> 1);
+            const int sees = (n & 1 ? other : even) - j0;
+            row_sees[nt][0] = (2 * t < sees ? 0xffffu : 0u) | (2 * t + 1 < sees ? 0xffff0000u : 0u);
+            row_sees[nt][1] = (2 * t + 8 < sees ? 0xffffu : 0u) | (2 * t + 9 < sees ? 0xffff0000u : 0u);
         }
     }
 
@@ -457,6 +484,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
             for (int i = 0; i < 2; ++i) {
                 b[nt][i] = hmul2(p[nt][i], vs[g][i]);
                 if (kFine) rest[nt][i] = hmul2_rest(p[nt][i], vs[g][i], b[nt][i]);
+                if (kEdge) b[nt][i] &= row_sees[nt][i];
+                if (kEdge && kFine) rest[nt][i] &= row_sees[nt][i];
             }
 #pragma unroll
         for (int k = 2 * g; k < 2 * g + 2; ++k) {
