@@ -213,28 +213,17 @@ LQ_API lq_status lq_sync(lq_handle h) {
     if (cudaDeviceSynchronize() != cudaSuccess) return LQ_ERR_CUDA;
     int flag = 0;
     if (cudaMemcpy(&flag, h->status_flag, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return LQ_ERR_CUDA;
-    if (flag & 1) {
-        // a wait ran out: the launch that timed out may have left arrival counts behind, so they
-        // are cleared with the flag
-        if (cudaMemset(h->status_flag, 0, 256) != cudaSuccess ||
-            cudaMemset(h->counters, 0, h->num_counters * sizeof(unsigned)) != cudaSuccess ||
-            cudaDeviceSynchronize() != cudaSuccess)
-            return LQ_ERR_CUDA;
-        return LQ_ERR_TIMEOUT;
-    }
-    if (flag & 2) {
-        // a decode GEMV met a weight outside the binary16 range of its tensor-core operands
-        if (cudaMemset(h->status_flag, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
-            return LQ_ERR_CUDA;
-        return LQ_ERR_RANGE;
-    }
-    if (flag & lq::kStatusIndex) {
-        // a rotation, cache or attention kernel left out an element whose index was out of range
-        if (cudaMemset(h->status_flag, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
-            return LQ_ERR_CUDA;
-        return LQ_ERR_INDEX;
-    }
-    return LQ_OK;
+    if (flag == 0) return LQ_OK;
+    // one condition a call, the gravest first; the others stay for the next
+    const int bit = flag & 1 ? 1 : flag & 2 ? 2 : lq::kStatusIndex;
+    flag &= ~bit;
+    if (cudaMemcpy(h->status_flag, &flag, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return LQ_ERR_CUDA;
+    // a wait ran out: the launch that timed out may have left arrival counts behind, so they are cleared with the flag
+    if (bit == 1 && cudaMemset(h->counters, 0, h->num_counters * sizeof(unsigned)) != cudaSuccess) return LQ_ERR_CUDA;
+    if (cudaDeviceSynchronize() != cudaSuccess) return LQ_ERR_CUDA;
+    // (2: a decode GEMV met a weight outside the binary16 range of its tensor-core operands; otherwise a rotation, cache or
+    // attention kernel left out an element whose index was out of range)
+    return bit == 1 ? LQ_ERR_TIMEOUT : bit == 2 ? LQ_ERR_RANGE : LQ_ERR_INDEX;
 }
 
 LQ_API lq_status lq_dequant(lq_handle h, int format, const uint8_t* codes, const void* scales,

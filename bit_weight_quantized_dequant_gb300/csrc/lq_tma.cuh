@@ -78,7 +78,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
             if (*abort) return false;
             if (global_timer_ns() - t0 > limit_ns || i >= (1u << 31)) {   // (the count is a backstop)
                 *abort = 1;
-                if (status) atomicExch(status, 1);
+                if (status) atomicOr(status, 1);
                 return false;
             }
         }

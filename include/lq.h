@@ -179,8 +179,9 @@ LQ_API const char* lq_status_string(int status);
 
 /*
  * lq_sync — wait for the device and report errors raised on it: LQ_ERR_CUDA for
- * an asynchronous CUDA error, LQ_ERR_TIMEOUT when a bounded device wait ran out
- * since the last lq_sync (the flag is cleared).
+ * an asynchronous CUDA error, LQ_ERR_TIMEOUT when a bounded device wait ran out,
+ * then LQ_ERR_RANGE, then LQ_ERR_INDEX when a kernel met one.  A call reports one
+ * condition and clears that one; others raised since stay for the next call.
  */
 LQ_API lq_status lq_sync(lq_handle h);
 
@@ -572,7 +573,7 @@ LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq
  * thread of one CTA waits, with the routine the pipelined kernels use, on a
  * shared-memory barrier that nothing completes.  After limit_us microseconds
  * (1 .. 1000000) the wait gives up, raises the handle's status word and the kernel
- * returns; the next lq_sync reports LQ_ERR_TIMEOUT and clears the status word and
+ * returns; the next lq_sync reports LQ_ERR_TIMEOUT and clears that condition and
  * the arrival counters.  Nothing faults and the context stays usable.  Errors:
  * LQ_ERR_INVALID_ARG (null handle, limit out of range), LQ_ERR_CUDA.
  */
