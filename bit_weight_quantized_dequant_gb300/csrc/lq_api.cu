@@ -502,7 +502,7 @@ LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq
     if (a.batch < 1 || a.tokens < 1 || a.q_heads < 1 || a.q_heads % cache->kv_heads != 0) return LQ_ERR_INVALID_ARG;
     if (a.batch > lq::kMaxAttnBatch || a.tokens > lq::kMaxAttnTokens) return LQ_ERR_UNSUPPORTED;
     if (a.max_pages < 1 || a.block_table_stride < a.max_pages || a.prefix_len < 0) return LQ_ERR_INVALID_ARG;
-    if ((int64_t)a.max_pages * cache->page_size > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)a.max_pages * cache->page_size > 0x7fffff00LL || a.prefix_len > 0x7fffff00) return LQ_ERR_UNSUPPORTED;
     if (a.prefix_len > 0 && !a.prefix_table) return LQ_ERR_INVALID_ARG;
     if ((int64_t)a.q_heads * cache->head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
     if (!(a.scale > 0.f) || !(a.scale < 3.0e38f)) return LQ_ERR_INVALID_ARG;

@@ -544,6 +544,7 @@ LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t
  *   - the request's own tokens j < lens[b] - tokens + 1 + t (lens counts the query tokens,
  *     which are in the cache already), token j in slot block_table[b][j / page_size] *
  *     page_size + j % page_size.
+ * prefix_len and max_pages * page_size go up to 0x7fffff00 (LQ_ERR_UNSUPPORTED above).
  * A row with no key gives out = 0 and lse = -inf.  lens[b] is taken as 0 below 0 and as
  * max_pages * page_size above that.  A page outside the cache (LQ_ERR_INDEX) hides its tokens.
  * q, out: [batch][tokens][q_heads][head_dim] of dtype (LQ_F16 or LQ_BF16), token strides in
