@@ -27,3 +27,30 @@ def test_more_units_than_blocks(lqm, handle, B, T, hq, hkv, D, bits, prefix, dty
     sample = sorted({min(B - 1, (128 * t + 64) // rows) for t in range(tiles)} | {0, B - 1})
     c.check(*c.run(handle), requests=sample)
     handle.sync()
+
+
+@pytest.mark.parametrize("B,T,hq,hkv,D,bits,prefix", [
+    (1024, 1, 4, 4, 128, 4, 390),              # two key blocks a share
+    (300, 1, 12, 12, 64, 8, 520),              # five
+    (130, 1, 8, 2, 128, 8, 2000),
+    (40, 2, 40, 40, 128, 4, 700),
+])
+def test_first_calls_with_nothing_in_the_caches(lqm, B, T, hq, hkv, D, bits, prefix):  # noqa: F811
+    """Values that come late, in a workspace that nothing has written: the sums are read when they are done, so a first
+    call answers what later ones do, bit for bit, and right in every unit."""
+    g = np.random.default_rng(B)
+    c = Case(lqm, [int(x) for x in g.integers(0, 33, B)], T=T, hq=hq, hkv=hkv, D=D, bits=bits, prefix=prefix, page=16, seed=B)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(12):
+        h = lqm.Handle(0)
+        flush.fill_(i)
+        out, lse = c.run(h)
+        h.sync()
+        if first is None:
+            first = out, lse
+            rows = T * (hq // hkv)
+            tiles = -(-B * rows // 128)
+            c.check(out, lse, requests=sorted({min(B - 1, (128 * t + 64) // rows) for t in range(tiles)}))
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+        h.close()
