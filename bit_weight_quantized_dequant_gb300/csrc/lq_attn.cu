@@ -39,6 +39,7 @@
 // and 3 us of start and 8 us from the last tile to the joined output come on top.  333 tokens, 32 heads:
 // 8.7 us, all latency.
 
+#include <algorithm>
 #include <mutex>
 
 #include "lq_attn.cuh"
@@ -807,78 +808,118 @@ int attn_blocks(int device, int num_sms, int requests) {
     return blocks;
 }
 
+// A run's scratch, and whether it is only to be asked for (launch false).
+struct Scratch {
+    char* at;
+    size_t room, need;
+    bool launch;
+    cudaStream_t stream;
+};
+
 template <int BITS, int D, int NT, int W, class T>
-lq_status run(lq_handle h, AttnParams& P, char* scratch, size_t room, cudaStream_t stream) {
+lq_status run(lq_handle h, AttnParams& P, Scratch& s) {
     constexpr int R = 8 * NT;
     P.row_tiles = (P.rows + R - 1) / R;
     const int blocks = attn_blocks<BITS, D, NT, W, T>(h->device, h->num_sms, P.requests);
     if (blocks < 1) return LQ_ERR_CUDA;
-    if ((size_t)P.requests * P.cache.kv_heads * P.row_tiles > h->num_counters) return LQ_ERR_WORKSPACE;
-    if ((size_t)blocks * 2 * R * (D + 2) * sizeof(float) > room) return LQ_ERR_WORKSPACE;
     // (tile indices are 32-bit, quotients of units below 2^20)
     if (((int64_t)P.max_len / kKvTile + 2 + kUnitCost<W>) * P.requests * P.cache.kv_heads * P.row_tiles > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
     if (blocks > 1024 || (int64_t)P.cache.kv_heads * P.row_tiles >= (1 << 20)) return LQ_ERR_UNSUPPORTED;
-    P.part = reinterpret_cast<float*>(scratch);
+    if ((size_t)P.requests * P.cache.kv_heads * P.row_tiles > h->num_counters) return LQ_ERR_WORKSPACE;
+    s.need = (size_t)blocks * 2 * R * (D + 2) * sizeof(float);
+    if (s.need > s.room) return LQ_ERR_WORKSPACE;
+    if (!s.launch) return LQ_OK;
+    P.part = reinterpret_cast<float*>(s.at);
     return launch_overlapped(attn_kernel<BITS, D, NT, W, T>, blocks, 32 * W,
-                             AttnSmem<BITS, D, NT, W>::kCum + 8 * (cum_room(P.requests) + 1), stream, P);
+                             AttnSmem<BITS, D, NT, W>::kCum + 8 * (cum_room(P.requests) + 1), s.stream, P);
 }
 
 template <int BITS, int D, int NT>
-lq_status run_typed(lq_handle h, AttnParams& P, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
+lq_status run_typed(lq_handle h, AttnParams& P, bool bf16, Scratch& s) {
     const int64_t units = (int64_t)P.requests * P.cache.kv_heads * ((P.rows + 8 * NT - 1) / (8 * NT));
-    if (units > 2 * h->num_sms)
-        return bf16 ? run<BITS, D, NT, 4, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, NT, 4, __half>(h, P, scratch, room, stream);
-    return bf16 ? run<BITS, D, NT, 8, __nv_bfloat16>(h, P, scratch, room, stream) : run<BITS, D, NT, 8, __half>(h, P, scratch, room, stream);
+    if (units > 2 * h->num_sms) return bf16 ? run<BITS, D, NT, 4, __nv_bfloat16>(h, P, s) : run<BITS, D, NT, 4, __half>(h, P, s);
+    return bf16 ? run<BITS, D, NT, 8, __nv_bfloat16>(h, P, s) : run<BITS, D, NT, 8, __half>(h, P, s);
 }
 
 template <int BITS, int D>
-lq_status run_rows(lq_handle h, AttnParams& P, bool bf16, char* scratch, size_t room, cudaStream_t stream) {
+lq_status run_rows(lq_handle h, AttnParams& P, bool bf16, Scratch& s) {
     // one n = 8 tile of rows where 8 hold them, two otherwise (a second tile costs a third more issue slots per key)
-    return P.rows <= 8 ? run_typed<BITS, D, 1>(h, P, bf16, scratch, room, stream) : run_typed<BITS, D, 2>(h, P, bf16, scratch, room, stream);
+    return P.rows <= 8 ? run_typed<BITS, D, 1>(h, P, bf16, s) : run_typed<BITS, D, 2>(h, P, bf16, s);
 }
 
-}  // namespace
+lq_status run_shape(lq_handle h, AttnParams& P, int bits, int D, bool bf16, Scratch s) {
+    if (D == 128) return bits == 4 ? run_rows<4, 128>(h, P, bf16, s) : run_rows<8, 128>(h, P, bf16, s);
+    return bits == 4 ? run_rows<4, 64>(h, P, bf16, s) : run_rows<8, 64>(h, P, bf16, s);
+}
 
-lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, cudaStream_t stream) {
-    AttnParams P;
+// Requests first .. first + n - 1 of a call, or with launch false whether the workspace has room for them at once.
+lq_status attend(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, int first, int n, bool launch, cudaStream_t stream) {
+    AttnParams P = {};
     P.cache = KvView{static_cast<uint8_t*>(c.pages), c.num_pages, c.page_size, c.kv_heads, c.page_size / kKvTile};
-    P.q = a.q, P.out = a.out, P.lse = a.lse;
+    const int64_t row0 = (int64_t)first * a.tokens;
+    P.q = static_cast<const uint16_t*>(a.q) + row0 * a.q_token_stride, P.out = static_cast<uint16_t*>(a.out) + row0 * a.out_token_stride;
+    P.lse = a.lse ? a.lse + row0 * a.q_heads : nullptr;
     P.q_stride = a.q_token_stride, P.out_stride = a.out_token_stride;
     P.tokens = a.tokens, P.q_heads = a.q_heads, P.group = a.q_heads / c.kv_heads;
     P.scale_log2 = a.scale * 1.4426950408889634f;
     P.counters = h->counters;
     P.status = h->status_flag;
-    if ((int64_t)a.batch * a.tokens * P.group > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
-    P.all_rows = a.batch * a.tokens * P.group;
+    if ((int64_t)n * a.tokens * P.group > 0x7fffffffLL) return LQ_ERR_UNSUPPORTED;
+    P.all_rows = n * a.tokens * P.group;
     P.page_shift = -1;
     for (int i = 0; i < 27; ++i)
         if (P.cache.tiles_per_page == 1 << i) P.page_shift = i;
     // workspace: what the prefix run leaves, then partial sums
     char* ws = reinterpret_cast<char*>(h->partials);
     const size_t cap = h->partial_floats * sizeof(float), rows = (size_t)c.kv_heads * P.all_rows;
-    const size_t slots = a.prefix_len > 0 ? prefix_tc_bytes(h, c.kv_heads, P.all_rows, a.prefix_len, c.head_dim) : 0;
-    const size_t pre = a.prefix_len == 0 ? 0 : slots ? slots : (rows * (c.head_dim + 1) * sizeof(float) + 255) & ~size_t(255);
-    if (pre > cap) return LQ_ERR_WORKSPACE;
-    P.pre_o = reinterpret_cast<float*>(ws);
-    P.pre_m = P.pre_o + rows * c.head_dim;
-    P.pre_rows = 0;
     const bool bf16 = a.dtype == LQ_BF16;
-    auto go = [&](AttnParams& p) {
-        if (c.head_dim == 128)
-            return c.bits == 4 ? run_rows<4, 128>(h, p, bf16, ws + pre, cap - pre, stream) : run_rows<8, 128>(h, p, bf16, ws + pre, cap - pre, stream);
-        return c.bits == 4 ? run_rows<4, 64>(h, p, bf16, ws + pre, cap - pre, stream) : run_rows<8, 64>(h, p, bf16, ws + pre, cap - pre, stream);
+    auto go = [&](AttnParams& p, size_t pre, bool now) {
+        return pre > cap ? LQ_ERR_WORKSPACE : run_shape(h, p, c.bits, c.head_dim, bf16, Scratch{ws + pre, cap - pre, 0, now, stream});
     };
-    if (a.prefix_len > 0) {
-        P.prefix = 1;
-        P.block_table = a.prefix_table, P.bt_stride = 0, P.lens = nullptr;
-        P.requests = 1, P.rows = P.all_rows, P.max_len = a.prefix_len;
-        const lq_status s = slots ? launch_prefix_tc(h, P, c.bits, c.head_dim, bf16, ws, stream) : go(P);
+    AttnParams own = P;
+    own.prefix = a.prefix_len > 0 ? 2 : 0;
+    own.block_table = a.block_table + first * a.block_table_stride, own.bt_stride = a.block_table_stride, own.lens = a.lens + first;
+    own.requests = n, own.rows = a.tokens * P.group, own.max_len = a.max_pages * c.page_size;
+    if (a.prefix_len == 0) return go(own, 0, launch);
+
+    P.prefix = 1;
+    P.block_table = a.prefix_table, P.bt_stride = 0, P.lens = nullptr;
+    P.requests = 1, P.rows = P.all_rows, P.max_len = a.prefix_len;
+    // The dense kernel where it is the better one and its slots fit; records are always the smaller.
+    const size_t slots = prefix_tc_bytes(h, c.kv_heads, P.all_rows, a.prefix_len, c.head_dim);
+    const bool dense = slots && go(own, slots, false) == LQ_OK;
+    const size_t pre = dense ? slots : (rows * (c.head_dim + 1) * sizeof(float) + 255) & ~size_t(255);
+    if (!dense) {
+        P.pre_o = reinterpret_cast<float*>(ws);
+        P.pre_m = P.pre_o + rows * c.head_dim;
+        const lq_status s = go(P, pre, launch);
+        if (s != LQ_OK) return s;
+    } else if (launch) {
+        const lq_status s = launch_prefix_tc(h, P, c.bits, c.head_dim, bf16, ws, stream);
         if (s != LQ_OK) return s;
     }
-    P.prefix = a.prefix_len > 0 ? 2 : 0;
-    P.block_table = a.block_table, P.bt_stride = a.block_table_stride, P.lens = a.lens;
-    P.requests = a.batch, P.rows = a.tokens * P.group, P.max_len = a.max_pages * c.page_size;
-    return go(P);
+    own.pre_o = P.pre_o, own.pre_m = P.pre_m;
+    own.pre_rows = P.pre_rows, own.pre_tiles = P.pre_tiles, own.pre_each = P.pre_each, own.pre_total = P.pre_total;
+    own.pre_blocks = P.pre_blocks, own.pre_slots = P.pre_slots;
+    return go(own, pre, launch);
+}
+
+}  // namespace
+
+lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, cudaStream_t stream) {
+    // all requests at once where the workspace has room for that, otherwise so many at a time that it has
+    int n = a.batch;
+    for (;; n = (n + 1) / 2) {
+        lq_status s = attend(h, c, a, 0, n, false, stream);
+        if (s == LQ_OK && a.batch % n) s = attend(h, c, a, 0, a.batch % n, false, stream);
+        if (s == LQ_OK) break;
+        if (s != LQ_ERR_WORKSPACE || n == 1) return s;
+    }
+    for (int first = 0; first < a.batch; first += n) {
+        const lq_status s = attend(h, c, a, first, std::min(n, a.batch - first), true, stream);
+        if (s != LQ_OK) return s;
+    }
+    return LQ_OK;
 }
 
 }  // namespace lq

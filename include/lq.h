@@ -549,7 +549,8 @@ LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t
  * max_pages * page_size above that.  A page outside the cache (LQ_ERR_INDEX) hides its tokens.
  * q, out: [batch][tokens][q_heads][head_dim] of dtype (LQ_F16 or LQ_BF16), token strides in
  * elements, rows 16-byte aligned; lse: fp32 [batch][tokens][q_heads] or NULL.  S of the
- * cache is not negative.  Uses the handle's workspace; LQ_ERR_WORKSPACE when it is too small.
+ * cache is not negative.  Uses the handle's workspace; where that has no room for all requests at once
+ * they are taken in turns (LQ_ERR_WORKSPACE when it has none for a single one).
  */
 typedef struct lq_kv_attention_args {
     const void* q;
