@@ -406,7 +406,7 @@ class Handle:
         return s[0] if n > 1 else heads * dim
 
     def _indices(self, name, t, dtype, n):
-        if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self.device:
+        if t is None or t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self.device:
             raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype} on cuda:{self.device}")
         return t.data_ptr()
 
