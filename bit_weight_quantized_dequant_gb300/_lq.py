@@ -386,15 +386,19 @@ class Handle:
     # ---- rotary positions, the low-bit KV cache and attention over it ----
     # (A decode step calls these once per layer: their checks are few and cheap.)
 
-    def _raw(self, stream, *made):
-        """The raw stream of a call; results made here on the current stream's allocator are kept until
-        `stream`, when it is another, is done with them."""
-        if stream is None:
-            return _torch()._C._cuda_getCurrentRawStream(self.device)
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-        return stream.cuda_stream
+    def _raw(self, stream):
+        """The raw stream of a call."""
+        return _torch()._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
+
+    def _new(self, shape, dtype, stream):
+        """A result of a call on `stream`, in memory of that stream: what the current stream's allocator has at hand may
+        still be read by work of that stream, which another does not wait for.  Freed, it is not reused before the
+        current stream's work so far is done either."""
+        torch = _torch()
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=self._device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
 
     def _rows(self, name, t, n, heads, dim, dtype):
         """Token stride of a [n][heads][dim] operand of this device, heads and dimensions contiguous."""
@@ -420,13 +424,14 @@ class Handle:
                    high_rotations=32.0, mscale=1.0, out=None, stream=None):
         """Rows first .. first + count - 1 of the rotation table, fp32 [count][rot_dim]: cosines, then
         sines.  factor stretches the positions: every frequency (original_length 0) or by parts."""
-        torch, made = _torch(), None
         if out is None:
-            out = made = torch.empty((count, rot_dim), dtype=torch.float32, device=self._device)
+            torch, shape = _torch(), (count, rot_dim)
+            out = torch.empty(shape, dtype=torch.float32, device=self._device) if stream is None else \
+                self._new(shape, torch.float32, stream)
         elif out.shape != (count, rot_dim):
             raise ValueError(f"out must be [{count}][{rot_dim}]")
         c = lq_rope_config(rot_dim, base, factor, original_length, low_rotations, high_rotations, mscale)
-        st = self._lib.lq_rope_table(self._h, ctypes.byref(c), first, count, self._table(out), self._raw(stream, made))
+        st = self._lib.lq_rope_table(self._h, ctypes.byref(c), first, count, self._table(out), self._raw(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_rope_table")
         return out
@@ -434,10 +439,10 @@ class Handle:
     def rope(self, x, positions, table, layout=ROPE_HALF, inverse=False, out=None, stream=None):
         """Rotate the first table.shape[1] dimensions of x [n][heads][dim] (any token and head stride) by
         its int32 positions' table rows; inverse=True applies the transpose (the gradient)."""
-        torch, made = _torch(), None
+        torch = _torch()
         n, heads, dim = shape = x.shape
         if out is None:
-            out = made = torch.empty(shape, dtype=x.dtype, device=x.device)
+            out = torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None else self._new(shape, x.dtype, stream)
         elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != self.device:
             raise ValueError(f"out must have x's shape and dtype on cuda:{self.device}")
         xs, ys = x.stride(), out.stride()
@@ -450,7 +455,7 @@ class Handle:
                          self._table(table), rows, self._indices("positions", positions, torch.int32, n), layout, inverse)
         if n == 0:
             return out
-        st = self._lib.lq_rope(self._h, ctypes.byref(a), self._raw(stream, made))
+        st = self._lib.lq_rope(self._h, ctypes.byref(a), self._raw(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_rope")
         return out
@@ -459,7 +464,7 @@ class Handle:
                   stream=None):
         """Quantise k and v [n][kv_heads][dim] into the cache's int64 slots (negative: skipped).  With a
         table, k is rotated first, and so is q [n][q_heads][dim] when given, into the returned tensor."""
-        torch, made = _torch(), None
+        torch = _torch()
         dt, n, dim, hkv = k.dtype, k.shape[0], cache.head_dim, cache.kv_heads
         ks, vs = self._rows("k", k, n, hkv, dim, dt), self._rows("v", v, n, hkv, dim, dt)
         qp = op = tp = pp = None
@@ -468,7 +473,8 @@ class Handle:
             hq = q.shape[1]
             qs = self._rows("q", q, n, hq, dim, dt)
             if q_out is None:
-                q_out = made = torch.empty((n, hq, dim), dtype=dt, device=q.device)
+                q_out = torch.empty((n, hq, dim), dtype=dt, device=q.device) if stream is None else \
+                    self._new((n, hq, dim), dt, stream)
                 os = hq * dim
             else:
                 os = self._rows("q_out", q_out, n, hq, dim, dt)
@@ -480,7 +486,7 @@ class Handle:
                               self._indices("slots", slots, torch.int64, n), tp, rows, pp, rot, layout)
         if n == 0:
             return q_out
-        st = self._lib.lq_kv_append(self._h, cache._on(self.device), ctypes.byref(a), self._raw(stream, made))
+        st = self._lib.lq_kv_append(self._h, cache._on(self.device), ctypes.byref(a), self._raw(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_append")
         return q_out
@@ -489,13 +495,16 @@ class Handle:
         """The cached keys and values of int64 slots [n], dense [n][kv_heads][dim] (default bfloat16)."""
         torch = _torch()
         dt, n = dtype or torch.bfloat16, slots.shape[0]
-        shape, dev = (n, cache.kv_heads, cache.head_dim), slots.device
-        k, v = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
         sp = self._indices("slots", slots, torch.int64, n)
+        shape, dev = (n, cache.kv_heads, cache.head_dim), slots.device
+        if stream is None:
+            k, v = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
+        else:
+            k, v = self._new(shape, dt, stream), self._new(shape, dt, stream)
         if n == 0:
             return k, v
         st = self._lib.lq_kv_read(self._h, cache._on(self.device), sp, n, k.data_ptr(), v.data_ptr(), _code(dt),
-                                  self._raw(stream, k, v))
+                                  self._raw(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_read")
         return k, v
@@ -506,7 +515,7 @@ class Handle:
         over the cache: request b's own tokens in the pages block_table[b] (int32), lens[b] (int32) of
         them, after the prefix_len tokens of prefix_table's pages, which all requests share.  Returns
         out (q's shape and dtype) and the fp32 log-sum-exp [batch][tokens][q_heads]."""
-        torch, dev, mo, ml = _torch(), self.device, None, None
+        torch, dev = _torch(), self.device
         B, T, hq, dim = shape = q.shape
         dt, row = q.dtype, hq * dim
 
@@ -520,12 +529,13 @@ class Handle:
 
         qs = token_stride("q", q)
         if out is None:
-            out = mo = torch.empty(shape, dtype=dt, device=q.device)
+            out = torch.empty(shape, dtype=dt, device=q.device) if stream is None else self._new(shape, dt, stream)
             os = row
         else:
             os = token_stride("out", out)
         if lse is None:
-            lse = ml = torch.empty((B, T, hq), dtype=torch.float32, device=q.device)
+            lse = torch.empty((B, T, hq), dtype=torch.float32, device=q.device) if stream is None else \
+                self._new((B, T, hq), torch.float32, stream)
         elif lse.shape != (B, T, hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError(f"lse must be contiguous fp32 [batch][tokens][heads] on cuda:{dev}")
         if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.get_device() != dev:
@@ -547,7 +557,7 @@ class Handle:
                                  block_table.data_ptr(), bs[0] if B > 1 else pages, pages,
                                  self._indices("lens", lens, torch.int32, B), pp, prefix_len or 0,
                                  dim ** -0.5 if scale is None else scale)
-        st = self._lib.lq_kv_attention(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream, mo, ml))
+        st = self._lib.lq_kv_attention(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream))
         if st != LQ_OK:
             raise LQError(st, "lq_kv_attention")
         return out, lse
