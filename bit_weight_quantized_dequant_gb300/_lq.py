@@ -198,6 +198,28 @@ def _stream(stream) -> int | None:
     return int(s.cuda_stream) or None
 
 
+@functools.lru_cache(maxsize=None)
+def _rotation():
+    """Handle.rope as a differentiable function of x: the gradient is the transpose of what came."""
+    import torch
+
+    class Rotation(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, handle, positions, table, layout, inverse, stream):
+            ctx.save_for_backward(positions, table)
+            ctx.how = handle, layout, inverse
+            return handle.rope(x, positions, table, layout, inverse, stream=stream)
+
+        @staticmethod
+        def backward(ctx, g):
+            (handle, layout, inverse), (positions, table) = ctx.how, ctx.saved_tensors
+            if g.stride(-1) != 1:
+                g = g.contiguous()
+            return handle.rope(g, positions, table, layout, not inverse), None, None, None, None, None, None
+
+    return Rotation
+
+
 @dataclass
 class QuantWeights:
     """One quantized matrix W [N][K] in device memory (layouts as in include/lq.h)."""
@@ -438,8 +460,14 @@ class Handle:
 
     def rope(self, x, positions, table, layout=ROPE_HALF, inverse=False, out=None, stream=None):
         """Rotate the first table.shape[1] dimensions of x [n][heads][dim] (any token and head stride) by
-        its int32 positions' table rows; inverse=True applies the transpose (the gradient)."""
+        its int32 positions' table rows; inverse=True applies the transpose (the gradient).  An x that
+        requires a gradient gets it through the result (then without out); no other call of a Handle
+        carries gradients."""
         torch = _torch()
+        if x.requires_grad and torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("out cannot take the rotation of an x that requires a gradient")
+            return _rotation().apply(x, self, positions, table, layout, inverse, stream)
         n, heads, dim = shape = x.shape
         if out is None:
             out = torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None else self._new(shape, x.dtype, stream)

@@ -10,6 +10,8 @@ torch = pytest.importorskip("torch")
 class _OnDevice:
     """What the checks look at of a tensor on cuda:0."""
 
+    requires_grad = False
+
     def __init__(self, shape, dtype):
         self.shape, self.dtype, self.device = torch.Size(shape), dtype, "cuda:0"
 
