@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ R
     const int64_t n = blockIdx.x;
     const float* row = table_row(P.table, P.positions, n, P.rows, P.rot, P.status, threadIdx.x == 0);
     const int half = P.rot / 2, each = half + P.D - P.rot;   // pairs, then single dimensions
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < P.heads * each; i += gridDim.y * 256) {
-        const int h = i / each, k = i - h * each;
+    // (unsigned: the step past the last of almost 2^31 pairs stays a number of its own)
+    for (unsigned i = blockIdx.y * 256 + threadIdx.x; i < (unsigned)(P.heads * each); i += gridDim.y * 256) {
+        const int h = (int)(i / (unsigned)each), k = (int)(i - (unsigned)h * (unsigned)each);
         const T* x = static_cast<const T*>(P.x) + n * P.xt + h * P.xh;
         T* y = static_cast<T*>(P.y) + n * P.yt + h * P.yh;
         if (k >= half) {
