@@ -580,10 +580,10 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
 }
 
 // Rows that one group of lanes walks: one where all rows then still fit the device at once (about 1536
-// threads an SM), otherwise a multiple of the four that are loaded together.
+// threads an SM) and the grid's second dimension, otherwise a multiple of the four that are loaded together.
 int rows_per_group(int64_t n, int lanes, int rows, int num_sms) {
     const int64_t groups = std::max<int64_t>(1, (int64_t)num_sms * 1536 / lanes);
-    const int chunks = (int)std::min<int64_t>(rows, std::max<int64_t>(1, (groups + n - 1) / n));
+    const int chunks = (int)std::min<int64_t>(std::min(rows, 65535), std::max<int64_t>(1, (groups + n - 1) / n));
     const int each = (rows + chunks - 1) / chunks;
     return each == 1 ? 1 : (each + 3) / 4 * 4;
 }
