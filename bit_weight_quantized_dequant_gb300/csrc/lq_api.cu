@@ -505,7 +505,7 @@ LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq
     if ((int64_t)a.max_pages * cache->page_size > 0x7fffff00LL || a.prefix_len > 0x7fffff00) return LQ_ERR_UNSUPPORTED;
     if (a.prefix_len > 0 && !a.prefix_table) return LQ_ERR_INVALID_ARG;
     if ((int64_t)a.q_heads * cache->head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
-    if (!(a.scale > 0.f) || !(a.scale < 3.0e38f)) return LQ_ERR_INVALID_ARG;
+    if (!(a.scale > 0.f) || !(a.scale < 2.35e38f)) return LQ_ERR_INVALID_ARG;   // (times log2 e it has to be finite)
     const uintptr_t words = reinterpret_cast<uintptr_t>(a.block_table) | reinterpret_cast<uintptr_t>(a.lens) |
                             reinterpret_cast<uintptr_t>(a.prefix_table) | reinterpret_cast<uintptr_t>(a.lse);
     if (!aligned_rows(a.q, a.q_token_stride, a.dtype) || !aligned_rows(a.out, a.out_token_stride, a.dtype) || (words & 3))

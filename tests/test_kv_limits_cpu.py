@@ -24,3 +24,12 @@ def test_prefix_of_almost_2_to_the_31_tokens(L, prefix_len):
     assert L.lq_kv_attention(H, ctypes.byref(c), ctypes.byref(a), None) == _lq.LQ_ERR_UNSUPPORTED
     a.prefix_len = 0x7fffff00
     assert L.lq_kv_attention(H, ctypes.byref(c), ctypes.byref(a), None) == _lq.LQ_ERR_ALIGNMENT
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 2.9e38])
+def test_scale_whose_base_2_form_is_infinite(L, scale):
+    c = _lq.lq_kv_cache(A16, 10, 64, 8, 128, 4)
+    a = _lq.lq_kv_attention_args(A16 + 8, A16, A16, 2, 3, 2, 32, 4096, 4096, A16, 5, 5, A16, A16, 100, scale)
+    assert L.lq_kv_attention(H, ctypes.byref(c), ctypes.byref(a), None) == _lq.LQ_ERR_INVALID_ARG
+    a.scale = 2.3e38
+    assert L.lq_kv_attention(H, ctypes.byref(c), ctypes.byref(a), None) == _lq.LQ_ERR_ALIGNMENT
