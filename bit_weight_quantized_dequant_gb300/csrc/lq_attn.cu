@@ -33,11 +33,11 @@
 // sums join the rows' own at the end of the second run.  Few rows or a short prefix
 // take this kernel for it, many rows the tensor-memory kernel (lq_attn_prefix.cu).
 //
-// Measured (128 dimensions, bf16): 24 requests of 1 .. 4001 tokens, 40 heads, 8 bits: 577 MB in 95 us,
-// 6.1 TB/s of a copy's 6.7.  One request of 128 Ki tokens, 64 query heads over 8, 4 bits: 168 MB in 49 us;
-// there the loop runs at 5.4 to 5.6 TB/s (ALU pipe 53 %, issue 54 %: 390 instructions per tile and warp),
-// and 3 us of start and 8 us from the last tile to the joined output come on top.  333 tokens, 32 heads:
-// 8.7 us, all latency.
+// Measured (128 dimensions, bf16): 24 requests of 1 .. 4001 tokens, 40 heads, 8 bits: 577 MB in 94 us,
+// 6.1 TB/s of a copy's 6.7.  One request of 128 Ki tokens, 64 query heads over 8, 4 bits: 168 MB in 51 us,
+// twice what its bytes take.  No pipe is full there (ALU 52 %, issue 53 %): 390 instructions per tile and warp in
+// chains that 15 warps per SM do not cover, SMs that end unevenly (75 k to 95 k cycles of 103 k), and 3 us of start
+// and 8 us from the last tile to the joined output.  333 tokens, 32 heads: 9.1 us, all latency.
 
 #include <algorithm>
 #include <mutex>
@@ -50,15 +50,17 @@ namespace {
 // Blocks of 8 warps, two on an SM, where units are few and long (fewer partial sums to join); of 4 warps, four
 // on an SM, where there are more units than blocks, so that more of them are in flight: what a unit costs
 // besides its tiles (its queries, the joining of its warps, its output) is latency.  Measured with
-// 64 requests of 50 .. 200 tokens, 40 kv heads, 8 bits: 56 us with 8 warps, 40 with 4; one request of 128 Ki
-// tokens, 8 kv heads, 4 bits: 49 and 59.
-// What a unit costs a block besides its tiles, in tiles (16 requests of 100 .. 4000 tokens, 8 kv heads, 16 rows: 37.3
-// us with 28 for 8 warps, 35.1 with 40; 26.0 and 27.5 for 24 requests of 8 rows with 40 and 60):
+// 64 requests of 50 .. 200 tokens, 40 kv heads, 8 bits: 61.9 us with 8 warps, 43.9 with 4; 24 requests of 1 .. 4001 tokens, 40
+// kv heads, 8 bits: 97.2 and 93.9; one request of 128 Ki tokens, 8 kv heads, 4 bits: 50.6 and 61.4.
+// What a unit costs a block besides its tiles, in tiles (100 .. 4000 tokens a request, 8 kv heads, 4 bits; 28, 40 and 60
+// for 8 warps: 16 requests of 16 rows 39.8, 35.6 and 35.1 us; 24 requests of 8 rows 31.1, 31.2 and 32.9):
 template <int W>
 constexpr int kUnitCost = W == 8 ? 40 : 20;
 // Warps that share an SM's registers: 16, with 128 each.  16 rows of 128 dimensions do not fit that (600 bytes a
-// thread spilled): 8, with 255.  Measured with 16 rows: 64 Ki tokens, 8 kv heads, 4 bits, 62.9 us with 16 warps and
-// 40.5 with 8; in 8 bits 70.8 and 41.7.  8 rows and 64 dimensions: 32.3 with 16, 38.1 with 8.
+// thread spilled): 8, with 255.  Measured with 16 rows: 64 Ki tokens, 8 kv heads, 4 bits, 64.8 us with 16 warps and
+// 40.7 with 8; in 8 bits 73.5 and 41.6.  8 rows of 128 dimensions, 16 and 8 warps: ragged batch as above 93.9 and 99.9, 64
+// short requests 43.9 and 52.3, but one request of 128 Ki tokens 50.6 and 49.5 (8 bits 59.0 and 56.7).  4 rows of 64
+// dimensions, 32 requests of 100 .. 16000 tokens, 4 bits: 54.6 and 72.6.
 template <int D, int NT>
 constexpr int kWarpsPerSm = NT == 2 && D == 128 ? 8 : 16;
 constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block takes one piece
@@ -66,8 +68,8 @@ constexpr int kPiece = 24;       // tiles of a piece of a unit, where one block 
 // kLeastS or more, so that the multiplication is skipped; otherwise it brings the largest into [1, 2), and goes down
 // when a larger one comes.  S 2^ks is exact, and P S 2^ks off by 2^-25 at most.  An S above kMostS among others
 // below, as a wide value group has it (a clamped infinity: 513 in 8 bits), moves no power of two, which would cost
-// every other token its bits: such products are taken one by one, in fp32.  (128 Ki tokens, 4 bits: 51 us, 283 if
-// all were taken so; where all of a group's are wide together, ks is below 0 and it takes 63.)
+// every other token its bits: such products are taken one by one, in fp32.  (128 Ki tokens, 4 bits: 51 us, 347 if
+// all were taken so; where all of a group's are wide together, ks is below 0 and it takes 62.)
 constexpr float kMostS = 3.875f, kLeastS = 0x1p-8f;
 constexpr uint32_t kMostS2 = 0x43c043c0u, kLeastS2 = 0x1c001c00u;   // (two of each in binary16)
 constexpr uint32_t kUnset = 1u << 31, kNoScales = 0x0e0e0e0eu;
@@ -239,7 +241,7 @@ __device__ __forceinline__ uint32_t choose_scales(const uint8_t* tile, State<D, 
 // Rows see seen[] tokens of the request's len (kEdge: some row may not see the whole tile).
 // kFine (binary16 outputs, whose own rounding is four times finer than bfloat16's): what the rounding of P S
 // left out is multiplied too (error against 64 bits 4.2e-4 -> 2.7e-4 of the output at four tokens of 8
-// requests, where rounding the output alone gives 2.1e-4; 21.1 -> 21.3 us).
+// requests, where rounding the output alone gives 2.1e-4; 20.5 -> 21.3 us).
 template <int BITS, int D, int NT, bool kEdge, bool kFine>
 __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS, D, NT>& Q, State<D, NT>& A, int j0, int len,
                                           const int (&seen)[NT][2], int lane) {

@@ -30,8 +30,9 @@
 // on with what is there, so every loop and barrier still ends, and the status word reports it.
 //
 // Measured with 48 requests of 64 query heads over 8 (128 dimensions, bf16) and 32100 shared tokens in 4
-// bits: 80 us (485 with the kernel of lq_attn.cu).  A block of 128 keys takes 3700 cycles, of which its MMAs
-// are 1607 (tensor pipe 43 %): codes becoming operands and the softmax bound it (issue 66 %, ALU 57 %).
+// bits: 85 us, and 116 the whole call (338 with the kernel of lq_attn.cu for the prefix).  A block of 128 keys takes
+// 3870 cycles, of which its MMAs are 1607 (tensor pipe 41 %): codes becoming operands, which each of the three row
+// tiles of a kv head expands for itself, and the softmax bound it (issue 65 %, ALU 56 %).
 
 #include <algorithm>
 #include <mutex>
@@ -594,11 +595,18 @@ int64_t key_places(int kv_heads, int all_rows, int prefix_len) {
 }  // namespace
 
 // Taken from 17 rows per kv head (where the other kernel reads the prefix once per 16 rows) and 385 shared tokens
-// on (where the other cuts a unit into pieces and joins them).  Measured (whole call, 128 dimensions, 4 bits; this
-// kernel and the other, us), 8 kv heads over 256 / 1000 / 16000 tokens: 20 rows, 1000 and 16000: 15.2, 20.3 / 28.0,
-// 32.7; 32 rows 15.1, 16.0 / 16.4, 20.7 / 29.9, 33.4; 64 rows 17.4, 16.2 / 18.4, 21.0 / 31.0, 46.7; 128 rows 20.9,
-// 16.5 / 20.9, 24.5 / 34.2, 71.8.  16 rows: 15.0, 20.2 over 1000 tokens with 8 heads, but 29.3, 27.9 over 16000 and
-// 64.9, 51.5 with 32 heads.  8 bits: the same within 10 %.
+// on (where the other cuts a unit into pieces and joins them).  Measured (whole call, 128 dimensions, 4 bits, one own token;
+// this kernel and the other, us) over 256 / 384 / 1000 / 4000 / 16000 tokens, 8 kv heads unless it says 32:
+//     17 rows         18.5, 19.5 / 18.6, 20.4 / 19.4, 24.6 / 22.8, 25.7 / 30.9, 34.9
+//     17 rows, 32     20.9, 19.9 / 21.4, 21.0 / 23.3, 28.8 / 32.4, 37.0 / 66.9, 74.7
+//     136 of group 8  22.7, 20.3 / 22.8, 20.9 / 25.0, 30.0 / 29.9, 39.3 / 47.4, 78.0
+//     512 of group 8  27.4, 31.1 / 27.3, 37.5 / 29.5, 46.1 / 38.4, 79.4 / 72.5, 218
+//     8192 of group 8 208, 254 / 214, 278 / 256, 406 / 400, 934
+//     1024 of group 1 129, 126 / 131, 130 / 137, 145 / 155, 209 / 221, 479
+//     1024, 32        478, 479 / 483, 495 / 506, 557 / 584, 825
+// So up to 384 tokens the other one is as good or better up to 200 rows, and gives away up to a quarter from 512 rows of
+// wide groups on.  Earlier figures for 16 rows: 15.0, 20.2 over 1000 tokens with 8 heads, but 29.3, 27.9 over 16000 and 64.9,
+// 51.5 with 32 heads.  8 bits: the same within 10 %.
 size_t prefix_tc_bytes(lq_handle h, int kv_heads, int all_rows, int prefix_len, int D) {
     const int64_t n = key_places(kv_heads, all_rows, prefix_len);
     if (all_rows <= 16 || prefix_len <= 384 || n > 0x7fffffffLL) return 0;

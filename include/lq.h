@@ -537,7 +537,9 @@ LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t
  * lq_kv_attention — attention of the newest `tokens` (1 .. 64) tokens of each of `batch`
  * (1 .. 1024) requests over the cache: for query head h of token t of request b,
  *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
- * over kv head h / (q_heads / kv_heads) and these keys j, in 32-bit statistics:
+ * over kv head h / (q_heads / kv_heads) and these keys j.  Scores, their statistics and all sums
+ * are held in 32 bits; probabilities, and their products with a value group's S, are rounded to
+ * 11 bits before the second product (for binary16 outputs the second rounding is made up for):
  *   - the prefix_len tokens of the pages prefix_table[], which all requests share: their
  *     part is computed once for all requests' rows together (from 17 rows per kv head and
  *     385 tokens on as a dense product whose values are rounded to binary16);
