@@ -910,13 +910,13 @@ lq_status attend(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& 
 }  // namespace
 
 lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, cudaStream_t stream) {
-    // all requests at once where the workspace has room for that, otherwise so many at a time that it has
+    // all requests at once where the workspace and 32-bit indices have room for that, otherwise so many at a time that they have
     int n = a.batch;
     for (;; n = (n + 1) / 2) {
         lq_status s = attend(h, c, a, 0, n, false, stream);
         if (s == LQ_OK && a.batch % n) s = attend(h, c, a, 0, a.batch % n, false, stream);
         if (s == LQ_OK) break;
-        if (s != LQ_ERR_WORKSPACE || n == 1) return s;
+        if ((s != LQ_ERR_WORKSPACE && s != LQ_ERR_UNSUPPORTED) || n == 1) return s;
     }
     for (int first = 0; first < a.batch; first += n) {
         const lq_status s = attend(h, c, a, first, std::min(n, a.batch - first), true, stream);

@@ -49,3 +49,13 @@ def test_without_room_for_one_request_nothing_is_written(lqm):  # noqa: F811
     torch.cuda.synchronize()
     assert bool((out == 7).all()) and bool((lse == 7).all())
     h.close()
+
+
+def test_more_tiles_than_an_index_counts(lqm, handle):  # noqa: F811
+    """1024 requests of 64 tokens, 64 query heads over 8, page lists that reach 128 Ki tokens: every limit of the header is
+    kept, and the tiles that the lists could hold, counted for every 16 rows, pass 2^31.  In turns."""
+    c = Case(lqm, _lens(1024, 81), T=64, hq=64, hkv=8, D=64, page=80, seed=5)
+    c.bt = np.ascontiguousarray(np.repeat(c.bt, 1639, 1))        # (tokens past a length are never looked up)
+    assert (1639 * 80 // 16) * 1024 * 8 * 32 > 2 ** 31
+    c.check(*c.run(handle), requests=[0, 255, 511, 512, 1023])
+    handle.sync()
