@@ -394,12 +394,12 @@ __device__ __forceinline__ void tile_step(const uint8_t* tile, const QFrag<BITS,
 #pragma unroll 1
             for (uint32_t rest = wide; rest; rest &= rest - 1) {
                 const int j = __ffs((int)rest) - 1;
-                float f[NT][2];   // P of rows 2 t, 2 t + 1
+                float f[NT][2];   // P of rows 2 t, 2 t + 1, rounded as it is against Z: the two parts of a value cancel where it is small
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        f[nt][i] = __shfl_sync(0xffffffffu, ex2((j & 8 ? x[nt][i + 2] : x[nt][i]) - A.ref[nt][i]), 4 * (j & 7) + t);
+                        f[nt][i] = __half2float(__float2half_rn(__shfl_sync(0xffffffffu, ex2((j & 8 ? x[nt][i + 2] : x[nt][i]) - A.ref[nt][i]), 4 * (j & 7) + t)));
                 uint32_t w[WV];
 #pragma unroll
                 for (int i = 0; i < WV; ++i) w[i] = lds32(tile + L::kVc + kv_word_at(4 * n + ((j & 7) >> 1), ((j & 1) + 2 * (j >> 3)) * WV + i));

@@ -147,3 +147,30 @@ def test_groups_and_tokens_of_many_sizes(lqm, handle, bits, D):  # noqa: F811
                 e.token(0, j, h, _set_value([grp], S, np.float16(-0.5 * top) * S))
     e.done()
     _tight(c, *c.run(handle), _spans(c, {(0, j): 512.0 for j in range(7, 700, 50)}))
+
+
+@pytest.mark.parametrize("bits,D", SHAPES)
+def test_small_values_of_a_wide_group_come_out_small(lqm, handle, bits, D):  # noqa: F811
+    """A wide group whose codes make S c + Z zero: with the token's probability rounded the same against both parts they cancel,
+    to fp32's rounding of sums as large as p |Z| (2^-24 a step, below 2^-20 in all), beside the ordinary bound of the rest."""
+    c = Case(lqm, [90], hq=2, hkv=2, D=D, bits=bits, dtype="f16", seed=9, poison=False)
+    e, S, code = Edit(c), np.float16(512.0 if bits == 8 else 4096.0), 100 if bits == 8 else 7
+    for h in range(2):
+        def fn(ko, vo, t):
+            vo[0][t, 32:64], vo[1][t, 1], vo[2][t, 1] = code, S, np.float16(-float(S) * code)
+        e.token(0, 20, h, fn)
+    e.done()
+    assert not c.v[c.bt[0][0], :, 20, 32:64].any()
+    out, lse = c.run(handle)
+    pages, offs = c.tokens(c.bt[0], 90)
+    for h in range(2):
+        k, v, z = (a[pages, h, offs].copy() for a in (c.k, c.v, c.z))
+        big = float(z[20, 32])
+        z[20, 32:64] = 0.0
+        q = c.q[0][:, h:h + 1].float().cpu().numpy()
+        o, s, mass, size = R.attend(q, k, v, [90], c.scale)
+        zmass, size = R.attend(q, k, z, [90], c.scale)[0], size * c.scale
+        p20 = np.exp((q.astype(np.float64) @ k[20].astype(np.float64)) * c.scale - s)[..., None]
+        bound = (2.0 ** -11 + 2.0 ** -18 * (1 + size[..., None])) * (mass + 2 * zmass) + 2.0 ** -11 * np.abs(o) + 2.0 ** -28 * 90
+        bound = bound + np.where((np.arange(D) // 32 == 1)[None, None], p20 * big * 2.0 ** -20, 0.0)
+        assert np.all(np.abs(out[0][:, h:h + 1].float().cpu().numpy() - o) <= bound)
