@@ -15,6 +15,7 @@ LQ_OK, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_ALIGNMENT, LQ_ERR_WORKSPAC
 FMT_2BIT, FMT_NF4, FMT_INT4, FMT_NF4_DQ = 1, 2, 3, 4
 F32, F16, BF16 = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+_INT_MAX = 0x7fffffff       # (larger numbers would lose their upper bits at the C boundary)
 
 #: every entry point include/lq.h declares
 EXPORTED = ("lq_create", "lq_destroy", "lq_status_string", "lq_sync", "lq_dequant", "lq_gemv",
@@ -446,6 +447,8 @@ class Handle:
                    high_rotations=32.0, mscale=1.0, out=None, stream=None):
         """Rows first .. first + count - 1 of the rotation table, fp32 [count][rot_dim]: cosines, then
         sines.  factor stretches the positions: every frequency (original_length 0) or by parts."""
+        if not (-1 < first <= _INT_MAX and count <= _INT_MAX):
+            raise ValueError("first and count must be below 2^31, first not negative")
         if out is None:
             torch, shape = _torch(), (count, rot_dim)
             out = torch.empty(shape, dtype=torch.float32, device=self._device) if stream is None else \
@@ -469,6 +472,8 @@ class Handle:
                 raise ValueError("out cannot take the rotation of an x that requires a gradient")
             return _rotation().apply(x, self, positions, table, layout, inverse, stream)
         n, heads, dim = shape = x.shape
+        if n > _INT_MAX or heads > _INT_MAX or dim > _INT_MAX:
+            raise ValueError("x has 2^31 or more tokens, heads or dimensions")
         if out is None:
             out = torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None else self._new(shape, x.dtype, stream)
         elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != self.device:

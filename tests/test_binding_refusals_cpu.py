@@ -51,3 +51,15 @@ def test_a_table_without_positions(handle):
         handle.rope(k, None, table, out=k)
     with pytest.raises(ValueError, match="slots"):
         handle.kv_append(Cache(), k, k, None)
+
+
+def test_sizes_past_31_bits(handle):
+    """Numbers that the C boundary would cut to 32 bits: 2^32 + 5 rows are not 5."""
+    for first, count in ((2 ** 32 + 5, 4), (0, 2 ** 32 + 4), (-1, 4), (2 ** 31, 4)):
+        with pytest.raises(ValueError, match="2.31"):
+            handle.rope_table(count, 2, first=first, out=_OnDevice((count, 2), torch.float32))
+    table = _OnDevice((9, 2), torch.float32)
+    for shape in ((2 ** 32 + 5, 1, 2), (1, 2 ** 32 + 5, 2), (1, 1, 2 ** 32 + 6)):
+        x = _OnDevice(shape, torch.float16)
+        with pytest.raises(ValueError, match="2.31"):
+            handle.rope(x, _OnDevice((shape[0],), torch.int32), table, out=x)
