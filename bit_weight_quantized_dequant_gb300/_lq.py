@@ -447,8 +447,8 @@ class Handle:
                    high_rotations=32.0, mscale=1.0, out=None, stream=None):
         """Rows first .. first + count - 1 of the rotation table, fp32 [count][rot_dim]: cosines, then
         sines.  factor stretches the positions: every frequency (original_length 0) or by parts."""
-        if not (-1 < first <= _INT_MAX and count <= _INT_MAX):
-            raise ValueError("first and count must be below 2^31, first not negative")
+        if abs(first) > _INT_MAX or abs(count) > _INT_MAX:
+            raise ValueError("first and count must be below 2^31")
         if out is None:
             torch, shape = _torch(), (count, rot_dim)
             out = torch.empty(shape, dtype=torch.float32, device=self._device) if stream is None else \

@@ -55,7 +55,7 @@ def test_a_table_without_positions(handle):
 
 def test_sizes_past_31_bits(handle):
     """Numbers that the C boundary would cut to 32 bits: 2^32 + 5 rows are not 5."""
-    for first, count in ((2 ** 32 + 5, 4), (0, 2 ** 32 + 4), (-1, 4), (2 ** 31, 4)):
+    for first, count in ((2 ** 32 + 5, 4), (0, 2 ** 32 + 4), (5 - 2 ** 32, 4), (2 ** 31, 4)):
         with pytest.raises(ValueError, match="2.31"):
             handle.rope_table(count, 2, first=first, out=_OnDevice((count, 2), torch.float32))
     table = _OnDevice((9, 2), torch.float32)
