@@ -24,7 +24,7 @@ EXPORTED = ("lq_create", "lq_destroy", "lq_status_string", "lq_sync", "lq_dequan
             "lq_select_anchors", "lq_quantize_2bit", "lq_quantize_nf4",
             "lq_stream_create", "lq_stream_run", "lq_stream_destroy", "lq_stream_run_direct",
             "lq_rope_table", "lq_rope", "lq_kv_tile_bytes", "lq_kv_append", "lq_kv_read", "lq_kv_attention",
-            "lq_selftest_wait")
+            "lq_kv_attention_window", "lq_kv_attention_chunk", "lq_logprobs", "lq_logprobs_grad", "lq_selftest_wait")
 
 _LIB = None
 
@@ -86,6 +86,28 @@ class lq_kv_attention_args(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
                 ("lens", ctypes.c_void_p), ("prefix_table", ctypes.c_void_p), ("prefix_len", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class lq_kv_chunk_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("q_token_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64), ("starts", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("lens", ctypes.c_void_p), ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class lq_logprobs_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("row_stride", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("logprob", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("top", ctypes.c_int), ("top_ids", ctypes.c_void_p),
+                ("top_logprobs", ctypes.c_void_p)]
+
+
+class lq_logprobs_grad_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("d_logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n", ctypes.c_int),
+                ("vocab", ctypes.c_int), ("row_stride", ctypes.c_int64), ("d_row_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("d_logprob", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p)]
 
 
 def library_path() -> Path:
@@ -157,6 +179,14 @@ def load_library(build_if_missing: bool = True):
     L.lq_kv_read.restype = I
     L.lq_kv_attention.argtypes = [P, C, ctypes.POINTER(lq_kv_attention_args), P]
     L.lq_kv_attention.restype = I
+    L.lq_kv_attention_window.argtypes = [P, C, ctypes.POINTER(lq_kv_attention_args), I, I, P]
+    L.lq_kv_attention_window.restype = I
+    L.lq_kv_attention_chunk.argtypes = [P, C, ctypes.POINTER(lq_kv_chunk_args), P]
+    L.lq_kv_attention_chunk.restype = I
+    L.lq_logprobs.argtypes = [P, ctypes.POINTER(lq_logprobs_args), P]
+    L.lq_logprobs.restype = I
+    L.lq_logprobs_grad.argtypes = [P, ctypes.POINTER(lq_logprobs_grad_args), P]
+    L.lq_logprobs_grad.restype = I
     L.lq_selftest_wait.argtypes = [P, ctypes.c_uint, P]
     L.lq_selftest_wait.restype = I
     _LIB = L
@@ -219,6 +249,32 @@ def _rotation():
             return handle.rope(g, positions, table, layout, not inverse), None, None, None, None, None, None
 
     return Rotation
+
+
+@functools.lru_cache(maxsize=None)
+def _scored():
+    """Handle.token_logprobs as a differentiable function of the logits, through the log probabilities and the entropy."""
+    import torch
+
+    class Scored(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, handle, tokens, top, stream):
+            logprob, entropy, lse, ids, best = handle._token_logprobs(logits, tokens, top, stream)
+            ctx.save_for_backward(logits, tokens, lse, entropy)
+            ctx.handle = handle
+            ctx.set_materialize_grads(False)
+            if ids is not None:
+                ctx.mark_non_differentiable(ids, best)
+            return logprob, entropy, ids, best
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, d_logprob, d_entropy, *_):
+            if d_logprob is None and d_entropy is None:
+                return None, None, None, None, None
+            return ctx.handle._token_logprobs_grad(*ctx.saved_tensors, d_logprob, d_entropy), None, None, None, None
+
+    return Scored
 
 
 @dataclass
@@ -542,12 +598,23 @@ class Handle:
             raise LQError(st, "lq_kv_read")
         return k, v
 
+    def _window(self, window, sinks):
+        """(window, sinks) as the library takes them; a window of 0 is none."""
+        if window is None:
+            if sinks:
+                raise ValueError("sinks are of a window, and there is none")
+            return 0, 0
+        if not 1 <= window <= _INT_MAX or not 0 <= sinks <= _INT_MAX:
+            raise ValueError("window must be 1 or more, sinks 0 or more, and both below 2^31")
+        return window, sinks
+
     def kv_attention(self, q, cache: KVCache, block_table, lens, scale=None, prefix_table=None, prefix_len=None, out=None,
-                     lse=None, stream=None):
+                     lse=None, stream=None, window=None, sinks=0):
         """Attention of q [batch][tokens][q_heads][dim] (each request's newest tokens, already in the cache)
         over the cache: request b's own tokens in the pages block_table[b] (int32), lens[b] (int32) of
-        them, after the prefix_len tokens of prefix_table's pages, which all requests share.  Returns
-        out (q's shape and dtype) and the fp32 log-sum-exp [batch][tokens][q_heads]."""
+        them, after the prefix_len tokens of prefix_table's pages, which all requests share.  With a window
+        (and then no prefix) a row sees the last `window` tokens up to its own, and the request's first
+        `sinks`.  Returns out (q's shape and dtype) and the fp32 log-sum-exp [batch][tokens][q_heads]."""
         torch, dev = _torch(), self.device
         B, T, hq, dim = shape = q.shape
         dt, row = q.dtype, hq * dim
@@ -590,10 +657,131 @@ class Handle:
                                  block_table.data_ptr(), bs[0] if B > 1 else pages, pages,
                                  self._indices("lens", lens, torch.int32, B), pp, prefix_len or 0,
                                  dim ** -0.5 if scale is None else scale)
-        st = self._lib.lq_kv_attention(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream))
+        if window is None and not sinks:
+            st = self._lib.lq_kv_attention(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream))
+            if st != LQ_OK:
+                raise LQError(st, "lq_kv_attention")
+            return out, lse
+        st = self._lib.lq_kv_attention_window(self._h, cache._on(dev), ctypes.byref(a), *self._window(window, sinks),
+                                              self._raw(stream))
         if st != LQ_OK:
-            raise LQError(st, "lq_kv_attention")
+            raise LQError(st, "lq_kv_attention_window")
         return out, lse
+
+    def kv_attention_chunk(self, q, cache: KVCache, block_table, lens, starts, scale=None, window=None, sinks=0, out=None,
+                           lse=None, stream=None):
+        """Attention of chunks of new tokens, as many of each request as there are, over the cache they are in
+        already: request b's rows of q [tokens][q_heads][dim] are starts[b] .. starts[b + 1] - 1 (int32
+        [batch + 1]), the newest of its lens[b] (int32) tokens in the pages block_table[b] (int32).  Row t sees
+        the tokens up to its own; with a window the last `window` of them and the request's first `sinks`.
+        Returns out (q's shape and dtype) and the fp32 log-sum-exp [tokens][q_heads]; rows that belong to no
+        request are left as they were."""
+        torch, dev = _torch(), self.device
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens][heads][dim]")
+        n, hq, dim = shape = q.shape
+        if n > _INT_MAX:
+            raise ValueError("q has 2^31 or more tokens")
+        dt = q.dtype
+        if dim != cache.head_dim:
+            raise ValueError(f"q must be [tokens][heads][{cache.head_dim}]")
+        qs = self._rows("q", q, n, hq, dim, dt)
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=q.device) if stream is None else self._new(shape, dt, stream)
+            os = hq * dim
+        else:
+            os = self._rows("out", out, n, hq, dim, dt)
+        if lse is None:
+            lse = torch.empty((n, hq), dtype=torch.float32, device=q.device) if stream is None else \
+                self._new((n, hq), torch.float32, stream)
+        elif lse.shape != (n, hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError(f"lse must be contiguous fp32 [tokens][heads] on cuda:{dev}")
+        if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.get_device() != dev:
+            raise ValueError(f"block_table must be int32 [batch][pages] on cuda:{dev}")
+        B, pages = block_table.shape
+        bs = block_table.stride()
+        if bs[1] != 1 and pages > 1:
+            raise ValueError("block_table's rows must be contiguous")
+        if B > _INT_MAX or pages > _INT_MAX:
+            raise ValueError("block_table has 2^31 or more requests or pages")
+        a = lq_kv_chunk_args(q.data_ptr(), out.data_ptr(), lse.data_ptr(), _code(dt), B, n, hq, qs, os,
+                             self._indices("starts", starts, torch.int32, B + 1), block_table.data_ptr(),
+                             bs[0] if B > 1 else pages, pages, self._indices("lens", lens, torch.int32, B),
+                             *self._window(window, sinks), dim ** -0.5 if scale is None else scale)
+        if n == 0:
+            return out, lse
+        st = self._lib.lq_kv_attention_chunk(self._h, cache._on(dev), ctypes.byref(a), self._raw(stream))
+        if st != LQ_OK:
+            raise LQError(st, "lq_kv_attention_chunk")
+        return out, lse
+
+    # ---- log probabilities ----
+
+    def _logits(self, name, t, shape=None):
+        """Row stride of a [n][vocab] operand of this device, vocabulary contiguous."""
+        if t.dim() != 2 or t.get_device() != self.device or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} must be [rows][vocab] on cuda:{self.device}")
+        n, V = t.shape
+        if n > _INT_MAX or V > _INT_MAX:
+            raise ValueError(f"{name} has 2^31 or more rows or tokens")
+        s = t.stride()
+        if s[1] != 1 and V > 1:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        return s[0] if n > 1 else V
+
+    def token_logprobs(self, logits, tokens, top=0, stream=None):
+        """Log probabilities of the given tokens (int64 [rows]; negative: left out, 0) under logits [rows][vocab] of fp32,
+        float16 or bfloat16, the entropy of each row, and its `top` (up to 64) best tokens with theirs.  Returns
+        (logprob, entropy, top_ids, top_logprobs): fp32 [rows] twice, int64 and fp32 [rows][top], equal logits by ascending
+        id (None both without top).  Logits that require a gradient get it through logprob and entropy."""
+        torch = _torch()
+        if logits.requires_grad and torch.is_grad_enabled():
+            if stream is None:
+                return _scored().apply(logits, self, tokens, top, None)
+            with torch.cuda.stream(stream):     # (so that the gradient is computed there too)
+                out = _scored().apply(logits, self, tokens, top, None)
+            for t in out:
+                if t is not None:
+                    t.record_stream(torch.cuda.current_stream(self.device))
+            return out
+        logprob, entropy, _, ids, best = self._token_logprobs(logits, tokens, top, stream)
+        return logprob, entropy, ids, best
+
+    def _token_logprobs(self, logits, tokens, top, stream):
+        torch = _torch()
+        rs = self._logits("logits", logits)
+        n, V = logits.shape
+        if not 0 <= top <= V:
+            raise ValueError("top must be from 0 to the vocabulary's size")
+        tp = self._indices("tokens", tokens, torch.int64, n)
+
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=logits.device) if stream is None else self._new(shape, dtype, stream)
+        logprob, entropy, lse = (new((n,), torch.float32) for _ in range(3))
+        ids = best = None
+        if top:
+            ids, best = new((n, top), torch.int64), new((n, top), torch.float32)
+        a = lq_logprobs_args(logits.data_ptr(), _code(logits.dtype), n, V, rs, tp, logprob.data_ptr(), entropy.data_ptr(),
+                             lse.data_ptr(), top, _ptr(ids), _ptr(best))
+        if n:
+            st = self._lib.lq_logprobs(self._h, ctypes.byref(a), self._raw(stream))
+            if st != LQ_OK:
+                raise LQError(st, "lq_logprobs")
+        return logprob, entropy, lse, ids, best
+
+    def _token_logprobs_grad(self, logits, tokens, lse, entropy, d_logprob, d_entropy):
+        torch = _torch()
+        n, V = logits.shape
+        grads = [None if d is None else d.contiguous() for d in (d_logprob, d_entropy)]
+        d_logits = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        a = lq_logprobs_grad_args(logits.data_ptr(), d_logits.data_ptr(), _code(logits.dtype), n, V,
+                                  self._logits("logits", logits), V, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
+                                  _ptr(grads[0]), _ptr(grads[1]))
+        if n:
+            st = self._lib.lq_logprobs_grad(self._h, ctypes.byref(a), self._raw(None))
+            if st != LQ_OK:
+                raise LQError(st, "lq_logprobs_grad")
+        return d_logits
 
     # ---- quantizers (the converter step; include/lq.h gives the definitions) ----
 

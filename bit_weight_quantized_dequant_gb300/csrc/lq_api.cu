@@ -5,6 +5,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <vector>
 
@@ -492,7 +493,12 @@ LQ_API lq_status lq_kv_read(lq_handle h, const lq_kv_cache* cache, const int64_t
     return lq::launch_kv_read(h, *cache, slots, n, k_out, v_out, dtype, static_cast<cudaStream_t>(stream));
 }
 
-LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, void* stream) {
+namespace {
+
+constexpr int kMostTokens = 0x7fffff00;   // of a request
+
+// window 0: none.
+lq_status kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, int window, int sinks, void* stream) {
     if (!h || !args) return LQ_ERR_INVALID_ARG;
     const lq_status s = check_cache(cache);
     if (s != LQ_OK) return s;
@@ -502,7 +508,7 @@ LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq
     if (a.batch < 1 || a.tokens < 1 || a.q_heads < 1 || a.q_heads % cache->kv_heads != 0) return LQ_ERR_INVALID_ARG;
     if (a.batch > lq::kMaxAttnBatch || a.tokens > lq::kMaxAttnTokens) return LQ_ERR_UNSUPPORTED;
     if (a.max_pages < 1 || a.block_table_stride < a.max_pages || a.prefix_len < 0) return LQ_ERR_INVALID_ARG;
-    if ((int64_t)a.max_pages * cache->page_size > 0x7fffff00LL || a.prefix_len > 0x7fffff00) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)a.max_pages * cache->page_size > kMostTokens || a.prefix_len > kMostTokens) return LQ_ERR_UNSUPPORTED;
     if (a.prefix_len > 0 && !a.prefix_table) return LQ_ERR_INVALID_ARG;
     if ((int64_t)a.q_heads * cache->head_dim > 0x7fffff00LL) return LQ_ERR_UNSUPPORTED;
     if (!(a.scale > 0.f) || !(a.scale < 2.35e38f)) return LQ_ERR_INVALID_ARG;   // (times log2 e it has to be finite)
@@ -512,7 +518,86 @@ LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq
         return LQ_ERR_ALIGNMENT;
     DeviceGuard guard(h->device);
     if (!guard.ok) return LQ_ERR_CUDA;
-    return lq::launch_kv_attention(h, *cache, a, static_cast<cudaStream_t>(stream));
+    return lq::launch_kv_attention(h, *cache, a, std::min(window, kMostTokens), std::min(sinks, kMostTokens), static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, void* stream) {
+    return kv_attention(h, cache, args, 0, 0, stream);
+}
+
+LQ_API lq_status lq_kv_attention_window(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, int window, int sinks,
+                                        void* stream) {
+    if (window < 1 || sinks < 0) return LQ_ERR_INVALID_ARG;
+    if (args && args->prefix_len != 0) return args->prefix_len < 0 ? LQ_ERR_INVALID_ARG : LQ_ERR_UNSUPPORTED;
+    return kv_attention(h, cache, args, window, sinks, stream);
+}
+
+LQ_API lq_status lq_kv_attention_chunk(lq_handle h, const lq_kv_cache* cache, const lq_kv_chunk_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_status s = check_cache(cache);
+    if (s != LQ_OK) return s;
+    lq_kv_chunk_args a = *args;
+    if (!a.q || !a.out || !a.starts || !a.block_table || !a.lens) return LQ_ERR_INVALID_ARG;
+    if (a.dtype != LQ_F16 && a.dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
+    if (a.batch < 1 || a.tokens < 0 || a.q_heads < 1 || a.q_heads % cache->kv_heads != 0) return LQ_ERR_INVALID_ARG;
+    if (a.max_pages < 1 || a.block_table_stride < a.max_pages || a.window < 0 || a.sinks < 0) return LQ_ERR_INVALID_ARG;
+    if (a.batch > lq::kMaxAttnBatch || (int64_t)a.max_pages * cache->page_size > kMostTokens) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)a.q_heads * cache->head_dim > kMostTokens) return LQ_ERR_UNSUPPORTED;
+    // (rows of a kv head count in 32 bits, with a request's last tile filled up)
+    if ((int64_t)a.tokens * (a.q_heads / cache->kv_heads) > 0x7fff0000LL) return LQ_ERR_UNSUPPORTED;
+    if (!(a.scale > 0.f) || !(a.scale < 2.35e38f)) return LQ_ERR_INVALID_ARG;   // (times log2 e it has to be finite)
+    const uintptr_t words = reinterpret_cast<uintptr_t>(a.block_table) | reinterpret_cast<uintptr_t>(a.lens) |
+                            reinterpret_cast<uintptr_t>(a.starts) | reinterpret_cast<uintptr_t>(a.lse);
+    if (!aligned_rows(a.q, a.q_token_stride, a.dtype) || !aligned_rows(a.out, a.out_token_stride, a.dtype) || (words & 3))
+        return LQ_ERR_ALIGNMENT;
+    if (a.tokens == 0) return LQ_OK;
+    a.window = std::min(a.window, kMostTokens), a.sinks = std::min(a.sinks, kMostTokens);
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_kv_chunk(h, *cache, a, static_cast<cudaStream_t>(stream));
+}
+
+// ---- log probabilities -------------------------------------------------------------
+
+namespace {
+
+bool aligned_to(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+}  // namespace
+
+LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_logprobs_args& a = *args;
+    if (!a.logits || !a.tokens || !a.logprob || !valid_dtype(a.dtype)) return LQ_ERR_INVALID_ARG;
+    if (a.n < 0 || a.vocab < 1 || a.top < 0 || a.top > a.vocab) return LQ_ERR_INVALID_ARG;
+    if (a.top > 0 && (!a.top_ids || !a.top_logprobs)) return LQ_ERR_INVALID_ARG;
+    if (a.top > lq::kMaxLogprobTop || a.vocab > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
+    if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) || !aligned_to(a.top_ids, 8) || !aligned_to(a.logprob, 4) ||
+        !aligned_to(a.entropy, 4) || !aligned_to(a.lse, 4) || !aligned_to(a.top_logprobs, 4))
+        return LQ_ERR_ALIGNMENT;
+    if (a.n == 0) return LQ_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_logprobs(h, a, static_cast<cudaStream_t>(stream));
+}
+
+LQ_API lq_status lq_logprobs_grad(lq_handle h, const lq_logprobs_grad_args* args, void* stream) {
+    if (!h || !args) return LQ_ERR_INVALID_ARG;
+    const lq_logprobs_grad_args& a = *args;
+    if (!a.logits || !a.d_logits || !a.tokens || !a.lse || !valid_dtype(a.dtype)) return LQ_ERR_INVALID_ARG;
+    if (a.n < 0 || a.vocab < 1 || (a.d_entropy && !a.entropy)) return LQ_ERR_INVALID_ARG;
+    if (a.vocab > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
+    if (a.n > 1 && a.d_row_stride < a.vocab) return LQ_ERR_INVALID_ARG;
+    if (a.d_logits == a.logits && a.n > 1 && a.d_row_stride != a.row_stride) return LQ_ERR_INVALID_ARG;
+    if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.d_logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) ||
+        !aligned_to(a.lse, 4) || !aligned_to(a.entropy, 4) || !aligned_to(a.d_logprob, 4) || !aligned_to(a.d_entropy, 4))
+        return LQ_ERR_ALIGNMENT;
+    if (a.n == 0) return LQ_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LQ_ERR_CUDA;
+    return lq::launch_logprobs_grad(h, a, static_cast<cudaStream_t>(stream));
 }
 
 // ---- the allocation-free GEMV entry point ---------------------------------------

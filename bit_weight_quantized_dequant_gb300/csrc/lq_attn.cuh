@@ -37,6 +37,7 @@ struct AttnParams {
     int all_rows;                        // rows of all requests per kv head
     int prefix;                          // 0: none, 1: this is the prefix run, 2: join the prefix's rows
     int* status;
+    int window, sinks;                   // (attn_kernel<kWin>) a row sees its last `window` tokens and the first `sinks`
 };
 
 // n / d for a quotient below 2^20 (n, d > 0): a reciprocal and one correction.
@@ -265,6 +266,17 @@ __device__ __forceinline__ void join(const AttnParams& P, int c0, int c1, int wa
         finish_row<D, T>(P, row0 + r, head, top, l, v, lane);
     }
 }
+
+// A run's scratch, and whether it is only to be asked for (launch false).
+struct Scratch {
+    char* at;
+    size_t room, need;
+    bool launch;
+    cudaStream_t stream;
+};
+
+// A run of requests through a sliding window (P.window, P.sinks).
+lq_status run_attn_window(lq_handle h, AttnParams& P, int bits, int D, bool bf16, Scratch s);
 
 // The shared prefix's run on the tensor-memory tensor cores, which leaves partial sums in `scratch`.
 // prefix_tc_bytes: what it needs of that, 0 where the other kernel takes the prefix.

@@ -1,0 +1,751 @@
+// Attention of chunks of new tokens over the low-bit KV cache, on the tensor-memory tensor cores.
+//
+// A unit is 128 rows of one kv head of one request (rows are (new token, query head of the group), tokens slower) and the key
+// blocks that they see: a dense contraction as in lq_attn_prefix.cu, whose roles, operands and precision this kernel has, with
+// these differences.
+//   - Every request has rows, pages and a length of its own, read on the device.  All units' key blocks form one sequence,
+//     each unit counted with its fixed cost, which the thread blocks share evenly (lq_chunk.h); a unit that is cut
+//     leaves partial sums in the workspace, and the last of its thread blocks to arrive joins them in order.
+//   - A row sees the tokens up to its own, and with a window the last of them and the sinks.  Blocks that no row of the unit
+//     sees are not visited; in one that not every row sees whole, scores are masked by two bounds per row.
+//   - A P of 0 times a cached NaN is NaN, so a value group (token and 32 dimensions) whose S or Z is no number counts as 0
+//     in the product, and rows that do see it get NaN in those dimensions at the unit's end.
+
+#include <algorithm>
+#include <mutex>
+
+#include "lq_attn_tc.cuh"
+#include "lq_chunk.h"
+
+namespace lq {
+namespace {
+
+struct ChunkParams {
+    KvView cache;
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_stride, out_stride, bt_stride;
+    const int32_t *block_table, *lens, *starts;
+    int requests, tokens, group, q_heads, max_len;
+    int window, sinks;
+    float scale_log2;
+    float* part;           // partial sums: 2 slots per thread block
+    unsigned* counters;    // one per thread block, zero between calls
+    int* status;
+};
+
+constexpr int kRows = 128;          // rows of a unit
+constexpr int kKeys = kTcKeys;      // keys of a block
+static_assert(kKeys == kChunkKeys, "key blocks");
+constexpr int kHalf = 4;            // tiles of half a block, which are loaded and expanded together
+constexpr int kSoftWarps = 8, kDqWarps = 16;
+// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those
+// of one scheduler (number mod 4 = 0) issue MMAs, load and expand one tile; the other three schedulers' expand.
+constexpr int kMmaWarp = 8, kLoadWarp = 12, kDqLast = 20, kWarpsAll = 28;   // (the load warps: 12 and 16)
+constexpr int kThreads = 32 * kWarpsAll;
+__device__ __forceinline__ int dq_index(int warp) {   // which expanding warp, -1: none
+    if (warp < kSoftWarps) return -1;
+    if (warp % 4 == 0) return warp == kDqLast ? kDqWarps - 1 : -1;
+    return (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
+}
+// tensor memory columns
+constexpr int kTmemCols = 512;
+constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
+constexpr int kColO = 256;          // D
+constexpr int kColQ = 384;          // D / 2
+constexpr int kColZ = 448;          // 8 (group sums of q), 32 written
+static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 32 <= kTmemCols, "tensor memory");
+
+template <int BITS, int D>
+struct ChunkSmem {
+    using L = KvLayout<BITS, D>;
+    static constexpr int kAtoms = TcOperand<D>::kAtoms, kAtom = TcOperand<D>::kAtom;
+    static constexpr int kKStage = 2 * kAtoms * kAtom;           // K rounded, K's rest
+    static constexpr int kVAtom = D * 128;                       // [D][64 keys]
+    static constexpr int kRawTile = L::kCodes + 2 * L::kMeta;    // a tile's keys (or values): codes, S, Z
+    static constexpr int kRawStage = kHalf * kRawTile;
+    static constexpr int kRawK = L::kBytes <= 2560 ? 4 : 2, kRawV = L::kBytes <= 2560 ? 4 : 2;   // half blocks in flight
+    static constexpr int kK = 0;
+    static constexpr int kZ = kK + 2 * kKStage;                  // Z of stage b in chunk 2 b of each key's row
+    static constexpr int kV = kZ + kAtom;
+    static constexpr int kRawOff = kV + 2 * kVAtom;
+    static constexpr int kMl = kRawOff + (kRawK + kRawV) * kRawStage;       // [2 halves][rows] maxima, then sums
+    static constexpr int kF = kMl + 2 * kRows * 4;               // [rows] score factors
+    static constexpr int kBad = kF + kRows * 4;                  // [2][keys] groups of a value that are no numbers
+    static constexpr int kBars = kBad + 2 * kKeys;
+    static constexpr int kNumBars = 2 * (kRawK + kRawV) + 2 * 3 + 3;
+    static constexpr int kSize = 1024 + kBars + 8 * kNumBars;
+    static_assert(kSize <= 226 * 1024 && kBars % 8 == 0 && kRawOff % 128 == 0 && kRawStage % 16 == 0, "shared memory");
+    static_assert(8 * (kMaxAttnBatch + 1) <= 2 * kKStage, "the requests' running sums lie where K will");
+};
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
+// Whether any thread of a row's two warps says so (and a barrier of the two).
+__device__ __forceinline__ bool pair_any(int pair, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)mine), "r"(2 + pair)
+        : "memory");
+    return any != 0;
+}
+
+// The bits below n of 32 (n of any sign).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// A place in the sequence of units: the request, the row tile, the kv head.
+struct Unit {
+    int b, rt, head;
+};
+
+// Requests as the kernel sees them: whatever the arrays hold, rows stay within the call's.
+struct Request {
+    int row0, fresh, len;
+    __device__ __forceinline__ Request(const ChunkParams& P, int b) {
+        row0 = min(max(P.starts[b], 0), P.tokens);
+        fresh = min(max(P.starts[b + 1], row0), P.tokens) - row0;
+        len = min(max(P.lens[b], 0), P.max_len);
+    }
+};
+__device__ __forceinline__ ChunkTile tile_of(const ChunkParams& P, const Request& q, int rt) {
+    return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, kRows, rt);
+}
+
+// A thread block's share: from block `j0` of unit `first` (at `place` of the sequence) to before block `j1` of unit `last`.
+struct Range {
+    Unit first, last;
+    int j0, j1;
+    int64_t place;
+    bool none;
+};
+
+// A walk over a share's units; every role has one.
+struct Walk {
+    const ChunkParams& P;
+    Range R;
+    Unit u;
+    Request q;
+    ChunkTile t;
+    int j0, j1;          // blocks of this unit that are this thread block's
+    int64_t place;       // of the unit's cost, its blocks follow
+    bool more;
+    __device__ __forceinline__ Walk(const ChunkParams& P_, const Range& r)
+        : P(P_), R(r), u(r.first), q(P_, r.first.b), t(tile_of(P_, q, r.first.rt)), place(r.place), more(!r.none) {
+        j0 = r.j0;
+        set_end();
+    }
+    __device__ __forceinline__ bool at_last() const { return u.b == R.last.b && u.rt == R.last.rt && u.head == R.last.head; }
+    __device__ __forceinline__ void set_end() {
+        j1 = at_last() ? R.j1 : t.blocks;
+        if (j1 <= j0) more = false;
+    }
+    __device__ __forceinline__ void next() {
+        if (at_last()) {
+            more = false;
+            return;
+        }
+        place += t.blocks + kChunkUnitCost;
+        j0 = 0;
+        if (++u.head == P.cache.kv_heads) {
+            u.head = 0;
+            if (++u.rt == chunk_tiles(q.fresh, P.group, kRows)) {
+                u.rt = 0;
+                do ++u.b; while (Request(P, u.b).fresh == 0);   // (the last unit lies ahead)
+                q = Request(P, u.b);
+            }
+            t = tile_of(P, q, u.rt);
+        }
+        set_end();
+    }
+};
+
+// (All threads of a block together.)  The share of block c of C; `cum` has room for requests + 1 sums.
+__device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, int64_t* cum, int64_t* total_out, Range* out) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // places of each request
+    for (int b = warp; b < P.requests; b += kWarpsAll) {
+        const Request q(P, b);
+        if (lane == 0 && c == 0) {
+            const int a0 = P.starts[b], a1 = P.starts[b + 1];
+            if (a0 < 0 || a1 < a0 || a1 > P.tokens) atomicOr(P.status, kStatusIndex);
+        }
+        const int tiles = chunk_tiles(q.fresh, P.group, kRows);
+        int64_t sum = 0;
+        for (int rt = lane; rt < tiles; rt += 32) sum += tile_of(P, q, rt).blocks + kChunkUnitCost;
+#pragma unroll
+        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) cum[b + 1] = sum * P.cache.kv_heads;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t base = 0;
+        for (int b0 = 0; b0 < P.requests; b0 += 32) {
+            int64_t v = b0 + lane < P.requests ? cum[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, v, s);
+                if (lane >= s) v += x;
+            }
+            if (b0 + lane < P.requests) cum[b0 + lane + 1] = base + v;
+            base += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) cum[0] = 0;
+        __syncwarp();
+        const int64_t total = base;
+        const WideShares shares(total, C);
+        // the unit and block at or after a place: lane-parallel over the row tiles of its request
+        auto find = [&](int64_t at, Unit& u, int& j, int64_t& place) {
+            int lo = 0, hi = P.requests - 1;             // the last request that begins at or before `at` (and has rows)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cum[mid] <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            u.b = lo;
+            const Request q(P, lo);
+            const int tiles = chunk_tiles(q.fresh, P.group, kRows), heads = P.cache.kv_heads;
+            int64_t from = cum[lo];
+            for (int r0 = 0; r0 < tiles; r0 += 32) {
+                const int64_t each = r0 + lane < tiles ? tile_of(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
+                int64_t v = each * heads;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, v, s);
+                    if (lane >= s) v += x;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, r0 + lane < tiles && from + v > at);
+                if (past) {
+                    const int who = __ffs((int)past) - 1;
+                    const int64_t e = __shfl_sync(0xffffffffu, each, who), end = from + __shfl_sync(0xffffffffu, v, who);
+                    const int64_t in = at - (end - e * heads);
+                    u.rt = r0 + who;
+                    u.head = (int)(in / e);
+                    place = end - e * heads + u.head * e;
+                    const int k = (int)(at - place);
+                    j = k > kChunkUnitCost ? k - kChunkUnitCost : 0;
+                    return;
+                }
+                from += __shfl_sync(0xffffffffu, v, 31);
+            }
+        };
+        Range r;
+        const int64_t g0 = shares.first(c), g1 = shares.first(c + 1);
+        r.none = g0 >= g1;
+        r.first = r.last = Unit{0, 0, 0};
+        r.j0 = r.j1 = 0;
+        r.place = 0;
+        if (!r.none) {
+            int64_t last_place;
+            int j_last;
+            find(g0, r.first, r.j0, r.place);
+            find(g1 - 1, r.last, j_last, last_place);
+            // blocks of the last unit before place g1
+            const int64_t k = g1 - last_place - kChunkUnitCost;
+            r.j1 = k > 0 ? (int)k : 0;
+            const bool same = r.first.b == r.last.b && r.first.rt == r.last.rt && r.first.head == r.last.head;
+            r.none = same && r.j1 <= r.j0;
+        }
+        if (lane == 0) *out = r, *total_out = total;
+    }
+    __syncthreads();
+    return *out;
+}
+
+// Value groups of one tile whose S or Z is no number are left out of meta (made 0) and recorded in bad[16], a bit per group
+// of the tile's tokens.  Returns whether there is one.
+template <int BITS, int D>
+__device__ __forceinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, int lane) {
+    using L = KvLayout<BITS, D>;
+    constexpr int G = D / 32;
+    uint2 x = make_uint2(0u, 0u);          // four of the S and Z
+    if (8 * lane < 2 * L::kMeta) x = lds64(meta + 8 * lane);
+    const uint32_t top = ((x.x & 0x7c007c00u) + 0x04000400u) | ((x.y & 0x7c007c00u) + 0x04000400u);   // (a carry where an exponent is all ones)
+    if (!__any_sync(0xffffffffu, (top & 0x80008000u) != 0)) return false;
+    if (lane < 16) {       // lane: the token's place in the rows of S and Z
+        uint32_t mask = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            uint16_t* s = reinterpret_cast<uint16_t*>(meta + g * 32 + 2 * lane);
+            uint16_t* z = reinterpret_cast<uint16_t*>(meta + L::kMeta + g * 32 + 2 * lane);
+            if ((*s & 0x7c00u) == 0x7c00u || (*z & 0x7c00u) == 0x7c00u) {
+                mask |= 1u << g;
+                *s = *z = 0;
+            }
+        }
+        // place 4 q + e holds token 2 q + (e & 1) + 8 (e >> 1)
+        bad[2 * (lane >> 2) + (lane & 1) + 8 * (lane >> 1 & 1)] = (uint8_t)mask;
+    }
+    __syncwarp();
+    return true;
+}
+
+template <int BITS, int D, class T>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams P) {
+    using L = KvLayout<BITS, D>;
+    using M = ChunkSmem<BITS, D>;
+    constexpr int G = D / 32, kRawAll = M::kRawK + M::kRawV;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms)
+    float* ml = reinterpret_cast<float*>(base + M::kMl);
+    float* factors = reinterpret_cast<float*>(base + M::kF);
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile uint32_t s_there[2][16];   // a half block's tiles in the cache, keys' and values' (no role is 16 ahead of another)
+    __shared__ volatile unsigned long long s_odd[2];   // a byte per tile of a block: whether it has values that are no numbers
+    __shared__ Range s_range;
+    __shared__ int64_t s_total;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const uint32_t bars = smem_u32(base + M::kBars);
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * kRawAll, k_full = raw_empty + 8 * kRawAll, s_full = k_full + 16;
+    const uint32_t p_full = s_full + 16, v_full = p_full + 16, o_done = v_full + 8, q_full = o_done + 8;
+    if (tid == 0) {
+        for (int i = 0; i < kRawAll; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, kHalf);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full + 8 * b, 2 * kHalf);
+            mbar_init(s_full + 8 * b, 1);
+            mbar_init(p_full + 8 * b, kSoftWarps);
+        }
+        mbar_init(v_full, 2 * kHalf);
+        mbar_init(o_done, 1);
+        mbar_init(q_full, 4);
+        fence_mbar_init();
+    }
+    // (the odd chunks of the Z rows multiply nothing: zero for good)
+    for (int i = tid; i < M::kAtom / 16; i += kThreads) sts128(base + M::kZ + 16 * i, 0, 0, 0, 0);
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int c = blockIdx.x, C = gridDim.x;
+    const Range R = range_of(P, c, C, reinterpret_cast<int64_t*>(base + M::kK), &s_total, &s_range);
+    int own_abort = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded(bar, parity & 1u, &own_abort, P.status); };
+
+    if (warp == kLoadWarp || warp == kLoadWarp + 4) {
+        // ---------------------------------------------------------------- keys' or values' bytes into their ring
+        const int what = warp != kLoadWarp, ring = what ? M::kRawV : M::kRawK, first = what ? M::kRawK : 0;
+        const uint32_t full = raw_full + 8 * first, empty = raw_empty + 8 * first;
+        const uint32_t dst0 = smem_u32(base + M::kRawOff + first * M::kRawStage);
+        int s = 0, turn = -1, i = 0;             // half blocks
+        for (Walk w(P, R); w.more; w.next()) {
+            const int n = 2 * (w.j1 - w.j0);
+            const int32_t* table = P.block_table + w.u.b * P.bt_stride;
+            const int end = min(w.t.p1 + 1, w.q.len);
+            const uint8_t* src = nullptr;
+            for (int k = 0; k < n; ++k, ++i) {
+                if (k % 8 == 0) {                // addresses of four blocks' tiles, one per lane
+                    const int j = w.j0 + (k + lane / kHalf) / 2;
+                    src = nullptr;
+                    if (j < w.j1) {
+                        const int tile = w.t.block(j) * 2 * kHalf + lane % (2 * kHalf);
+                        if (tile * kKvTile < end) {
+                            const int pi = tile / P.cache.tiles_per_page, page = table[pi];
+                            if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
+                            else
+                                src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + w.u.head) * P.cache.tiles_per_page +
+                                                       (tile - pi * P.cache.tiles_per_page)) * (int64_t)L::kBytes;
+                        }
+                    }
+                }
+                if (turn >= 0) wait(empty + 8 * s, turn);
+                __syncwarp();
+                const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (k % 8 * kHalf)) & ((1u << kHalf) - 1u);
+                if (lane == 0) {
+                    s_there[what][i & 15] = there;
+                    if (there) mbar_arrive_expect_tx(full + 8 * s, __popc(there) * M::kRawTile);
+                    else mbar_arrive(full + 8 * s);
+                }
+                __syncwarp();
+                if (lane / kHalf == k % 8 && src) {
+                    const uint32_t dst = dst0 + s * M::kRawStage + lane % kHalf * M::kRawTile;
+                    bulk_load(dst, src + (what ? L::kVc : 0), L::kCodes, full + 8 * s);
+                    bulk_load(dst + L::kCodes, src + (what ? L::kVs : L::kKs), 2 * L::kMeta, full + 8 * s);
+                }
+                if (++s == ring) s = 0, ++turn;
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- all MMAs, one thread
+        constexpr uint32_t idS = idesc_f16(false, kRows, kKeys), idO = idesc_f16(false, kRows, D);
+        // (descriptors count 16-byte units from their first: a constant each)
+        const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
+        const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
+        auto scores = [&](int i) {
+            const int b = i & 1;
+            const uint32_t d = tmem + kColS + kKeys * b;
+            const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
+            wait(k_full + 8 * b, i >> 1);
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int st = 0; st < D / 16; ++st)
+                        tc_mma_f16_ts(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS,
+                                      (part | st) != 0);
+                tc_mma_f16_ts(d, tmem + kColZ, zd + 2 * b, idS, 1);
+                tc_commit(s_full + 8 * b);
+            }
+            __syncwarp();
+        };
+        int done = 0, u = 0;   // blocks of earlier units, units
+        for (Walk w(P, R); w.more; w.next(), ++u) {
+            const int nb = w.j1 - w.j0;
+            wait(q_full, u);
+            tc_fence_after();
+            scores(done);
+            for (int j = 0; j < nb; ++j) {
+                const int i = done + j, b = i & 1;
+                if (j + 1 < nb) scores(i + 1);
+                wait(v_full, i);
+                wait(p_full + 8 * b, i >> 1);
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int st = 0; st < kKeys / 16; ++st)
+                        tc_mma_f16_ts(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4),
+                                      vd + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, j != 0 || st != 0);
+                    tc_commit(o_done);
+                }
+                __syncwarp();
+            }
+            done += nb;
+        }
+        __syncwarp();
+    } else if (dq_index(warp) >= 0) {
+        // ---------------------------------------------------------------- codes to operands
+        const int wi = dq_index(warp), tile_no = wi % kHalf, half = wi / kHalf & 1;   // this warp's tile of every block
+        const bool keys = wi < 2 * kHalf;
+        const int ring = keys ? M::kRawK : M::kRawV, first = keys ? 0 : M::kRawK, no = half * kHalf + tile_no;
+        uint8_t* raw = base + M::kRawOff + first * M::kRawStage + tile_no * M::kRawTile;
+        int s = half % ring, turn = half / ring, i = 0;   // half block 2 i + half in stage (2 i + half) % ring
+        for (Walk w(P, R); w.more; w.next()) {
+            const int end = min(w.t.p1 + 1, w.q.len);
+            for (int j = w.j0; j < w.j1; ++j, ++i) {
+                const int b = i & 1, kb = w.t.block(j);
+                wait(raw_full + 8 * (first + s), turn);
+                // the stage's last MMAs have read it
+                if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
+                if (!keys && i >= 1) wait(o_done, i - 1);
+                uint8_t* tile = raw + s * M::kRawStage;
+                const bool there = s_there[keys ? 0 : 1][(2 * i + half) & 15] >> tile_no & 1u;
+                const int left = there ? end - kb * kKeys - no * kKvTile : 0;
+                if (keys) {
+                    expand_keys<BITS, D>(tile, tile + L::kCodes, base + M::kK + b * M::kKStage, base + M::kZ, 2 * b, no, left, lane);
+                } else {
+                    const bool odd = there && leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + b * kKeys + no * kKvTile, lane);
+                    if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[b])[no] = odd;
+                    expand_values<BITS, D>(tile, tile + L::kCodes, base + M::kV + half * M::kVAtom, tile_no, left, lane);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(keys ? k_full + 8 * b : v_full);
+                    mbar_arrive(raw_empty + 8 * (first + s));
+                }
+                s += 2;
+                if (s >= ring) s -= ring, ++turn;
+            }
+        }
+    } else if (warp < kSoftWarps) {
+        // ---------------------------------------------------------------- softmax: two threads per row
+        const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        int done = 0;
+        for (Walk w(P, R); w.more; w.next()) {
+            const int nb = w.j1 - w.j0, rows = min(kRows, w.q.fresh * P.group - w.u.rt * kRows);
+            const int row = w.u.rt * kRows + r, tok = row / P.group, qh = w.u.head * P.group + (row - tok * P.group);
+            const int64_t at = (int64_t)w.q.row0 + tok;
+            const bool live = r < rows;
+            if (half == 0) {
+                // Q, scaled by a power of two into [2^9, 2^10), its columns in the order of K's rows
+                float top = 0.f;
+                const uint16_t* src = static_cast<const uint16_t*>(P.q) + at * P.q_stride + (int64_t)qh * D;
+#pragma unroll 8
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(elem_to_float<T>((uint16_t)(x[e >> 1] >> (16 * (e & 1))))));
+                }
+                int e = top > 0.f ? 9 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+                e = min(max(e, -120), 120);
+                const float up = pow2i(e);
+                factors[r] = fmaxf(P.scale_log2 * pow2i(-e), 0x1p-126f);   // (a hidden score is -inf times it)
+                uint32_t z[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {                     // 64 dimensions: 32 columns
+                    uint32_t o[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 64 * h + 8 * k) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = elem_to_float<T>((uint16_t)(x[i >> 1] >> (16 * (i & 1)))) * up;
+                        if (BITS == 4) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[4 * k + i] = pack_half2_rn(f[i], f[i + 4]);
+                        } else {
+                            o[4 * k] = pack_half2_rn(f[0], f[2]), o[4 * k + 1] = pack_half2_rn(f[1], f[3]);
+                            o[4 * k + 2] = pack_half2_rn(f[4], f[6]), o[4 * k + 3] = pack_half2_rn(f[5], f[7]);
+                        }
+                    }
+                    tmem_st32(lanes + kColQ + 32 * h, o);
+#pragma unroll
+                    for (int gg = 0; gg < 2; ++gg) {                   // sums of the rounded values of a group
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 p = unpack2(o[16 * gg + i]);
+                            sum += p.x + p.y;
+                        }
+                        const int g = 2 * h + gg;
+                        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
+                        z[g >> 1] |= (uint32_t)__half_as_ushort(hi) << (16 * (g & 1));
+                        z[G / 2 + (g >> 1)] |= (uint32_t)__half_as_ushort(lo) << (16 * (g & 1));
+                    }
+                }
+                tmem_st32(lanes + kColZ, z);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            soft_sync();   // the factors
+            const float f = factors[r];
+            const int p = live ? w.q.len - w.q.fresh + tok : -1;       // the row's position
+            float m = -INFINITY, l = 0.f, ref = 0.f;
+            uint32_t poison = 0;                                       // groups of dimensions that saw no number
+            // the value groups of a block (whose product is done) that this row saw and that are no numbers
+            auto odd_values = [&](int i, int kb) {
+                if (s_odd[i & 1] == 0) return;
+                for (int k = 0; k < kKeys; ++k) {
+                    if (!(reinterpret_cast<volatile uint8_t*>(&s_odd[i & 1])[k / kKvTile])) continue;
+                    const int j = kb * kKeys + k;
+                    if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & 1) * kKeys + k];
+                }
+            };
+            for (int j = 0; j < nb; ++j) {
+                const int i = done + j, b = i & 1, kb = w.t.block(w.j0 + j);
+                wait(s_full + 8 * b, i >> 1);
+                tc_fence_after();
+                const uint32_t col = lanes + kColS + kKeys * b + 64 * half;
+                const bool whole = w.t.whole(kb, P.window, P.sinks);
+                const uint32_t there = s_there[0][(2 * i + half) & 15];
+                const bool some = !whole || there != (1u << kHalf) - 1u;
+                const int first = kb * kKeys + 64 * half;
+                // 32 scores at a time, read twice (for the maximum and for P): registers are what 28 warps leave
+                auto load = [&](int h, float (&x)[32]) {
+                    tmem_ld32(col + 32 * h, reinterpret_cast<uint32_t(&)[32]>(x));
+                    if (some) {
+                        const int j0 = first + 32 * h;
+                        uint32_t sees = below(p + 1 - j0);
+                        if (P.window > 0) sees &= ~below(p + 1 - P.window - j0) | below(P.sinks - j0);
+                        sees &= (there >> (2 * h) & 1u ? 0xffffu : 0u) | (there >> (2 * h + 1) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(sees >> k & 1u)) x[k] = -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    load(h, x);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) mx = fmaxf(fmaxf(mx, x[k]), x[k + 1]);
+                }
+                mx *= f;
+                if (pair_any(warp & 3, mx > m + kTau)) {
+                    ml[half * kRows + r] = mx;
+                    pair_any(warp & 3, false);
+                    mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
+                    const float now = mx > m + kTau ? mx : m, a = m == now ? 1.f : ex2(m - now);
+                    if (j > 0 && __any_sync(0xffffffffu, m != now)) {   // each thread its half of O's dimensions
+                        wait(o_done, i - 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lanes + kColO + d, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            tmem_st32(lanes + kColO + d, o);
+                        }
+                    }
+                    l *= a;
+                    m = now;
+                    ref = now == -INFINITY ? 0.f : now - kPBits;
+                }
+                // The O before, whether or not a reference moved (see lq_attn_prefix.cu).
+                if (i > 0) wait(o_done, i - 1);
+                if (j > 0) odd_values(i - 1, w.t.block(w.j0 + j - 1));
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    load(h, x);
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 y = fma2(make_float2(x[k], x[k + 1]), make_float2(f, f), make_float2(-ref, -ref));
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum = add2(sum, e);
+                        pr[k / 2] = pack_half2_rn(e.x, e.y);
+                    }
+                    tmem_st16(col + 16 * h, pr);   // (over scores that have been read)
+                }
+                l += sum.x + sum.y;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * b);
+            }
+
+            // ---- the unit's rows: each thread half of its row's dimensions ----
+            soft_sync();   // (the maxima's last readers are done)
+            ml[half * kRows + r] = l;
+            soft_sync();
+            l = ml[r] + ml[kRows + r];
+            wait(o_done, done + nb - 1);
+            tc_fence_after();
+            odd_values(done + nb - 1, w.t.block(w.j1 - 1));
+            uint16_t* out = static_cast<uint16_t*>(P.out) + at * P.out_stride + (int64_t)qh * D;
+            auto finish = [&](int d, float (&v)[32], float inv) {      // 32 dimensions from d on
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    alignas(16) T y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = (T)(v[k + e] * inv);
+                    *reinterpret_cast<uint4*>(out + d + k) = *reinterpret_cast<const uint4*>(y);
+                }
+            };
+            auto finish_sum = [&](float top, float total) {
+                if (half == 0 && live && P.lse)
+                    P.lse[at * P.q_heads + qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPBits) * 0.6931471805599453f;
+            };
+            const bool all_here = w.j0 == 0 && w.j1 == w.t.blocks;
+            constexpr int kSlot = kRows * (D + 2);
+            float* slot = P.part + (int64_t)(2 * c + (w.j0 == 0 ? 1 : 0)) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                float v[32];
+                tmem_ld32(lanes + kColO + d, reinterpret_cast<uint32_t(&)[32]>(v));
+                if (poison >> (d / 32) & 1u) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = NAN;
+                }
+                if (all_here) {
+                    if (live) finish(d, v, inv);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<float4*>(slot + ((d + k) / 4 * kRows + r) * 4) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                }
+            }
+            if (all_here) {
+                finish_sum(m, l);
+            } else {
+                if (half == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m, l);
+                const WideShares shares(s_total, C);
+                const int64_t from = w.place + kChunkUnitCost;
+                const int c0 = shares.of(from), c1 = shares.of(from + w.t.blocks - 1);
+                soft_sync();
+                // (release of what the block wrote before the barrier, acquire of what the others did)
+                if (tid == 0) s_last = arrive_gpu(P.counters + c0) == (unsigned)(c1 - c0);
+                soft_sync();
+                if (s_last) {
+                    auto part = [&](int k) { return P.part + (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kSlot; };
+                    auto sums = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * r)); };
+                    float top = -INFINITY, total = 0.f;
+                    for (int k = 0; k <= c1 - c0; ++k) top = fmaxf(top, sums(k).x);
+                    const float mine = top == -INFINITY ? 0.f : top;
+                    for (int k = 0; k <= c1 - c0; ++k) total += sums(k).y * ex2(sums(k).x - mine);
+                    const float all = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll 1
+                    for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                        float v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll 1
+                        for (int k = 0; k <= c1 - c0; ++k) {
+                            const float e = ex2(sums(k).x - mine);
+                            const float* o = part(k);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(o + ((d / 4 + q) * kRows + r) * 4));
+                                v[4 * q] = fmaf(x.x, e, v[4 * q]), v[4 * q + 1] = fmaf(x.y, e, v[4 * q + 1]);
+                                v[4 * q + 2] = fmaf(x.z, e, v[4 * q + 2]), v[4 * q + 3] = fmaf(x.w, e, v[4 * q + 3]);
+                            }
+                        }
+                        if (live) finish(d, v, all);
+                    }
+                    finish_sum(top, total);
+                    if (tid == 0) P.counters[c0] = 0;
+                }
+            }
+            tc_fence_before();
+            soft_sync();   // both halves are done with O, the factors and the sums
+            done += nb;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int BITS, int D, class T>
+lq_status run(lq_handle h, const ChunkParams& P, cudaStream_t stream) {
+    using M = ChunkSmem<BITS, D>;
+    static std::mutex mu;
+    static bool ready[kMaxDevices] = {};   // the shared-memory attribute is set
+    if (h->device < 0 || h->device >= kMaxDevices || M::kSize > h->max_smem_optin) return LQ_ERR_UNSUPPORTED;
+    {
+        const std::lock_guard<std::mutex> lock(mu);
+        if (!ready[h->device]) {
+            if (cudaFuncSetAttribute(chunk_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSize) != cudaSuccess)
+                return LQ_ERR_CUDA;
+            ready[h->device] = true;
+        }
+    }
+    if ((size_t)h->num_sms > h->num_counters || (size_t)h->num_sms * 2 * kRows * (D + 2) > h->partial_floats) return LQ_ERR_WORKSPACE;
+    return launch_overlapped(chunk_kernel<BITS, D, T>, h->num_sms, kThreads, M::kSize, stream, P);
+}
+
+}  // namespace
+
+lq_status launch_kv_chunk(lq_handle h, const lq_kv_cache& c, const lq_kv_chunk_args& a, cudaStream_t stream) {
+    ChunkParams P = {};
+    P.cache = KvView{static_cast<uint8_t*>(c.pages), c.num_pages, c.page_size, c.kv_heads, c.page_size / kKvTile};
+    P.q = a.q, P.out = a.out, P.lse = a.lse;
+    P.q_stride = a.q_token_stride, P.out_stride = a.out_token_stride, P.bt_stride = a.block_table_stride;
+    P.block_table = a.block_table, P.lens = a.lens, P.starts = a.starts;
+    P.requests = a.batch, P.tokens = a.tokens, P.group = a.q_heads / c.kv_heads, P.q_heads = a.q_heads;
+    P.max_len = a.max_pages * c.page_size;
+    P.window = a.window, P.sinks = a.sinks;
+    P.scale_log2 = a.scale * 1.4426950408889634f;
+    P.part = h->partials, P.counters = h->counters, P.status = h->status_flag;
+    const bool bf16 = a.dtype == LQ_BF16;
+    if (c.head_dim == 128) {
+        if (c.bits == 4) return bf16 ? run<4, 128, __nv_bfloat16>(h, P, stream) : run<4, 128, __half>(h, P, stream);
+        return bf16 ? run<8, 128, __nv_bfloat16>(h, P, stream) : run<8, 128, __half>(h, P, stream);
+    }
+    if (c.bits == 4) return bf16 ? run<4, 64, __nv_bfloat16>(h, P, stream) : run<4, 64, __half>(h, P, stream);
+    return bf16 ? run<8, 64, __nv_bfloat16>(h, P, stream) : run<8, 64, __half>(h, P, stream);
+}
+
+}  // namespace lq

@@ -1,0 +1,54 @@
+// What the chunk attention kernel's blocks share out: tiles of a request's new rows, and the key blocks that each of them
+// visits.  Whole-number arithmetic of the host and the device alike, so that it can be walked through without a GPU.
+#pragma once
+
+#include <stdint.h>
+
+#include "lq_share.h"
+
+namespace lq {
+
+constexpr int kChunkKeys = 128;      // keys of a block
+constexpr int kChunkUnitCost = 6;    // what a unit costs a thread block, in its key blocks
+
+// Tile `rt` (of `tile_rows` rows) of a request of `len` tokens of which `fresh` are new: its rows are (new token, query head of
+// the group), tokens slower.  window 0: none.
+struct ChunkTile {
+    int p0, p1;        // positions of its first and last row (below 0: it sees nothing)
+    int lowest;        // the first token that a row's window holds
+    int sunk, gap;     // key blocks that hold sinks only, and those left out behind them
+    int blocks;        // key blocks that it visits, 1 at least
+    LQ_HD ChunkTile(int len, int fresh, int group, int window, int sinks, int tile_rows, int rt) {
+        const int64_t r0 = (int64_t)rt * tile_rows, rows = (int64_t)fresh * group;
+        const int64_t r1 = (r0 + tile_rows < rows ? r0 + tile_rows : rows) - 1;
+        p0 = len - fresh + (int)(r0 / group);
+        p1 = len - fresh + (int)(r1 / group);
+        lowest = window > 0 && p0 >= window ? p0 - window + 1 : 0;
+        const int from = lowest / kChunkKeys, end = (p1 < 0 ? 0 : p1 / kChunkKeys + 1);
+        const int s = (int)(((int64_t)sinks + kChunkKeys - 1) / kChunkKeys);
+        sunk = s < from ? s : from;
+        gap = from - sunk;
+        blocks = end - gap > 1 ? end - gap : 1;
+    }
+    LQ_HD int block(int i) const { return i < sunk ? i : i + gap; }      // number of the i-th block visited
+    // whether every row sees all of key block kb
+    LQ_HD bool whole(int kb, int window, int sinks) const {
+        const int64_t first = (int64_t)kb * kChunkKeys, last = first + kChunkKeys - 1;
+        return last <= p0 && (window <= 0 || first > (int64_t)p1 - window || last < sinks);
+    }
+};
+
+LQ_HD int chunk_tiles(int fresh, int group, int tile_rows) { return (int)(((int64_t)fresh * group + tile_rows - 1) / tile_rows); }
+
+// n things shared out to c parties in order, as Shares, past 32 bits.
+struct WideShares {
+    int64_t q, rem;
+    LQ_HD WideShares(int64_t n, int c) : q(n / c), rem(n - q * c) {}
+    LQ_HD int64_t first(int k) const { return q * k + (k < rem ? k : rem); }
+    LQ_HD int of(int64_t i) const {
+        const int64_t more = rem * (q + 1);
+        return (int)(i < more ? i / (q + 1) : rem + (i - more) / q);
+    }
+};
+
+}  // namespace lq

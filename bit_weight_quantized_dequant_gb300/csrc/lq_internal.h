@@ -110,6 +110,7 @@ lq_status launch_gemm_grouped(lq_handle h, const lq_problem* problems, int count
 constexpr int kStatusIndex = 4;         // status word: a position, slot or page out of range was left out
 constexpr int kMaxAttnBatch = 1024;     // requests of one attention call
 constexpr int kMaxAttnTokens = 64;      // query tokens of a request
+constexpr int kMaxLogprobTop = 64;      // alternatives of a row of logits
 
 // A launch that may begin while the kernel before it in the stream ends (programmatic dependent launch: the
 // kernel waits, with griddepcontrol.wait, before it touches memory).  Such a kernel reads what an earlier one
@@ -134,6 +135,10 @@ lq_status launch_rope(lq_handle h, const lq_rope_args& a, cudaStream_t stream);
 lq_status launch_kv_append(lq_handle h, const lq_kv_cache& c, const lq_kv_append_args& a, cudaStream_t stream);
 lq_status launch_kv_read(lq_handle h, const lq_kv_cache& c, const int64_t* slots, int n, void* k, void* v, int dtype,
                          cudaStream_t stream);
-lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, cudaStream_t stream);
+// (window 0: a row sees all of its request's earlier tokens)
+lq_status launch_kv_attention(lq_handle h, const lq_kv_cache& c, const lq_kv_attention_args& a, int window, int sinks, cudaStream_t stream);
+lq_status launch_kv_chunk(lq_handle h, const lq_kv_cache& c, const lq_kv_chunk_args& a, cudaStream_t stream);
+lq_status launch_logprobs(lq_handle h, const lq_logprobs_args& a, cudaStream_t stream);
+lq_status launch_logprobs_grad(lq_handle h, const lq_logprobs_grad_args& a, cudaStream_t stream);
 
 }  // namespace lq

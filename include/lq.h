@@ -573,6 +573,95 @@ typedef struct lq_kv_attention_args {
 LQ_API lq_status lq_kv_attention(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, void* stream);
 
 /*
+ * lq_kv_attention_window — lq_kv_attention through a sliding window: of the tokens that a row sees there, the one at
+ * position p of its request (counting from 0, its own included) sees those after p - window, and the first `sinks` tokens
+ * of the request whatever their distance.  window >= 1, sinks >= 0; what lies between is not read, and its pages need not
+ * exist (their entries of the block table are not used).  With a shared prefix: LQ_ERR_UNSUPPORTED (its pages may
+ * stand at the head of each request's own list instead).  Everything else is lq_kv_attention's.
+ */
+LQ_API lq_status lq_kv_attention_window(lq_handle h, const lq_kv_cache* cache, const lq_kv_attention_args* args, int window,
+                                        int sinks, void* stream);
+
+/*
+ * lq_kv_attention_chunk — attention of a chunk of new tokens of each of `batch` (1 .. 1024) requests over the cache, for
+ * any number of them (a prompt or a piece of one): request b's new tokens are rows starts[b] .. starts[b + 1] - 1 of q, the
+ * newest of its lens[b] tokens, and are in the cache already.  Row t of T of a request of n tokens stands at position
+ * p = n - T + t and sees its tokens j <= p; with a window (> 0; 0: none) those with j > p - window or j < sinks.
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
+ * over kv head h / (q_heads / kv_heads).  A row that sees nothing (p < 0) gives out = 0 and lse = -inf.  Rows of q in no
+ * request are not touched in out and lse.  Scores, their statistics and all sums are held in 32 bits; probabilities and
+ * the cache's values are rounded to binary16 before their product.
+ * q, out: [tokens][q_heads][head_dim] of dtype (LQ_F16 or LQ_BF16), token strides in elements, rows 16-byte aligned; out
+ * may be q when the strides are equal.  lse: fp32 [tokens][q_heads] or NULL.  starts[] does not decrease and stays within
+ * 0 .. tokens; an entry that does not is moved there and reported (LQ_ERR_INDEX).  lens, block_table, max_pages, scale and
+ * pages outside the cache as in lq_kv_attention; lens, starts and block_table are read on the device, so a captured call
+ * serves any division of the rows.  Uses the handle's workspace (LQ_ERR_WORKSPACE when it has no room for two blocks' rows
+ * on each SM).  With tokens = 0 nothing is launched.
+ */
+typedef struct lq_kv_chunk_args {
+    const void* q;
+    void* out;
+    float* lse;
+    int dtype;
+    int batch, tokens, q_heads;
+    int64_t q_token_stride, out_token_stride;
+    const int32_t* starts;        /* [batch + 1] */
+    const int32_t* block_table;   /* [batch][block_table_stride], max_pages of each row used */
+    int64_t block_table_stride;
+    int max_pages;
+    const int32_t* lens;          /* [batch] */
+    int window, sinks;
+    float scale;
+} lq_kv_chunk_args;
+
+LQ_API lq_status lq_kv_attention_chunk(lq_handle h, const lq_kv_cache* cache, const lq_kv_chunk_args* args, void* stream);
+
+/* ---- Log probabilities: what a scored prompt or a decode step ends in --------------------
+ *
+ * lq_logprobs — of n rows of `vocab` logits (any alignment of their type; row r at logits + r * row_stride elements):
+ *     lse[r] = ln sum_i exp(x_i),  logprob[r] = x_t - lse with t = tokens[r],  entropy[r] = -sum_i p_i ln p_i
+ * with p_i = exp(x_i - lse), all fp32, and the `top` (0 .. 64, at most vocab) largest logits: top_ids[r][k] their indices,
+ * largest first, equal ones by ascending index, top_logprobs[r][k] their log probabilities.  A negative token is left out
+ * (logprob 0); so is one at or past vocab (LQ_ERR_INDEX).  A logit of -inf is a token that cannot come; a row of nothing
+ * else gives lse and every log probability -inf and entropy 0.  A NaN or +inf makes a row's logprob, entropy and
+ * top_logprobs NaN (top_ids then count NaN as the largest).  entropy and lse may be NULL.  Sums are fp32 about the row's maximum.
+ * Rows that are fewer than fill the device are split over blocks by means of the handle's workspace.
+ */
+typedef struct lq_logprobs_args {
+    const void* logits;
+    int dtype;                 /* LQ_F32, LQ_F16 or LQ_BF16 */
+    int n, vocab;
+    int64_t row_stride;
+    const int64_t* tokens;     /* [n] */
+    float *logprob, *entropy, *lse;   /* [n] */
+    int top;
+    int64_t* top_ids;          /* [n][top] */
+    float* top_logprobs;       /* [n][top] */
+} lq_logprobs_args;
+
+LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* stream);
+
+/*
+ * lq_logprobs_grad — the gradient of lq_logprobs' logprob and entropy: with g = d_logprob[r] and e = d_entropy[r] (either
+ * may be NULL: zeros; g counts as 0 for a token that was left out),
+ *     d_logits[r][i] = p_i (-g - e (ln p_i + entropy[r])) + (i == t ? g : 0)     (fp32, rounded once to dtype)
+ * and 0 where p_i is 0 and i is not t.  tokens, lse and entropy (needed with d_entropy only) are lq_logprobs' own.
+ * d_logits has dtype and its own row stride (at least vocab), and may be logits when the strides are equal.
+ */
+typedef struct lq_logprobs_grad_args {
+    const void* logits;
+    void* d_logits;
+    int dtype;
+    int n, vocab;
+    int64_t row_stride, d_row_stride;
+    const int64_t* tokens;
+    const float *lse, *entropy;
+    const float *d_logprob, *d_entropy;
+} lq_logprobs_grad_args;
+
+LQ_API lq_status lq_logprobs_grad(lq_handle h, const lq_logprobs_grad_args* args, void* stream);
+
+/*
  * lq_selftest_wait — exercises the timeout path of the kernels' bounded waits.  One
  * thread of one CTA waits, with the routine the pipelined kernels use, on a
  * shared-memory barrier that nothing completes.  After limit_us microseconds
