@@ -268,8 +268,9 @@ def _scored():
             return logprob, entropy, ids, best
 
         @staticmethod
-        @torch.autograd.function.once_differentiable
         def backward(ctx, d_logprob, d_entropy, *_):
+            if torch.is_grad_enabled():     # (a graph of the gradient was asked for)
+                raise RuntimeError("token_logprobs has no second derivative")
             if d_logprob is None and d_entropy is None:
                 return None, None, None, None, None
             return ctx.handle._token_logprobs_grad(*ctx.saved_tensors, d_logprob, d_entropy), None, None, None, None

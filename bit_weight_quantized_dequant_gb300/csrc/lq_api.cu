@@ -573,7 +573,7 @@ LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* st
     if (!a.logits || !a.tokens || !a.logprob || !valid_dtype(a.dtype)) return LQ_ERR_INVALID_ARG;
     if (a.n < 0 || a.vocab < 1 || a.top < 0 || a.top > a.vocab) return LQ_ERR_INVALID_ARG;
     if (a.top > 0 && (!a.top_ids || !a.top_logprobs)) return LQ_ERR_INVALID_ARG;
-    if (a.top > lq::kMaxLogprobTop || a.vocab > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
+    if (a.top > lq::kMaxLogprobTop || a.vocab > 0x7fff0000 || a.n > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
     if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) || !aligned_to(a.top_ids, 8) || !aligned_to(a.logprob, 4) ||
         !aligned_to(a.entropy, 4) || !aligned_to(a.lse, 4) || !aligned_to(a.top_logprobs, 4))
         return LQ_ERR_ALIGNMENT;
@@ -588,7 +588,7 @@ LQ_API lq_status lq_logprobs_grad(lq_handle h, const lq_logprobs_grad_args* args
     const lq_logprobs_grad_args& a = *args;
     if (!a.logits || !a.d_logits || !a.tokens || !a.lse || !valid_dtype(a.dtype)) return LQ_ERR_INVALID_ARG;
     if (a.n < 0 || a.vocab < 1 || (a.d_entropy && !a.entropy)) return LQ_ERR_INVALID_ARG;
-    if (a.vocab > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
+    if (a.vocab > 0x7fff0000 || a.n > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
     if (a.n > 1 && a.d_row_stride < a.vocab) return LQ_ERR_INVALID_ARG;
     if (a.d_logits == a.logits && a.n > 1 && a.d_row_stride != a.row_stride) return LQ_ERR_INVALID_ARG;
     if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.d_logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) ||

@@ -94,16 +94,18 @@ def test_many_rows(lqm, handle, n, V, top):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("how", ["constant", "few values", "up", "down", "negative", "zeros of both signs", "one thread", "subnormal"])
+@pytest.mark.parametrize("how", ["constant", "few values", "up", "down", "negative", "zeros of both signs", "one thread", "by thread",
+                                 "subnormal"])
 @pytest.mark.parametrize("top", [1, 8, 9, 64])
 def test_equal_logits_go_to_the_lower_id(lqm, handle, dtype, how, top):  # noqa: F811
-    V, n = 20011, 3
+    V, n = 150011, 3
     g = torch.Generator().manual_seed(5)
     j = torch.arange(V).float()
     x = {"constant": torch.full((V,), -2.5), "few values": torch.randint(-3, 3, (V,), generator=g).float(), "up": j / 64,
          "down": -j / 64, "negative": -torch.randint(1, 30, (V,), generator=g).float(),
          "zeros of both signs": torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0),
          "one thread": torch.where(j % 2048 < 8, 9.0, -torch.rand(V, generator=g)),
+         "by thread": -(j // 8 % 512 * 64 + j // 4096 * 8 + j % 8) / 64.0,
          "subnormal": torch.randint(-5, 6, (V,), generator=g).float() * 2.0 ** -24}[how]
     x = x.expand(n, V).to(DT[dtype]).contiguous().cuda()
     t = torch.tensor([0, V - 1, 77], device="cuda")
@@ -141,6 +143,22 @@ def test_rows_that_are_no_distribution(lqm, handle):  # noqa: F811
     assert bool(logprob[1:3].isnan().all()) and bool(entropy[1:3].isnan().all()) and bool(best[1:3].isnan().all())
     assert int(ids[1, 0]) == 8888 and int(ids[2, 0]) == 5
     check(x[3:], t[3:], tuple(o[3:] for o in (logprob, entropy, ids, best)), 3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("bad", [np.inf, np.nan, -np.nan])
+@pytest.mark.parametrize("n", [1, 400])
+def test_ids_among_many_that_are_no_numbers(lqm, handle, dtype, bad, n):  # noqa: F811
+    """NaN counts as the largest, infinity comes next, equal ones by id."""
+    x, t = rows(n, 30000, dtype, seed=15)
+    x[:, 1000:29000:3] = bad
+    x[:, 17], x[:, 29999] = np.inf, np.nan
+    logprob, entropy, ids, best = handle.token_logprobs(x, t, top=40)
+    assert bool(logprob.isnan().all()) and bool(entropy.isnan().all()) and bool(best.isnan().all())
+    key = torch.where(x[0].isnan(), 2, torch.where(x[0] == np.inf, 1, 0)).cpu()
+    want = torch.sort(key, descending=True, stable=True)[1][:40]
+    assert key[want].min() > 0
+    assert bool((ids.cpu() == want).all())
 
 
 def test_large_logits(lqm, handle):  # noqa: F811
