@@ -35,20 +35,15 @@ struct ChunkParams {
     int* status;
 };
 
-constexpr int kRows = 128;          // rows of a unit
+constexpr int kRows = 128;          // rows of a CTA
 constexpr int kKeys = kTcKeys;      // keys of a block
 static_assert(kKeys == kChunkKeys, "key blocks");
-constexpr int kHalf = 4;            // tiles of half a block, which are loaded and expanded together
-constexpr int kSoftWarps = 8, kDqWarps = 16;
-// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those
-// of one scheduler (number mod 4 = 0) issue MMAs, load and expand one tile; the other three schedulers' expand.
-constexpr int kMmaWarp = 8, kLoadWarp = 12, kDqLast = 20, kWarpsAll = 28;   // (the load warps: 12 and 16)
-constexpr int kThreads = 32 * kWarpsAll;
-__device__ __forceinline__ int dq_index(int warp) {   // which expanding warp, -1: none
-    if (warp < kSoftWarps) return -1;
-    if (warp % 4 == 0) return warp == kDqLast ? kDqWarps - 1 : -1;
-    return (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
-}
+constexpr int kTiles = kKeys / kKvTile;
+// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4), then those that expand keys and
+// values, the one that issues MMAs and those that load keys' and values' bytes.
+constexpr int kSoftWarps = 8, kDqWarps = 4;      // (four for keys, four for values)
+constexpr int kKeyWarp = kSoftWarps, kValueWarp = kKeyWarp + kDqWarps, kMmaWarp = kValueWarp + kDqWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kWarpsAll = 20, kThreads = 32 * kWarpsAll;   // (load warps: keys', values'; one is idle)
 // tensor memory columns
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
@@ -57,26 +52,29 @@ constexpr int kColQ = 384;          // D / 2
 constexpr int kColZ = 448;          // 8 (group sums of q), 32 written
 static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 32 <= kTmemCols, "tensor memory");
 
-template <int BITS, int D>
+// Shared memory of one of CTAS CTAs: its share of a block's keys (rows of K) and of the dimensions (rows of V).
+template <int BITS, int D, int CTAS>
 struct ChunkSmem {
     using L = KvLayout<BITS, D>;
-    static constexpr int kAtoms = TcOperand<D>::kAtoms, kAtom = TcOperand<D>::kAtom;
+    static constexpr int kKeysHere = kKeys / CTAS, kTilesHere = kTiles / CTAS, kDimsHere = D / CTAS;
+    static constexpr int kAtoms = TcOperand<D, kKeysHere>::kAtoms, kAtom = TcOperand<D, kKeysHere>::kAtom;
     static constexpr int kKStage = 2 * kAtoms * kAtom;           // K rounded, K's rest
-    static constexpr int kVAtom = D * 128;                       // [D][64 keys]
+    static constexpr int kVAtom = kDimsHere * 128;               // [dimensions][64 keys]
+    static constexpr int kVStages = CTAS == 2 ? 2 : 1;
     static constexpr int kRawTile = L::kCodes + 2 * L::kMeta;    // a tile's keys (or values): codes, S, Z
-    static constexpr int kRawStage = kHalf * kRawTile;
-    static constexpr int kRawK = L::kBytes <= 2560 ? 4 : 2, kRawV = L::kBytes <= 2560 ? 4 : 2;   // half blocks in flight
+    static constexpr int kRawStageK = kTilesHere * kRawTile, kRawStageV = kTiles * kRawTile;
+    static constexpr int kRaw = CTAS == 2 ? (L::kBytes <= 2560 ? 4 : 3) : L::kBytes <= 2560 ? 2 : 1;   // blocks in flight
     static constexpr int kK = 0;
     static constexpr int kZ = kK + 2 * kKStage;                  // Z of stage b in chunk 2 b of each key's row
     static constexpr int kV = kZ + kAtom;
-    static constexpr int kRawOff = kV + 2 * kVAtom;
-    static constexpr int kMl = kRawOff + (kRawK + kRawV) * kRawStage;       // [2 halves][rows] maxima, then sums
+    static constexpr int kRawK = kV + kVStages * 2 * kVAtom, kRawV = kRawK + kRaw * kRawStageK;
+    static constexpr int kMl = kRawV + kRaw * kRawStageV;        // [2 halves][rows] maxima, then sums
     static constexpr int kF = kMl + 2 * kRows * 4;               // [rows] score factors
-    static constexpr int kBad = kF + kRows * 4;                  // [2][keys] groups of a value that are no numbers
-    static constexpr int kBars = kBad + 2 * kKeys;
-    static constexpr int kNumBars = 2 * (kRawK + kRawV) + 2 * 3 + 3;
+    static constexpr int kBad = kF + kRows * 4;                  // [4 blocks][keys] groups of a value that are no numbers
+    static constexpr int kBars = kBad + 4 * kKeys;
+    static constexpr int kNumBars = 4 * kRaw + 2 * 5 + 1;
     static constexpr int kSize = 1024 + kBars + 8 * kNumBars;
-    static_assert(kSize <= 226 * 1024 && kBars % 8 == 0 && kRawOff % 128 == 0 && kRawStage % 16 == 0, "shared memory");
+    static_assert(kSize <= 226 * 1024 && kBars % 8 == 0 && kRawK % 128 == 0 && kRawTile % 16 == 0, "shared memory");
     static_assert(8 * (kMaxAttnBatch + 1) <= 2 * kKStage, "the requests' running sums lie where K will");
 };
 
@@ -109,8 +107,9 @@ struct Request {
         len = min(max(P.lens[b], 0), P.max_len);
     }
 };
+template <int CTAS>
 __device__ __forceinline__ ChunkTile tile_of(const ChunkParams& P, const Request& q, int rt) {
-    return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, kRows, rt);
+    return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, CTAS * kRows, rt);
 }
 
 // A thread block's share: from block `j0` of unit `first` (at `place` of the sequence) to before block `j1` of unit `last`.
@@ -122,6 +121,7 @@ struct Range {
 };
 
 // A walk over a share's units; every role has one.
+template <int CTAS>
 struct Walk {
     const ChunkParams& P;
     Range R;
@@ -132,7 +132,7 @@ struct Walk {
     int64_t place;       // of the unit's cost, its blocks follow
     bool more;
     __device__ __forceinline__ Walk(const ChunkParams& P_, const Range& r)
-        : P(P_), R(r), u(r.first), q(P_, r.first.b), t(tile_of(P_, q, r.first.rt)), place(r.place), more(!r.none) {
+        : P(P_), R(r), u(r.first), q(P_, r.first.b), t(tile_of<CTAS>(P_, q, r.first.rt)), place(r.place), more(!r.none) {
         j0 = r.j0;
         set_end();
     }
@@ -150,18 +150,19 @@ struct Walk {
         j0 = 0;
         if (++u.head == P.cache.kv_heads) {
             u.head = 0;
-            if (++u.rt == chunk_tiles(q.fresh, P.group, kRows)) {
+            if (++u.rt == chunk_tiles(q.fresh, P.group, CTAS * kRows)) {
                 u.rt = 0;
                 do ++u.b; while (Request(P, u.b).fresh == 0);   // (the last unit lies ahead)
                 q = Request(P, u.b);
             }
-            t = tile_of(P, q, u.rt);
+            t = tile_of<CTAS>(P, q, u.rt);
         }
         set_end();
     }
 };
 
-// (All threads of a block together.)  The share of block c of C; `cum` has room for requests + 1 sums.
+// (All threads of a CTA together.)  The share of party c of C; `cum` has room for requests + 1 sums.
+template <int CTAS>
 __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, int64_t* cum, int64_t* total_out, Range* out) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // places of each request
@@ -171,9 +172,9 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
             const int a0 = P.starts[b], a1 = P.starts[b + 1];
             if (a0 < 0 || a1 < a0 || a1 > P.tokens) atomicOr(P.status, kStatusIndex);
         }
-        const int tiles = chunk_tiles(q.fresh, P.group, kRows);
+        const int tiles = chunk_tiles(q.fresh, P.group, CTAS * kRows);
         int64_t sum = 0;
-        for (int rt = lane; rt < tiles; rt += 32) sum += tile_of(P, q, rt).blocks + kChunkUnitCost;
+        for (int rt = lane; rt < tiles; rt += 32) sum += tile_of<CTAS>(P, q, rt).blocks + kChunkUnitCost;
 #pragma unroll
         for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         if (lane == 0) cum[b + 1] = sum * P.cache.kv_heads;
@@ -205,10 +206,10 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
             }
             u.b = lo;
             const Request q(P, lo);
-            const int tiles = chunk_tiles(q.fresh, P.group, kRows), heads = P.cache.kv_heads;
+            const int tiles = chunk_tiles(q.fresh, P.group, CTAS * kRows), heads = P.cache.kv_heads;
             int64_t from = cum[lo];
             for (int r0 = 0; r0 < tiles; r0 += 32) {
-                const int64_t each = r0 + lane < tiles ? tile_of(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
+                const int64_t each = r0 + lane < tiles ? tile_of<CTAS>(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
                 int64_t v = each * heads;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -281,74 +282,90 @@ __device__ __forceinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad
     return true;
 }
 
-template <int BITS, int D, class T>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams P) {
+// CTAS = 2: a cluster of two CTAs takes units of 256 rows, 128 in each one's tensor memory.  The even CTA issues the pair's
+// MMAs (M 256), of whose other operand each CTA holds half: the keys of half a block, the values' half of the dimensions.
+template <int BITS, int D, class T, int CTAS>
+__device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     using L = KvLayout<BITS, D>;
-    using M = ChunkSmem<BITS, D>;
-    constexpr int G = D / 32, kRawAll = M::kRawK + M::kRawV;
+    using M = ChunkSmem<BITS, D, CTAS>;
+    constexpr int G = D / 32;
+    constexpr bool kPair = CTAS == 2;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms)
+    uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms; alike in both CTAs)
     float* ml = reinterpret_cast<float*>(base + M::kMl);
     float* factors = reinterpret_cast<float*>(base + M::kF);
     __shared__ uint32_t s_tmem;
-    __shared__ volatile uint32_t s_there[2][16];   // a half block's tiles in the cache, keys' and values' (no role is 16 ahead of another)
-    __shared__ volatile unsigned long long s_odd[2];   // a byte per tile of a block: whether it has values that are no numbers
+    __shared__ volatile uint32_t s_there[2][8];        // a block's tiles in the cache, for keys (all of them) and values (no role is 8 ahead of another)
+    __shared__ volatile unsigned long long s_odd[4];   // a byte per tile of a block: whether it has values that are no numbers (read up to two blocks later)
     __shared__ Range s_range;
     __shared__ int64_t s_total;
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kPair ? (int)cluster_rank() : 0;
 
     const uint32_t bars = smem_u32(base + M::kBars);
-    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * kRawAll, k_full = raw_empty + 8 * kRawAll, s_full = k_full + 16;
-    const uint32_t p_full = s_full + 16, v_full = p_full + 16, o_done = v_full + 8, q_full = o_done + 8;
+    // each CTA's: bytes of keys and values there and used, scores there, O done; the even CTA's: operands, P and Q there
+    const uint32_t kr_full = bars, kr_empty = kr_full + 8 * M::kRaw, vr_full = kr_empty + 8 * M::kRaw, vr_empty = vr_full + 8 * M::kRaw;
+    const uint32_t s_full = vr_empty + 8 * M::kRaw, o_done = s_full + 16, k_full = o_done + 16, v_full = k_full + 16, p_full = v_full + 16;
+    const uint32_t q_full = p_full + 16;
     if (tid == 0) {
-        for (int i = 0; i < kRawAll; ++i) {
-            mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, kHalf);
+        for (int i = 0; i < M::kRaw; ++i) {
+            mbar_init(kr_full + 8 * i, 1);
+            mbar_init(kr_empty + 8 * i, kDqWarps);
+            mbar_init(vr_full + 8 * i, 1);
+            mbar_init(vr_empty + 8 * i, kDqWarps);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full + 8 * b, 2 * kHalf);
             mbar_init(s_full + 8 * b, 1);
-            mbar_init(p_full + 8 * b, kSoftWarps);
+            mbar_init(o_done + 8 * b, 1);
+            mbar_init(k_full + 8 * b, CTAS * kDqWarps);
+            mbar_init(v_full + 8 * b, CTAS * kDqWarps);
+            mbar_init(p_full + 8 * b, CTAS * kSoftWarps);
         }
-        mbar_init(v_full, 2 * kHalf);
-        mbar_init(o_done, 1);
-        mbar_init(q_full, 4);
+        mbar_init(q_full, CTAS * 4);
         fence_mbar_init();
     }
     // (the odd chunks of the Z rows multiply nothing: zero for good)
     for (int i = tid; i < M::kAtom / 16; i += kThreads) sts128(base + M::kZ + 16 * i, 0, 0, 0, 0);
-    if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    if (warp == kMmaWarp) {
+        if (kPair) tmem_alloc_pair(smem_u32(&s_tmem), kTmemCols);
+        else tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    }
     fence_async_smem();
     tc_fence_before();
-    __syncthreads();
+    if (kPair) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_launch_dependents();
     pdl_wait();
 
-    const int c = blockIdx.x, C = gridDim.x;
-    const Range R = range_of(P, c, C, reinterpret_cast<int64_t*>(base + M::kK), &s_total, &s_range);
+    const int c = blockIdx.x / CTAS, C = gridDim.x / CTAS;
+    const Range R = range_of<CTAS>(P, c, C, reinterpret_cast<int64_t*>(base + M::kK), &s_total, &s_range);
     int own_abort = 0;
-    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded(bar, parity & 1u, &own_abort, P.status); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded<kPair>(bar, parity & 1u, &own_abort, P.status); };
+    auto arrive = [&](uint32_t bar) {           // on the even CTA's barrier
+        if (kPair) mbar_arrive_remote(mapa_shared(bar, 0));
+        else mbar_arrive(bar);
+    };
 
-    if (warp == kLoadWarp || warp == kLoadWarp + 4) {
+    if (warp == kLoadWarp || warp == kLoadWarp + 1) {
         // ---------------------------------------------------------------- keys' or values' bytes into their ring
-        const int what = warp != kLoadWarp, ring = what ? M::kRawV : M::kRawK, first = what ? M::kRawK : 0;
-        const uint32_t full = raw_full + 8 * first, empty = raw_empty + 8 * first;
-        const uint32_t dst0 = smem_u32(base + M::kRawOff + first * M::kRawStage);
-        int s = 0, turn = -1, i = 0;             // half blocks
-        for (Walk w(P, R); w.more; w.next()) {
-            const int n = 2 * (w.j1 - w.j0);
+        const int what = warp - kLoadWarp;
+        const uint32_t full = what ? vr_full : kr_full, empty = what ? vr_empty : kr_empty;
+        const uint32_t dst0 = smem_u32(base + (what ? M::kRawV : M::kRawK));
+        const int stage_bytes = what ? M::kRawStageV : M::kRawStageK;
+        int s = 0, turn = -1, i = 0;             // blocks
+        for (Walk<CTAS> w(P, R); w.more; w.next()) {
             const int32_t* table = P.block_table + w.u.b * P.bt_stride;
             const int end = min(w.t.p1 + 1, w.q.len);
             const uint8_t* src = nullptr;
-            for (int k = 0; k < n; ++k, ++i) {
-                if (k % 8 == 0) {                // addresses of four blocks' tiles, one per lane
-                    const int j = w.j0 + (k + lane / kHalf) / 2;
+            for (int j = w.j0; j < w.j1; ++j, ++i) {
+                const int k = j - w.j0;
+                if (k % 4 == 0) {                // addresses of four blocks' tiles, one per lane
                     src = nullptr;
-                    if (j < w.j1) {
-                        const int tile = w.t.block(j) * 2 * kHalf + lane % (2 * kHalf);
+                    if (j + lane / kTiles < w.j1) {
+                        const int tile = w.t.block(j + lane / kTiles) * kTiles + lane % kTiles;
                         if (tile * kKvTile < end) {
                             const int pi = tile / P.cache.tiles_per_page, page = table[pi];
                             if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
@@ -360,102 +377,118 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 if (turn >= 0) wait(empty + 8 * s, turn);
                 __syncwarp();
-                const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (k % 8 * kHalf)) & ((1u << kHalf) - 1u);
+                const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (k % 4 * kTiles)) & ((1u << kTiles) - 1u);
+                // (of the keys only this CTA's half is loaded)
+                const uint32_t wanted = what ? there : there & (((1u << M::kTilesHere) - 1u) << (rank * M::kTilesHere));
                 if (lane == 0) {
-                    s_there[what][i & 15] = there;
-                    if (there) mbar_arrive_expect_tx(full + 8 * s, __popc(there) * M::kRawTile);
+                    s_there[what][i & 7] = there;
+                    if (wanted) mbar_arrive_expect_tx(full + 8 * s, __popc(wanted) * M::kRawTile);
                     else mbar_arrive(full + 8 * s);
                 }
                 __syncwarp();
-                if (lane / kHalf == k % 8 && src) {
-                    const uint32_t dst = dst0 + s * M::kRawStage + lane % kHalf * M::kRawTile;
+                const int no = lane % kTiles;
+                if (lane / kTiles == k % 4 && (wanted >> no & 1u)) {
+                    const uint32_t dst = dst0 + s * stage_bytes + (what ? no : no - rank * M::kTilesHere) * M::kRawTile;
                     bulk_load(dst, src + (what ? L::kVc : 0), L::kCodes, full + 8 * s);
                     bulk_load(dst + L::kCodes, src + (what ? L::kVs : L::kKs), 2 * L::kMeta, full + 8 * s);
                 }
-                if (++s == ring) s = 0, ++turn;
+                if (++s == M::kRaw) s = 0, ++turn;
             }
         }
     } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- all MMAs, one thread
-        constexpr uint32_t idS = idesc_f16(false, kRows, kKeys), idO = idesc_f16(false, kRows, D);
-        // (descriptors count 16-byte units from their first: a constant each)
-        const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
-        const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
-        auto scores = [&](int i) {
-            const int b = i & 1;
-            const uint32_t d = tmem + kColS + kKeys * b;
-            const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
-            wait(k_full + 8 * b, i >> 1);
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int st = 0; st < D / 16; ++st)
-                        tc_mma_f16_ts(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS,
-                                      (part | st) != 0);
-                tc_mma_f16_ts(d, tmem + kColZ, zd + 2 * b, idS, 1);
-                tc_commit(s_full + 8 * b);
-            }
-            __syncwarp();
-        };
-        int done = 0, u = 0;   // blocks of earlier units, units
-        for (Walk w(P, R); w.more; w.next(), ++u) {
-            const int nb = w.j1 - w.j0;
-            wait(q_full, u);
-            tc_fence_after();
-            scores(done);
-            for (int j = 0; j < nb; ++j) {
-                const int i = done + j, b = i & 1;
-                if (j + 1 < nb) scores(i + 1);
-                wait(v_full, i);
-                wait(p_full + 8 * b, i >> 1);
+        // ---------------------------------------------------------------- all MMAs, one thread of the even CTA
+        if (rank == 0) {
+            constexpr uint32_t idS = idesc_f16(false, CTAS * kRows, kKeys), idO = idesc_f16(false, CTAS * kRows, D);
+            auto mma = [&](uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
+                if (kPair) tc_mma_f16_ts_pair(d, a, b, id, add);
+                else tc_mma_f16_ts(d, a, b, id, add);
+            };
+            auto commit = [&](uint32_t bar) {
+                if (kPair) tc_commit_pair(bar);
+                else tc_commit(bar);
+            };
+            // (descriptors count 16-byte units from their first: a constant each)
+            const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
+            const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
+            auto scores = [&](int i) {
+                const int b = i & 1;
+                const uint32_t d = tmem + kColS + kKeys * b;
+                const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
+                wait(k_full + 8 * b, i >> 1);
                 tc_fence_after();
                 if (lane == 0) {
 #pragma unroll
-                    for (int st = 0; st < kKeys / 16; ++st)
-                        tc_mma_f16_ts(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4),
-                                      vd + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, j != 0 || st != 0);
-                    tc_commit(o_done);
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int st = 0; st < D / 16; ++st)
+                            mma(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS, (part | st) != 0);
+                    mma(d, tmem + kColZ, zd + 2 * b, idS, 1);
+                    commit(s_full + 8 * b);
                 }
                 __syncwarp();
+            };
+            int done = 0, u = 0;   // blocks of earlier units, units
+            for (Walk<CTAS> w(P, R); w.more; w.next(), ++u) {
+                const int nb = w.j1 - w.j0;
+                wait(q_full, u);
+                tc_fence_after();
+                scores(done);
+                for (int j = 0; j < nb; ++j) {
+                    const int i = done + j, b = i & 1;
+                    if (j + 1 < nb) scores(i + 1);
+                    wait(v_full + 8 * b, i >> 1);
+                    wait(p_full + 8 * b, i >> 1);
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t v = vd + (M::kVStages == 2 && b ? 2 * M::kVAtom / 16 : 0);
+#pragma unroll
+                        for (int st = 0; st < kKeys / 16; ++st)
+                            mma(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4), v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16,
+                                idO, j != 0 || st != 0);
+                        commit(o_done + 8 * b);
+                    }
+                    __syncwarp();
+                }
+                done += nb;
             }
-            done += nb;
         }
         __syncwarp();
-    } else if (dq_index(warp) >= 0) {
+    } else if (warp >= kKeyWarp && warp < kMmaWarp) {
         // ---------------------------------------------------------------- codes to operands
-        const int wi = dq_index(warp), tile_no = wi % kHalf, half = wi / kHalf & 1;   // this warp's tile of every block
-        const bool keys = wi < 2 * kHalf;
-        const int ring = keys ? M::kRawK : M::kRawV, first = keys ? 0 : M::kRawK, no = half * kHalf + tile_no;
-        uint8_t* raw = base + M::kRawOff + first * M::kRawStage + tile_no * M::kRawTile;
-        int s = half % ring, turn = half / ring, i = 0;   // half block 2 i + half in stage (2 i + half) % ring
-        for (Walk w(P, R); w.more; w.next()) {
+        const bool keys = warp < kValueWarp;
+        const int wi = (warp - kKeyWarp) % kDqWarps, tiles = (keys ? M::kTilesHere : kTiles) / kDqWarps;   // this warp's tiles of every block
+        const uint32_t full = keys ? kr_full : vr_full, empty = keys ? kr_empty : vr_empty;
+        uint8_t* raw = base + (keys ? M::kRawK : M::kRawV);
+        int s = 0, turn = 0, i = 0;
+        for (Walk<CTAS> w(P, R); w.more; w.next()) {
             const int end = min(w.t.p1 + 1, w.q.len);
             for (int j = w.j0; j < w.j1; ++j, ++i) {
                 const int b = i & 1, kb = w.t.block(j);
-                wait(raw_full + 8 * (first + s), turn);
+                wait(full + 8 * s, turn);
                 // the stage's last MMAs have read it
                 if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
-                if (!keys && i >= 1) wait(o_done, i - 1);
-                uint8_t* tile = raw + s * M::kRawStage;
-                const bool there = s_there[keys ? 0 : 1][(2 * i + half) & 15] >> tile_no & 1u;
-                const int left = there ? end - kb * kKeys - no * kKvTile : 0;
-                if (keys) {
-                    expand_keys<BITS, D>(tile, tile + L::kCodes, base + M::kK + b * M::kKStage, base + M::kZ, 2 * b, no, left, lane);
-                } else {
-                    const bool odd = there && leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + b * kKeys + no * kKvTile, lane);
-                    if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[b])[no] = odd;
-                    expand_values<BITS, D>(tile, tile + L::kCodes, base + M::kV + half * M::kVAtom, tile_no, left, lane);
+                if (!keys && i >= M::kVStages) wait(o_done + 8 * ((i - M::kVStages) & 1), (i - M::kVStages) >> 1);
+                const uint32_t there = s_there[keys ? 0 : 1][i & 7];
+                for (int k = 0; k < tiles; ++k) {
+                    const int here = wi * tiles + k, no = keys ? rank * M::kTilesHere + here : here;   // tile of the stage, of the block
+                    uint8_t* tile = raw + s * (keys ? M::kRawStageK : M::kRawStageV) + here * M::kRawTile;
+                    const int left = there >> no & 1u ? end - kb * kKeys - no * kKvTile : 0;
+                    if (keys) {
+                        expand_keys<BITS, D, M::kKeysHere>(tile, tile + L::kCodes, base + M::kK + b * M::kKStage, base + M::kZ, 2 * b, here, left, lane);
+                    } else {
+                        const bool odd = (there >> no & 1u) && leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + no * kKvTile, lane);
+                        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[no] = odd;
+                        expand_values<BITS, D, CTAS>(tile, tile + L::kCodes, base + M::kV + ((M::kVStages == 2 ? 2 * b : 0) + no / 4) * M::kVAtom, no % 4,
+                                                     left, lane, rank);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(keys ? k_full + 8 * b : v_full);
-                    mbar_arrive(raw_empty + 8 * (first + s));
+                    arrive((keys ? k_full : v_full) + 8 * b);
+                    mbar_arrive(empty + 8 * s);
                 }
-                s += 2;
-                if (s >= ring) s -= ring, ++turn;
+                if (++s == M::kRaw) s = 0, ++turn;
             }
         }
     } else if (warp < kSoftWarps) {
@@ -463,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         int done = 0;
-        for (Walk w(P, R); w.more; w.next()) {
-            const int nb = w.j1 - w.j0, rows = min(kRows, w.q.fresh * P.group - w.u.rt * kRows);
-            const int row = w.u.rt * kRows + r, tok = row / P.group, qh = w.u.head * P.group + (row - tok * P.group);
+        for (Walk<CTAS> w(P, R); w.more; w.next()) {
+            const int nb = w.j1 - w.j0, row0 = (w.u.rt * CTAS + rank) * kRows, rows = min(kRows, w.q.fresh * P.group - row0);
+            const int row = row0 + r, tok = row / P.group, qh = w.u.head * P.group + (row - tok * P.group);
             const int64_t at = (int64_t)w.q.row0 + tok;
             const bool live = r < rows;
             if (half == 0) {
@@ -522,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 tmem_st32(lanes + kColZ, z);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+                if (lane == 0) arrive(q_full);
             }
             soft_sync();   // the factors
             const float f = factors[r];
@@ -531,11 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             uint32_t poison = 0;                                       // groups of dimensions that saw no number
             // the value groups of a block (whose product is done) that this row saw and that are no numbers
             auto odd_values = [&](int i, int kb) {
-                if (s_odd[i & 1] == 0) return;
+                if (s_odd[i & 3] == 0) return;
                 for (int k = 0; k < kKeys; ++k) {
-                    if (!(reinterpret_cast<volatile uint8_t*>(&s_odd[i & 1])[k / kKvTile])) continue;
+                    if (!(reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[k / kKvTile])) continue;
                     const int j = kb * kKeys + k;
-                    if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & 1) * kKeys + k];
+                    if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & 3) * kKeys + k];
                 }
             };
             for (int j = 0; j < nb; ++j) {
@@ -544,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 tc_fence_after();
                 const uint32_t col = lanes + kColS + kKeys * b + 64 * half;
                 const bool whole = w.t.whole(kb, P.window, P.sinks);
-                const uint32_t there = s_there[0][(2 * i + half) & 15];
-                const bool some = !whole || there != (1u << kHalf) - 1u;
+                const uint32_t there = s_there[0][i & 7] >> (half * kTiles / 2) & ((1u << kTiles / 2) - 1u);
+                const bool some = !whole || there != (1u << kTiles / 2) - 1u;
                 const int first = kb * kKeys + 64 * half;
                 // 32 scores at a time, read twice (for the maximum and for P): registers are what 28 warps leave
                 auto load = [&](int h, float (&x)[32]) {
@@ -575,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
                     const float now = mx > m + kTau ? mx : m, a = m == now ? 1.f : ex2(m - now);
                     if (j > 0 && __any_sync(0xffffffffu, m != now)) {   // each thread its half of O's dimensions
-                        wait(o_done, i - 1);
+                        wait(o_done + 8 * (b ^ 1), (i - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
@@ -591,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     ref = now == -INFINITY ? 0.f : now - kPBits;
                 }
                 // The O before, whether or not a reference moved (see lq_attn_prefix.cu).
-                if (i > 0) wait(o_done, i - 1);
+                if (i > 0) wait(o_done + 8 * (b ^ 1), (i - 1) >> 1);
                 if (j > 0) odd_values(i - 1, w.t.block(w.j0 + j - 1));
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -611,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 l += sum.x + sum.y;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * b);
+                if (lane == 0) arrive(p_full + 8 * b);
             }
 
             // ---- the unit's rows: each thread half of its row's dimensions ----
@@ -619,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             ml[half * kRows + r] = l;
             soft_sync();
             l = ml[r] + ml[kRows + r];
-            wait(o_done, done + nb - 1);
+            wait(o_done + 8 * ((done + nb - 1) & 1), (done + nb - 1) >> 1);
             tc_fence_after();
             odd_values(done + nb - 1, w.t.block(w.j1 - 1));
             uint16_t* out = static_cast<uint16_t*>(P.out) + at * P.out_stride + (int64_t)qh * D;
@@ -638,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             const bool all_here = w.j0 == 0 && w.j1 == w.t.blocks;
             constexpr int kSlot = kRows * (D + 2);
-            float* slot = P.part + (int64_t)(2 * c + (w.j0 == 0 ? 1 : 0)) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
+            float* slot = P.part + (int64_t)((2 * c + (w.j0 == 0 ? 1 : 0)) * CTAS + rank) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
@@ -665,10 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const int c0 = shares.of(from), c1 = shares.of(from + w.t.blocks - 1);
                 soft_sync();
                 // (release of what the block wrote before the barrier, acquire of what the others did)
-                if (tid == 0) s_last = arrive_gpu(P.counters + c0) == (unsigned)(c1 - c0);
+                if (tid == 0) s_last = arrive_gpu(P.counters + c0 * CTAS + rank) == (unsigned)(c1 - c0);
                 soft_sync();
                 if (s_last) {
-                    auto part = [&](int k) { return P.part + (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kSlot; };
+                    auto part = [&](int k) { return P.part + (int64_t)((2 * (c0 + k) + (k == 0 ? 1 : 0)) * CTAS + rank) * kSlot; };
                     auto sums = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * r)); };
                     float top = -INFINITY, total = 0.f;
                     for (int k = 0; k <= c1 - c0; ++k) top = fmaxf(top, sums(k).x);
@@ -694,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         if (live) finish(d, v, all);
                     }
                     finish_sum(top, total);
-                    if (tid == 0) P.counters[c0] = 0;
+                    if (tid == 0) P.counters[c0 * CTAS + rank] = 0;
                 }
             }
             tc_fence_before();
@@ -703,27 +736,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (kPair) cluster_sync_all();   // (no arrival or tensor-memory access of either CTA is still to come)
+    else __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) {
+        if (kPair) tmem_dealloc_pair(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int BITS, int D, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_pair_kernel(const __grid_constant__ ChunkParams P) { chunk_body<BITS, D, T, 2>(P); }
+
+// Clusters of the kernel that fit on the device at once (0 on error); sets its shared-memory attribute.  Kept per device.
+template <int BITS, int D, class T>
+int pairs_at_once(int device, int max_smem) {
+    static std::mutex mu;
+    static int known[kMaxDevices] = {};
+    constexpr int smem = ChunkSmem<BITS, D, 2>::kSize;
+    if (device < 0 || device >= kMaxDevices || smem > max_smem) return 0;
+    const std::lock_guard<std::mutex> lock(mu);
+    if (known[device] == 0) {
+        auto kernel = chunk_pair_kernel<BITS, D, T>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+        cudaGetLastError();
+        known[device] = n;
+    }
+    return known[device];
 }
 
 template <int BITS, int D, class T>
 lq_status run(lq_handle h, const ChunkParams& P, cudaStream_t stream) {
-    using M = ChunkSmem<BITS, D>;
-    static std::mutex mu;
-    static bool ready[kMaxDevices] = {};   // the shared-memory attribute is set
-    if (h->device < 0 || h->device >= kMaxDevices || M::kSize > h->max_smem_optin) return LQ_ERR_UNSUPPORTED;
-    {
-        const std::lock_guard<std::mutex> lock(mu);
-        if (!ready[h->device]) {
-            if (cudaFuncSetAttribute(chunk_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSize) != cudaSuccess)
-                return LQ_ERR_CUDA;
-            ready[h->device] = true;
-        }
-    }
-    if ((size_t)h->num_sms > h->num_counters || (size_t)h->num_sms * 2 * kRows * (D + 2) > h->partial_floats) return LQ_ERR_WORKSPACE;
-    return launch_overlapped(chunk_kernel<BITS, D, T>, h->num_sms, kThreads, M::kSize, stream, P);
+    const int pairs = pairs_at_once<BITS, D, T>(h->device, h->max_smem_optin);
+    if (pairs < 1) return LQ_ERR_UNSUPPORTED;
+    if ((size_t)pairs * 2 > h->num_counters || (size_t)pairs * 4 * kRows * (D + 2) > h->partial_floats) return LQ_ERR_WORKSPACE;
+    return launch_overlapped(chunk_pair_kernel<BITS, D, T>, dim3(2 * pairs), kThreads, ChunkSmem<BITS, D, 2>::kSize, stream, P);
 }
 
 }  // namespace

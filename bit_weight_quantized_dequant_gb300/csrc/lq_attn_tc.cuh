@@ -8,11 +8,11 @@
 namespace lq {
 
 constexpr int kTcKeys = 128;        // keys of a block
-// A K-major operand of D columns: rows of 64 values (128 bytes), kTcKeys of them an atom.
-template <int D>
+// A K-major operand of D columns and KEYS rows: rows of 64 values (128 bytes), KEYS of them an atom.
+template <int D, int KEYS = kTcKeys>
 struct TcOperand {
     static constexpr int kAtoms = D / 64;
-    static constexpr int kAtom = kTcKeys * 128;
+    static constexpr int kAtom = KEYS * 128;
 };
 
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return reinterpret_cast<__half2&>(v); }
@@ -56,10 +56,10 @@ __device__ __forceinline__ __half2 clamp_top(__half2 v) { return __hmin2_nan(v, 
 
 // Keys of one tile: [token][dims] rows of the K stage, in the order of the words' pairs (Q's columns
 // follow it), and Z.  left: tokens of the prefix from the tile's first on.
-template <int BITS, int D>
+template <int BITS, int D, int KEYS = kTcKeys>
 __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, uint8_t* zs, int zchunk, int tile_no, int left, int lane) {
     using L = KvLayout<BITS, D>;
-    using M = TcOperand<D>;
+    using M = TcOperand<D, KEYS>;
     constexpr int G = D / 32, WK = L::WK, U = WK / G;   // U words of a group (1 or 2)
     const int n = lane >> 2, t = lane & 3, odd = n & 1;
     // Odd tokens take their groups two by two in the other order (below: group st ^ odd at step st), so that
@@ -113,11 +113,12 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
     }
 }
 
-// Values of one tile: [dimension][keys] rows of the V stage, two keys per word.
-template <int BITS, int D>
-__device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, int tile_no, int left, int lane) {
+// Values of one tile: [dimension][keys] rows of the V stage, two keys per word.  PARTS = 2: only half of the dimensions, those
+// whose codes lie in the lower (part 0) or upper halves of the words.
+template <int BITS, int D, int PARTS = 1>
+__device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, int tile_no, int left, int lane, int part = 0) {
     using L = KvLayout<BITS, D>;
-    constexpr int G = D / 32, WV = L::WV;
+    constexpr int G = D / 32 / PARTS, WV = L::WV, kPer = 32 / BITS;
     const int n = lane >> 2, t = lane & 3;
     alignas(16) uint32_t vw[4 * WV];
 #pragma unroll
@@ -126,22 +127,25 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
     const uint32_t keep[2] = {(2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u),
                               (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u)};
     uint8_t* at[2] = {stage + n * 128 + (((2 * tile_no) ^ n) << 4) + 4 * t, stage + n * 128 + (((2 * tile_no + 1) ^ n) << 4) + 4 * t};
+    meta += part * G * 32;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const uint2 sv = lds64(meta + g * 32 + 8 * t), zv = lds64(meta + L::kMeta + g * 32 + 8 * t);
         const uint32_t s[2] = {sv.x & keep[0], sv.y & keep[1]}, z[2] = {zv.x & keep[0], zv.y & keep[1]};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int slab = 4 * g + k, wi = slab % WV, e = slab / WV;   // dimension 8 slab + n
+            const int slab = 4 * g + k, wi = slab % WV, e = slab / WV;   // dimension 8 slab + n (of the part's)
+            const uint32_t halves = PARTS == 2 ? (part ? 0x7632 : 0x5410) : e < kPer / 2 ? 0x5410 : 0x7632;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint32_t wa = vw[2 * half * WV + wi], wb = vw[(2 * half + 1) * WV + wi];
+                const uint32_t y = prmt(wa, wb, halves);
                 __half2 c;
                 if (BITS == 4) {
-                    const uint32_t y = prmt(wa, wb, e < 4 ? 0x5410 : 0x7632), w = (e & 2) ? y >> 8 : y;
+                    const uint32_t w = (e & 2) ? y >> 8 : y;
                     c = (e & 1) ? less_64(w & 0x00f000f0u) : less_1024(w & 0x000f000fu);
                 } else {
-                    const uint32_t y = prmt(wa, wb, e < 2 ? 0x5410 : 0x7632), w = (e & 1) ? y >> 8 : y;
+                    const uint32_t w = (e & 1) ? y >> 8 : y;
                     c = less_1024(w & 0x00ff00ffu);
                 }
                 const __half2 v = clamp_top(__hfma2(c, as_half2(s[half]), as_half2(z[half])));   // (S rounded up may pass it)
