@@ -39,11 +39,16 @@ constexpr int kRows = 128;          // rows of a CTA
 constexpr int kKeys = kTcKeys;      // keys of a block
 static_assert(kKeys == kChunkKeys, "key blocks");
 constexpr int kTiles = kKeys / kKvTile;
-// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4), then those that expand keys and
-// values, the one that issues MMAs and those that load keys' and values' bytes.
+// Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those of one
+// scheduler (number mod 4 = 0) issue MMAs and load, the other three schedulers' expand: the MMA warp's instructions, few
+// and each waited for by the tensor cores, are not in line behind theirs.
 constexpr int kSoftWarps = 8, kDqWarps = 4;      // (four for keys, four for values)
-constexpr int kKeyWarp = kSoftWarps, kValueWarp = kKeyWarp + kDqWarps, kMmaWarp = kValueWarp + kDqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kWarpsAll = 20, kThreads = 32 * kWarpsAll;   // (load warps: keys', values'; one is idle)
+constexpr int kMmaWarp = 8, kLoadWarp = 12;      // (load warps: 12 keys', 16 values')
+constexpr int kWarpsAll = 20, kThreads = 32 * kWarpsAll;
+__device__ __forceinline__ int dq_index(int warp) {   // which expanding warp (the first four keys'), -1: none
+    const int i = (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
+    return warp < kSoftWarps || warp % 4 == 0 || i >= 2 * kDqWarps ? -1 : i;
+}
 // tensor memory columns
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
@@ -88,6 +93,13 @@ __device__ __forceinline__ bool pair_any(int pair, bool mine) {
         : "r"((uint32_t)mine), "r"(2 + pair)
         : "memory");
     return any != 0;
+}
+
+// One lane of a whole warp, which the compiler knows to be one: operands of what it issues stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // The bits below n of 32 (n of any sign).
@@ -349,9 +361,9 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         else mbar_arrive(bar);
     };
 
-    if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    if (warp == kLoadWarp || warp == kLoadWarp + 4) {
         // ---------------------------------------------------------------- keys' or values' bytes into their ring
-        const int what = warp - kLoadWarp;
+        const int what = warp != kLoadWarp;
         const uint32_t full = what ? vr_full : kr_full, empty = what ? vr_empty : kr_empty;
         const uint32_t dst0 = smem_u32(base + (what ? M::kRawV : M::kRawK));
         const int stage_bytes = what ? M::kRawStageV : M::kRawStageK;
@@ -416,7 +428,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
                 wait(k_full + 8 * b, i >> 1);
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -439,7 +451,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     wait(v_full + 8 * b, i >> 1);
                     wait(p_full + 8 * b, i >> 1);
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint64_t v = vd + (M::kVStages == 2 && b ? 2 * M::kVAtom / 16 : 0);
 #pragma unroll
                         for (int st = 0; st < kKeys / 16; ++st)
@@ -453,10 +465,10 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
             }
         }
         __syncwarp();
-    } else if (warp >= kKeyWarp && warp < kMmaWarp) {
+    } else if (dq_index(warp) >= 0) {
         // ---------------------------------------------------------------- codes to operands
-        const bool keys = warp < kValueWarp;
-        const int wi = (warp - kKeyWarp) % kDqWarps, tiles = (keys ? M::kTilesHere : kTiles) / kDqWarps;   // this warp's tiles of every block
+        const bool keys = dq_index(warp) < kDqWarps;
+        const int wi = dq_index(warp) % kDqWarps, tiles = (keys ? M::kTilesHere : kTiles) / kDqWarps;   // this warp's tiles of every block
         const uint32_t full = keys ? kr_full : vr_full, empty = keys ? kr_empty : vr_empty;
         uint8_t* raw = base + (keys ? M::kRawK : M::kRawV);
         int s = 0, turn = 0, i = 0;
