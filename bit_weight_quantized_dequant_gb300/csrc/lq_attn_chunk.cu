@@ -42,13 +42,20 @@ constexpr int kTiles = kKeys / kKvTile;
 // Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those of one
 // scheduler (number mod 4 = 0) issue MMAs and load, the other three schedulers' expand: the MMA warp's instructions, few
 // and each waited for by the tensor cores, are not in line behind theirs.
-constexpr int kSoftWarps = 8, kDqWarps = 4;      // (four for keys, four for values)
+constexpr int kSoftWarps = 8, kKeyWarps = 4, kValueWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 12;      // (load warps: 12 keys', 16 values')
-constexpr int kWarpsAll = 20, kThreads = 32 * kWarpsAll;
+constexpr int kWarpsAll = 24, kThreads = 32 * kWarpsAll;
 __device__ __forceinline__ int dq_index(int warp) {   // which expanding warp (the first four keys'), -1: none
-    const int i = (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
-    return warp < kSoftWarps || warp % 4 == 0 || i >= 2 * kDqWarps ? -1 : i;
+    return warp < kSoftWarps || warp % 4 == 0 ? -1 : (warp - kSoftWarps) / 4 * 3 + warp % 4 - 1;
 }
+// P = 2^kPUp p in binary16, and a row's reference moves when a score passes it by 2^kPast: P stays below 2^15, and a move,
+// for which the sums so far are read and written, is rare.  (2^-33 is what a probability is off by at least.)
+constexpr float kPUp = 8.f, kPast = 7.f;
+
+// registers of a thread at launch (what its bounds give), then of the softmax's and the others'
+constexpr int kRegs = 80, kSoftRegs = 112, kOtherRegs = 64;
+static_assert(32 * (kSoftWarps * kSoftRegs + (kWarpsAll - kSoftWarps) * kOtherRegs) <= kThreads * kRegs, "registers");
+static_assert((kWarpsAll - kSoftWarps) / 4 * 3 == kKeyWarps + kValueWarps, "expanding warps");
 // tensor memory columns
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
@@ -84,16 +91,9 @@ struct ChunkSmem {
 };
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
-// Whether any thread of a row's two warps says so (and a barrier of the two).
-__device__ __forceinline__ bool pair_any(int pair, bool mine) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"((uint32_t)mine), "r"(2 + pair)
-        : "memory");
-    return any != 0;
-}
+// From a warp to the other warp of its rows and back: what it wrote before is there for the other.
+__device__ __forceinline__ void tell(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void hear(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 // One lane of a whole warp, which the compiler knows to be one: operands of what it issues stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -266,18 +266,44 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
     return *out;
 }
 
+// Whether a tile's keys may have terms S c past the end of binary16's range (all lanes together).
+template <int BITS, int D>
+__device__ __forceinline__ bool wide_keys(const uint8_t* meta, int lane) {
+    constexpr uint32_t kMost = BITS == 4 ? 0x6c00u : 0x5c00u;   // 4096 and 256
+    uint2 x = make_uint2(0u, 0u);
+    if (8 * lane < KvLayout<BITS, D>::kMeta) x = lds64(meta + 8 * lane);
+    const uint32_t over = ((x.x & 0x7fff7fffu) + (0x7fffu - kMost) * 0x10001u) | ((x.y & 0x7fff7fffu) + (0x7fffu - kMost) * 0x10001u);
+    return __any_sync(0xffffffffu, (over & 0x80008000u) != 0);
+}
+// Whether a tile's values S c + Z may, or are no numbers.
+template <int BITS, int D>
+__device__ __forceinline__ bool wide_values(const uint8_t* meta, int lane) {
+    using L = KvLayout<BITS, D>;
+    constexpr uint32_t kMostS = BITS == 4 ? 0x6400u : 0x5400u, kMostZ = 0x7400u;   // 1024 and 64, 16384
+    uint2 x = make_uint2(0u, 0u);
+    if (8 * lane < 2 * L::kMeta) x = lds64(meta + 8 * lane);
+    const uint32_t room = (0x7fffu - (8 * lane < L::kMeta ? kMostS : kMostZ)) * 0x10001u;
+    const uint32_t over = ((x.x & 0x7fff7fffu) + room) | ((x.y & 0x7fff7fffu) + room);
+    return __any_sync(0xffffffffu, (over & 0x80008000u) != 0);
+}
+// Seldom, and so not in the way of the others' instructions: tiles whose terms are clamped.
+template <int BITS, int D, int KEYS>
+__device__ __noinline__ void expand_wide_keys(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, uint8_t* zs, int zchunk, int tile_no, int left, int lane) {
+    expand_keys<BITS, D, KEYS, true>(tile, meta, stage, zs, zchunk, tile_no, left, lane);
+}
+template <int BITS, int D, int PARTS>
+__device__ __noinline__ void expand_wide_values(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, int tile_no, int left, int lane, int part) {
+    expand_values<BITS, D, PARTS, true>(tile, meta, stage, tile_no, left, lane, part);
+}
+
 // Value groups of one tile whose S or Z is no number are left out of meta (made 0) and recorded in bad[16], a bit per group
 // of the tile's tokens.  Returns whether there is one.
 template <int BITS, int D>
-__device__ __forceinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, int lane) {
+__device__ __noinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, int lane) {
     using L = KvLayout<BITS, D>;
     constexpr int G = D / 32;
-    uint2 x = make_uint2(0u, 0u);          // four of the S and Z
-    if (8 * lane < 2 * L::kMeta) x = lds64(meta + 8 * lane);
-    const uint32_t top = ((x.x & 0x7c007c00u) + 0x04000400u) | ((x.y & 0x7c007c00u) + 0x04000400u);   // (a carry where an exponent is all ones)
-    if (!__any_sync(0xffffffffu, (top & 0x80008000u) != 0)) return false;
+    uint32_t mask = 0;
     if (lane < 16) {       // lane: the token's place in the rows of S and Z
-        uint32_t mask = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint16_t* s = reinterpret_cast<uint16_t*>(meta + g * 32 + 2 * lane);
@@ -291,7 +317,7 @@ __device__ __forceinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad
         bad[2 * (lane >> 2) + (lane & 1) + 8 * (lane >> 1 & 1)] = (uint8_t)mask;
     }
     __syncwarp();
-    return true;
+    return __any_sync(0xffffffffu, mask != 0);
 }
 
 // CTAS = 2: a cluster of two CTAs takes units of 256 rows, 128 in each one's tensor memory.  The even CTA issues the pair's
@@ -312,6 +338,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     __shared__ Range s_range;
     __shared__ int64_t s_total;
     __shared__ int s_last;
+    __shared__ volatile int s_past[2][4];              // the last block in which a half's warp met a score past its row's reference
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = kPair ? (int)cluster_rank() : 0;
 
@@ -320,18 +347,19 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     const uint32_t kr_full = bars, kr_empty = kr_full + 8 * M::kRaw, vr_full = kr_empty + 8 * M::kRaw, vr_empty = vr_full + 8 * M::kRaw;
     const uint32_t s_full = vr_empty + 8 * M::kRaw, o_done = s_full + 16, k_full = o_done + 16, v_full = k_full + 16, p_full = v_full + 16;
     const uint32_t q_full = p_full + 16;
+    if (tid < 8) s_past[tid >> 2][tid & 3] = -1;
     if (tid == 0) {
         for (int i = 0; i < M::kRaw; ++i) {
             mbar_init(kr_full + 8 * i, 1);
-            mbar_init(kr_empty + 8 * i, kDqWarps);
+            mbar_init(kr_empty + 8 * i, kKeyWarps);
             mbar_init(vr_full + 8 * i, 1);
-            mbar_init(vr_empty + 8 * i, kDqWarps);
+            mbar_init(vr_empty + 8 * i, kValueWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(s_full + 8 * b, 1);
             mbar_init(o_done + 8 * b, 1);
-            mbar_init(k_full + 8 * b, CTAS * kDqWarps);
-            mbar_init(v_full + 8 * b, CTAS * kDqWarps);
+            mbar_init(k_full + 8 * b, CTAS * kKeyWarps);
+            mbar_init(v_full + 8 * b, CTAS * kValueWarps);
             mbar_init(p_full + 8 * b, CTAS * kSoftWarps);
         }
         mbar_init(q_full, CTAS * 4);
@@ -361,6 +389,9 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         else mbar_arrive(bar);
     };
 
+    // The softmax warps hold a row's scores, the others little: kThreads * kRegs registers at launch, as many afterwards.
+    if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp || warp == kLoadWarp + 4) {
         // ---------------------------------------------------------------- keys' or values' bytes into their ring
         const int what = warp != kLoadWarp;
@@ -467,8 +498,10 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         __syncwarp();
     } else if (dq_index(warp) >= 0) {
         // ---------------------------------------------------------------- codes to operands
-        const bool keys = dq_index(warp) < kDqWarps;
-        const int wi = dq_index(warp) % kDqWarps, tiles = (keys ? M::kTilesHere : kTiles) / kDqWarps;   // this warp's tiles of every block
+        const bool keys = dq_index(warp) < kKeyWarps;
+        const int wi = keys ? dq_index(warp) : dq_index(warp) - kKeyWarps;
+        constexpr int tiles = M::kTilesHere / kKeyWarps;                     // this warp's tiles of every block: of keys, and one of values
+        static_assert(kValueWarps == kTiles, "a tile of values for each warp");
         const uint32_t full = keys ? kr_full : vr_full, empty = keys ? kr_empty : vr_empty;
         uint8_t* raw = base + (keys ? M::kRawK : M::kRawV);
         int s = 0, turn = 0, i = 0;
@@ -481,18 +514,28 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
                 if (!keys && i >= M::kVStages) wait(o_done + 8 * ((i - M::kVStages) & 1), (i - M::kVStages) >> 1);
                 const uint32_t there = s_there[keys ? 0 : 1][i & 7];
-                for (int k = 0; k < tiles; ++k) {
-                    const int here = wi * tiles + k, no = keys ? rank * M::kTilesHere + here : here;   // tile of the stage, of the block
-                    uint8_t* tile = raw + s * (keys ? M::kRawStageK : M::kRawStageV) + here * M::kRawTile;
-                    const int left = there >> no & 1u ? end - kb * kKeys - no * kKvTile : 0;
-                    if (keys) {
-                        expand_keys<BITS, D, M::kKeysHere>(tile, tile + L::kCodes, base + M::kK + b * M::kKStage, base + M::kZ, 2 * b, here, left, lane);
-                    } else {
-                        const bool odd = (there >> no & 1u) && leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + no * kKvTile, lane);
-                        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[no] = odd;
-                        expand_values<BITS, D, CTAS>(tile, tile + L::kCodes, base + M::kV + ((M::kVStages == 2 ? 2 * b : 0) + no / 4) * M::kVAtom, no % 4,
-                                                     left, lane, rank);
+                if (keys) {
+#pragma unroll 1
+                    for (int k = 0; k < tiles; ++k) {
+                        const int here = wi * tiles + k, no = rank * M::kTilesHere + here;   // tile of the stage, of the block
+                        const uint8_t* tile = raw + s * M::kRawStageK + here * M::kRawTile;
+                        const int left = there >> no & 1u ? end - kb * kKeys - no * kKvTile : 0;
+                        uint8_t *stage = base + M::kK + b * M::kKStage, *zs = base + M::kZ;
+                        if (wide_keys<BITS, D>(tile + L::kCodes, lane)) expand_wide_keys<BITS, D, M::kKeysHere>(tile, tile + L::kCodes, stage, zs, 2 * b, here, left, lane);
+                        else expand_keys<BITS, D, M::kKeysHere, false>(tile, tile + L::kCodes, stage, zs, 2 * b, here, left, lane);
                     }
+                } else {
+                    uint8_t* tile = raw + s * M::kRawStageV + wi * M::kRawTile;
+                    const int left = there >> wi & 1u ? end - kb * kKeys - wi * kKvTile : 0;
+                    uint8_t* stage = base + M::kV + ((M::kVStages == 2 ? 2 * b : 0) + wi / 4) * M::kVAtom;
+                    bool no_numbers = false;
+                    if ((there >> wi & 1u) && wide_values<BITS, D>(tile + L::kCodes, lane)) {
+                        no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + wi * kKvTile, lane);
+                        expand_wide_values<BITS, D, CTAS>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                    } else {
+                        expand_values<BITS, D, CTAS, false>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                    }
+                    if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[wi] = no_numbers;
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -503,10 +546,13 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 if (++s == M::kRaw) s = 0, ++turn;
             }
         }
-    } else if (warp < kSoftWarps) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ---------------------------------------------------------------- softmax: two threads per row
-        const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block
+        const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block, and half of the dimensions
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int mine = 2 + 2 * (warp & 3) + half, other = mine ^ 1, both = 10 + (warp & 3);   // barriers
         int done = 0;
         for (Walk<CTAS> w(P, R); w.more; w.next()) {
             const int nb = w.j1 - w.j0, row0 = (w.u.rt * CTAS + rank) * kRows, rows = min(kRows, w.q.fresh * P.group - row0);
@@ -583,45 +629,70 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & 3) * kKeys + k];
                 }
             };
+            // The product of block i.  A wait tells a barrier's phases apart by their parity alone: the product before on this
+            // barrier, of block i - 2, has ended when this is called (see the scores' wait), and the one after waits for P.
+            auto wait_o = [&](int i) {
+                wait(o_done + 8 * (i & 1), i >> 1);
+                tc_fence_after();
+            };
             for (int j = 0; j < nb; ++j) {
                 const int i = done + j, b = i & 1, kb = w.t.block(w.j0 + j);
                 wait(s_full + 8 * b, i >> 1);
                 tc_fence_after();
                 const uint32_t col = lanes + kColS + kKeys * b + 64 * half;
-                const bool whole = w.t.whole(kb, P.window, P.sinks);
-                const uint32_t there = s_there[0][i & 7] >> (half * kTiles / 2) & ((1u << kTiles / 2) - 1u);
-                const bool some = !whole || there != (1u << kTiles / 2) - 1u;
-                const int first = kb * kKeys + 64 * half;
-                // 32 scores at a time, read twice (for the maximum and for P): registers are what 28 warps leave
-                auto load = [&](int h, float (&x)[32]) {
-                    tmem_ld32(col + 32 * h, reinterpret_cast<uint32_t(&)[32]>(x));
-                    if (some) {
-                        const int j0 = first + 32 * h;
-                        uint32_t sees = below(p + 1 - j0);
-                        if (P.window > 0) sees &= ~below(p + 1 - P.window - j0) | below(P.sinks - j0);
-                        sees &= (there >> (2 * h) & 1u ? 0xffffu : 0u) | (there >> (2 * h + 1) & 1u ? 0xffff0000u : 0u);
+                const uint32_t there = s_there[0][i & 7] >> (half * kTiles / 2);
+                const bool some = !w.t.whole(kb, P.window, P.sinks) || (there & ((1u << kTiles / 2) - 1u)) != (1u << kTiles / 2) - 1u;
+                auto hide = [&](int h, uint32_t (&x)[32]) {
+                    const int j0 = kb * kKeys + 64 * half + 32 * h;
+                    uint32_t sees = below(p + 1 - j0);
+                    if (P.window > 0) sees &= ~below(p + 1 - P.window - j0) | below(P.sinks - j0);
+                    sees &= (there >> (2 * h) & 1u ? 0xffffu : 0u) | (there >> (2 * h + 1) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(sees >> k & 1u)) x[k] = -INFINITY;
+                    for (int k = 0; k < 32; ++k)
+                        if (!(sees >> k & 1u)) x[k] = 0xff800000u;
+                };
+                uint32_t xa[32], xb[32];
+                auto load = [&] {
+                    tmem_ld32_issue(col, xa);
+                    tmem_ld32_issue(col + 32, xb);
+                    tmem_ld32_wait(xa);
+                    tmem_ld32_waited(xb);
+                    if (some) hide(0, xa), hide(1, xb);
+                };
+                float2 sum;
+                auto probabilities = [&](uint32_t (&x)[32], uint32_t (&pr)[16]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(f, f), make_float2(-ref, -ref));
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum = add2(sum, e);
+                        pr[k / 2] = pack_half2_rn(e.x, e.y);
                     }
                 };
-                float mx = -INFINITY;
+                load();
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    load(h, x);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) mx = fmaxf(fmaxf(mx, x[k]), x[k + 1]);
+                for (int k = 0; k < 32; k += 2) {
+                    top4[k / 2 & 1] = fmaxf(fmaxf(top4[k / 2 & 1], __uint_as_float(xa[k])), __uint_as_float(xa[k + 1]));
+                    top4[2 + (k / 2 & 1)] = fmaxf(fmaxf(top4[2 + (k / 2 & 1)], __uint_as_float(xb[k])), __uint_as_float(xb[k + 1]));
                 }
-                mx *= f;
-                if (pair_any(warp & 3, mx > m + kTau)) {
+                float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * f;
+                // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile
+                const bool past = __any_sync(0xffffffffu, mx > m + kPast);
+                if (past && lane == 0) s_past[half][warp & 3] = i;
+                tell(mine);
+                uint32_t pa[16], pb[16];
+                sum = make_float2(0.f, 0.f);
+                probabilities(xa, pa);
+                probabilities(xb, pb);
+                hear(other);
+                if (past || s_past[half ^ 1][warp & 3] == i) {         // (both warps of the rows alike)
                     ml[half * kRows + r] = mx;
-                    pair_any(warp & 3, false);
+                    asm volatile("bar.sync %0, 64;" ::"r"(both) : "memory");
                     mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
-                    const float now = mx > m + kTau ? mx : m, a = m == now ? 1.f : ex2(m - now);
-                    if (j > 0 && __any_sync(0xffffffffu, m != now)) {   // each thread its half of O's dimensions
-                        wait(o_done + 8 * (b ^ 1), (i - 1) >> 1);
-                        tc_fence_after();
+                    const float now = mx > m + kPast ? mx : m, a = m == now ? 1.f : ex2(m - now);
+                    if (j > 0 && __any_sync(0xffffffffu, m != now)) {  // each thread its half of O's dimensions
+                        wait_o(i - 1);
 #pragma unroll 1
                         for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
                             uint32_t o[32];
@@ -633,40 +704,32 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     }
                     l *= a;
                     m = now;
-                    ref = now == -INFINITY ? 0.f : now - kPBits;
+                    ref = now == -INFINITY ? 0.f : now - kPUp;
+                    load();
+                    sum = make_float2(0.f, 0.f);
+                    probabilities(xa, pa);
+                    probabilities(xb, pb);
                 }
-                // The O before, whether or not a reference moved (see lq_attn_prefix.cu).
-                if (i > 0) wait(o_done + 8 * (b ^ 1), (i - 1) >> 1);
-                if (j > 0) odd_values(i - 1, w.t.block(w.j0 + j - 1));
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    load(h, x);
-                    uint32_t pr[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float2 y = fma2(make_float2(x[k], x[k + 1]), make_float2(f, f), make_float2(-ref, -ref));
-                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                        sum = add2(sum, e);
-                        pr[k / 2] = pack_half2_rn(e.x, e.y);
-                    }
-                    tmem_st16(col + 16 * h, pr);   // (over scores that have been read)
-                }
+                tmem_st16_issue(col, pa);      // (over scores that have been read)
+                tmem_st16_issue(col + 16, pb);
                 l += sum.x + sum.y;
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(p_full + 8 * b);
+                // (with a block's scores the product of the block before the last is done too: MMAs end in their order)
+                if (j >= 2) odd_values(i - 2, w.t.block(w.j0 + j - 2));
             }
 
             // ---- the unit's rows: each thread half of its row's dimensions ----
+            const int last = done + nb - 1;
             soft_sync();   // (the maxima's last readers are done)
             ml[half * kRows + r] = l;
             soft_sync();
             l = ml[r] + ml[kRows + r];
-            wait(o_done + 8 * ((done + nb - 1) & 1), (done + nb - 1) >> 1);
-            tc_fence_after();
-            odd_values(done + nb - 1, w.t.block(w.j1 - 1));
+            wait_o(last);
+            if (nb >= 2) odd_values(last - 1, w.t.block(w.j1 - 2));
+            odd_values(last, w.t.block(w.j1 - 1));
             uint16_t* out = static_cast<uint16_t*>(P.out) + at * P.out_stride + (int64_t)qh * D;
             auto finish = [&](int d, float (&v)[32], float inv) {      // 32 dimensions from d on
 #pragma unroll
@@ -679,7 +742,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
             };
             auto finish_sum = [&](float top, float total) {
                 if (half == 0 && live && P.lse)
-                    P.lse[at * P.q_heads + qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPBits) * 0.6931471805599453f;
+                    P.lse[at * P.q_heads + qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPUp) * 0.6931471805599453f;
             };
             const bool all_here = w.j0 == 0 && w.j1 == w.t.blocks;
             constexpr int kSlot = kRows * (D + 2);

@@ -53,10 +53,12 @@ __device__ __forceinline__ __half2 code_pair(uint32_t w, int r) {
 
 // Not past the end of binary16's range (NaN stays).
 __device__ __forceinline__ __half2 clamp_top(__half2 v) { return __hmin2_nan(v, __float2half2_rn(65504.f)); }
+template <bool CLAMP>
+__device__ __forceinline__ __half2 clamped(__half2 v) { return CLAMP ? clamp_top(v) : v; }
 
 // Keys of one tile: [token][dims] rows of the K stage, in the order of the words' pairs (Q's columns
 // follow it), and Z.  left: tokens of the prefix from the tile's first on.
-template <int BITS, int D, int KEYS = kTcKeys>
+template <int BITS, int D, int KEYS = kTcKeys, bool CLAMP = true>
 __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, uint8_t* zs, int zchunk, int tile_no, int left, int lane) {
     using L = KvLayout<BITS, D>;
     using M = TcOperand<D, KEYS>;
@@ -97,9 +99,9 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2 c = code_pair<BITS>(kw[U * st + i / (4 / U)], i % (4 / U)), p = clamp_top(__hmul2(c, s2));
+                const __half2 c = code_pair<BITS>(kw[U * st + i / (4 / U)], i % (4 / U)), p = clamped<CLAMP>(__hmul2(c, s2));
                 hi[i] = as_bits(p);
-                lo[i] = as_bits(clamp_top(__hfma2(c, s2, __hneg2(p))));     // c S - p, exactly (unless p was clamped)
+                lo[i] = as_bits(clamped<CLAMP>(__hfma2(c, s2, __hneg2(p))));     // c S - p, exactly (unless p was clamped)
             }
             uint8_t* at = base + (st & 1 ? odd_at : even_at) + (st >> 1) * M::kAtom;
             sts128(at, hi[0], hi[1], hi[2], hi[3]);
@@ -115,7 +117,7 @@ __device__ __forceinline__ void expand_keys(const uint8_t* tile, const uint8_t* 
 
 // Values of one tile: [dimension][keys] rows of the V stage, two keys per word.  PARTS = 2: only half of the dimensions, those
 // whose codes lie in the lower (part 0) or upper halves of the words.
-template <int BITS, int D, int PARTS = 1>
+template <int BITS, int D, int PARTS = 1, bool CLAMP = true>
 __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t* meta, uint8_t* stage, int tile_no, int left, int lane, int part = 0) {
     using L = KvLayout<BITS, D>;
     constexpr int G = D / 32 / PARTS, WV = L::WV, kPer = 32 / BITS;
@@ -148,7 +150,7 @@ __device__ __forceinline__ void expand_values(const uint8_t* tile, const uint8_t
                     const uint32_t w = (e & 1) ? y >> 8 : y;
                     c = less_1024(w & 0x00ff00ffu);
                 }
-                const __half2 v = clamp_top(__hfma2(c, as_half2(s[half]), as_half2(z[half])));   // (S rounded up may pass it)
+                const __half2 v = clamped<CLAMP>(__hfma2(c, as_half2(s[half]), as_half2(z[half])));   // (S rounded up may pass it)
                 *reinterpret_cast<uint32_t*>(at[half] + slab * 1024) = as_bits(v);
             }
         }

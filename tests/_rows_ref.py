@@ -7,7 +7,8 @@ Bounds, with u = 2^-11 the relative rounding of a binary16:
 * a probability is rounded by u.  lq_kv_attention: P S against c and P against Z, each by u, with |S c| <= |v| + |Z|, so
   u (|v| + 2 |Z|) per unit of probability (its half-step figure u / 2 twice).  lq_kv_attention_chunk: P by u and the value
   itself by u, or by 2^-25 below 2^-14;
-* P counts in units of 2^-11 and is a subnormal binary16 below 2^-14: 2^-36 of a value's size for each of n keys;
+* lq_kv_attention holds P in units of 2^-11, lq_kv_attention_chunk of 2^-8; below 2^-14 it is a subnormal binary16, off by
+  2^-25: 2^-36 and 2^-33 of a value's size for each of n keys;
 * the output's own rounding: 2^-8 of it for bfloat16, 2^-11 for binary16.
 """
 from __future__ import annotations
@@ -154,7 +155,7 @@ class Rows:
                 else:
                     zmass = attend(q[rows, hs], k, z, seen, self.scale)[0]
                     bound = (2.0 ** -11 + 2.0 ** -18 * (1 + size[..., None])) * (mass + 2 * zmass)
-                bound = bound + ulp * np.abs(o) + (2.0 ** -24 + n * 2.0 ** -36) * most
+                bound = bound + ulp * np.abs(o) + (2.0 ** -24 + n * 2.0 ** (-33 if dense else -36)) * most
                 err = np.abs(got - o)
                 worst = max(worst, float((err / (bound + 1e-30)).max()))
                 assert np.all(err <= bound + 1e-30), (b, h, float((err / (bound + 1e-30)).max()))
