@@ -61,8 +61,8 @@ constexpr int kTmemCols = 512;
 constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
 constexpr int kColO = 256;          // D
 constexpr int kColQ = 384;          // D / 2
-constexpr int kColZ = 448;          // 8 (group sums of q), 32 written
-static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 32 <= kTmemCols, "tensor memory");
+constexpr int kColZ = 448;          // 8 (group sums of q)
+static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 8 <= kTmemCols, "tensor memory");
 
 // Shared memory of one of CTAS CTAs: its share of a block's keys (rows of K) and of the dimensions (rows of V).
 template <int BITS, int D, int CTAS>
@@ -81,19 +81,20 @@ struct ChunkSmem {
     static constexpr int kV = kZ + kAtom;
     static constexpr int kRawK = kV + kVStages * 2 * kVAtom, kRawV = kRawK + kRaw * kRawStageK;
     static constexpr int kMl = kRawV + kRaw * kRawStageV;        // [2 halves][rows] maxima, then sums
-    static constexpr int kF = kMl + 2 * kRows * 4;               // [rows] score factors
-    static constexpr int kBad = kF + kRows * 4;                  // [4 blocks][keys] groups of a value that are no numbers
+    static constexpr int kF = kMl + 2 * kRows * 4;               // [2 halves][rows] queries' largest values
+    static constexpr int kGroups = kF + 2 * kRows * 4;           // [rows] queries' group sums, their rests
+    static constexpr int kBad = kGroups + kRows * 2 * (D / 32) * 2;                  // [4 blocks][keys] groups of a value that are no numbers
     static constexpr int kBars = kBad + 4 * kKeys;
     static constexpr int kNumBars = 4 * kRaw + 2 * 5 + 1;
     static constexpr int kSize = 1024 + kBars + 8 * kNumBars;
     static_assert(kSize <= 226 * 1024 && kBars % 8 == 0 && kRawK % 128 == 0 && kRawTile % 16 == 0, "shared memory");
-    static_assert(8 * (kMaxAttnBatch + 1) <= 2 * kKStage, "the requests' running sums lie where K will");
+    static_assert(3 * 8 * (kMaxAttnBatch + 1) <= 2 * kKStage, "the requests' running sums lie where K will");
 };
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
-// From a warp to the other warp of its rows and back: what it wrote before is there for the other.
-__device__ __forceinline__ void tell(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void hear(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// The two warps of the same rows.  (Both wait: with an arrival of its own for each direction, a warp that is ahead could arrive
+// twice before the other has waited once.)
+__device__ __forceinline__ void rows_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory"); }
 
 // One lane of a whole warp, which the compiler knows to be one: operands of what it issues stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -123,6 +124,20 @@ template <int CTAS>
 __device__ __forceinline__ ChunkTile tile_of(const ChunkParams& P, const Request& q, int rt) {
     return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, CTAS * kRows, rt);
 }
+
+// A thread's row of a unit: its place in q and out, its head, its token's position.
+struct Row {
+    int64_t at;
+    int qh, p;
+    bool live;
+    __device__ __forceinline__ Row(const ChunkParams& P, const Request& q, const Unit& u, int ctas, int rank, int r) {
+        const int row = (u.rt * ctas + rank) * kRows + r, tok = (unsigned)row / (unsigned)P.group;
+        live = row < q.fresh * P.group;
+        at = (int64_t)q.row0 + tok;
+        qh = u.head * P.group + (row - tok * P.group);
+        p = live ? q.len - q.fresh + tok : -1;
+    }
+};
 
 // A thread block's share: from block `j0` of unit `first` (at `place` of the sequence) to before block `j1` of unit `last`.
 struct Range {
@@ -173,10 +188,17 @@ struct Walk {
     }
 };
 
-// (All threads of a CTA together.)  The share of party c of C; `cum` has room for requests + 1 sums.
+// Parties that share a sequence of places: so many that none has fewer than kLeast, which costs less than joining a unit's parts.
+__device__ __forceinline__ int parties(int64_t total, int C) {
+    constexpr int kLeast = 2 * kChunkUnitCost;
+    return total >= (int64_t)kLeast * C ? C : max(1, (int)total / kLeast);
+}
+
+// (All threads of a CTA together.)  The share of party c of C; `cum` has room for three sums of each request.
 template <int CTAS>
 __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, int64_t* cum, int64_t* total_out, Range* out) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto from_of = [&](int which) { return cum + (which + 1) * (kMaxAttnBatch + 1); };   // where each request's places begin, two copies
     // places of each request
     for (int b = warp; b < P.requests; b += kWarpsAll) {
         const Request q(P, b);
@@ -192,34 +214,35 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
         if (lane == 0) cum[b + 1] = sum * P.cache.kv_heads;
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp < 2) {        // the first place by one warp, the last by another
         int64_t base = 0;
         for (int b0 = 0; b0 < P.requests; b0 += 32) {
-            int64_t v = b0 + lane < P.requests ? cum[b0 + lane + 1] : 0;
+            const int64_t mine = b0 + lane < P.requests ? cum[b0 + lane + 1] : 0;
+            int64_t v = mine;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int64_t x = __shfl_up_sync(0xffffffffu, v, s);
                 if (lane >= s) v += x;
             }
-            if (b0 + lane < P.requests) cum[b0 + lane + 1] = base + v;
+            if (b0 + lane < P.requests) from_of(warp)[b0 + lane] = base + v - mine;
             base += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) cum[0] = 0;
         __syncwarp();
-        const int64_t total = base;
-        const WideShares shares(total, C);
+        const int64_t total = base, *start = from_of(warp);
+        const int all = parties(total, C);
+        const WideShares shares(total, all);
         // the unit and block at or after a place: lane-parallel over the row tiles of its request
         auto find = [&](int64_t at, Unit& u, int& j, int64_t& place) {
             int lo = 0, hi = P.requests - 1;             // the last request that begins at or before `at` (and has rows)
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (cum[mid] <= at) lo = mid;
+                if (start[mid] <= at) lo = mid;
                 else hi = mid - 1;
             }
             u.b = lo;
             const Request q(P, lo);
             const int tiles = chunk_tiles(q.fresh, P.group, CTAS * kRows), heads = P.cache.kv_heads;
-            int64_t from = cum[lo];
+            int64_t from = start[lo];
             for (int r0 = 0; r0 < tiles; r0 += 32) {
                 const int64_t each = r0 + lane < tiles ? tile_of<CTAS>(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
                 int64_t v = each * heads;
@@ -243,27 +266,25 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
                 from += __shfl_sync(0xffffffffu, v, 31);
             }
         };
-        Range r;
-        const int64_t g0 = shares.first(c), g1 = shares.first(c + 1);
-        r.none = g0 >= g1;
-        r.first = r.last = Unit{0, 0, 0};
-        r.j0 = r.j1 = 0;
-        r.place = 0;
-        if (!r.none) {
-            int64_t last_place;
-            int j_last;
-            find(g0, r.first, r.j0, r.place);
-            find(g1 - 1, r.last, j_last, last_place);
+        const int64_t g0 = c < all ? shares.first(c) : total, g1 = c < all ? shares.first(c + 1) : total;
+        Unit u{0, 0, 0};
+        int j = 0;
+        int64_t place = 0;
+        if (g0 < g1) find(warp == 0 ? g0 : g1 - 1, u, j, place);
+        if (lane == 0 && warp == 0) {
+            out->none = g0 >= g1;
+            out->first = u, out->j0 = j, out->place = place;
+            *total_out = total;
+        } else if (lane == 0) {
             // blocks of the last unit before place g1
-            const int64_t k = g1 - last_place - kChunkUnitCost;
-            r.j1 = k > 0 ? (int)k : 0;
-            const bool same = r.first.b == r.last.b && r.first.rt == r.last.rt && r.first.head == r.last.head;
-            r.none = same && r.j1 <= r.j0;
+            const int64_t k = g1 - place - kChunkUnitCost;
+            out->last = u, out->j1 = k > 0 ? (int)k : 0;
         }
-        if (lane == 0) *out = r, *total_out = total;
     }
     __syncthreads();
-    return *out;
+    Range r = *out;
+    r.none |= r.first.b == r.last.b && r.first.rt == r.last.rt && r.first.head == r.last.head && r.j1 <= r.j0;
+    return r;
 }
 
 // Whether a tile's keys may have terms S c past the end of binary16's range (all lanes together).
@@ -331,14 +352,14 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms; alike in both CTAs)
     float* ml = reinterpret_cast<float*>(base + M::kMl);
-    float* factors = reinterpret_cast<float*>(base + M::kF);
+    float* tops = reinterpret_cast<float*>(base + M::kF);
     __shared__ uint32_t s_tmem;
     __shared__ volatile uint32_t s_there[2][8];        // a block's tiles in the cache, for keys (all of them) and values (no role is 8 ahead of another)
     __shared__ volatile unsigned long long s_odd[4];   // a byte per tile of a block: whether it has values that are no numbers (read up to two blocks later)
     __shared__ Range s_range;
     __shared__ int64_t s_total;
     __shared__ int s_last;
-    __shared__ volatile int s_past[2][4];              // the last block in which a half's warp met a score past its row's reference
+    __shared__ volatile int s_past[2][2][4];           // [odd or even blocks]: the last block in which a half's warp met a score past its row's reference
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = kPair ? (int)cluster_rank() : 0;
 
@@ -347,7 +368,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     const uint32_t kr_full = bars, kr_empty = kr_full + 8 * M::kRaw, vr_full = kr_empty + 8 * M::kRaw, vr_empty = vr_full + 8 * M::kRaw;
     const uint32_t s_full = vr_empty + 8 * M::kRaw, o_done = s_full + 16, k_full = o_done + 16, v_full = k_full + 16, p_full = v_full + 16;
     const uint32_t q_full = p_full + 16;
-    if (tid < 8) s_past[tid >> 2][tid & 3] = -1;
+    if (tid < 16) s_past[tid >> 3][tid >> 2 & 1][tid & 3] = -1;
     if (tid == 0) {
         for (int i = 0; i < M::kRaw; ++i) {
             mbar_init(kr_full + 8 * i, 1);
@@ -362,7 +383,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
             mbar_init(v_full + 8 * b, CTAS * kValueWarps);
             mbar_init(p_full + 8 * b, CTAS * kSoftWarps);
         }
-        mbar_init(q_full, CTAS * 4);
+        mbar_init(q_full, CTAS * kSoftWarps);
         fence_mbar_init();
     }
     // (the odd chunks of the Z rows multiply nothing: zero for good)
@@ -552,72 +573,74 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         // ---------------------------------------------------------------- softmax: two threads per row
         const int half = warp >> 2, r = 32 * (warp & 3) + lane;        // keys 64 half .. + 63 of a block, and half of the dimensions
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const int mine = 2 + 2 * (warp & 3) + half, other = mine ^ 1, both = 10 + (warp & 3);   // barriers
-        int done = 0;
-        for (Walk<CTAS> w(P, R); w.more; w.next()) {
-            const int nb = w.j1 - w.j0, row0 = (w.u.rt * CTAS + rank) * kRows, rows = min(kRows, w.q.fresh * P.group - row0);
-            const int row = row0 + r, tok = row / P.group, qh = w.u.head * P.group + (row - tok * P.group);
-            const int64_t at = (int64_t)w.q.row0 + tok;
-            const bool live = r < rows;
-            if (half == 0) {
-                // Q, scaled by a power of two into [2^9, 2^10), its columns in the order of K's rows
-                float top = 0.f;
-                const uint16_t* src = static_cast<const uint16_t*>(P.q) + at * P.q_stride + (int64_t)qh * D;
-#pragma unroll 8
-                for (int k = 0; k < D / 8; ++k) {
-                    const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        // A unit's queries: scaled by a power of two into [2^9, 2^10), their columns in the order of K's rows, and the sums of their
+        // groups in two terms; each thread half of its row's dimensions.  Returns what scores are multiplied by.
+        auto put_queries = [&](const Row& x) {
+            const uint16_t* src = static_cast<const uint16_t*>(P.q) + x.at * P.q_stride + (int64_t)x.qh * D + half * (D / 2);
+            uint4 v[D / 16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(elem_to_float<T>((uint16_t)(x[e >> 1] >> (16 * (e & 1))))));
-                }
-                int e = top > 0.f ? 9 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-                e = min(max(e, -120), 120);
-                const float up = pow2i(e);
-                factors[r] = fmaxf(P.scale_log2 * pow2i(-e), 0x1p-126f);   // (a hidden score is -inf times it)
-                uint32_t z[32];
+            for (int k = 0; k < D / 16; ++k) v[k] = x.live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+            float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = 0u;
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t y[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {                     // 64 dimensions: 32 columns
-                    uint32_t o[32];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 64 * h + 8 * k) : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                        float f[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = elem_to_float<T>((uint16_t)(x[i >> 1] >> (16 * (i & 1)))) * up;
-                        if (BITS == 4) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) o[4 * k + i] = pack_half2_rn(f[i], f[i + 4]);
-                        } else {
-                            o[4 * k] = pack_half2_rn(f[0], f[2]), o[4 * k + 1] = pack_half2_rn(f[1], f[3]);
-                            o[4 * k + 2] = pack_half2_rn(f[4], f[6]), o[4 * k + 3] = pack_half2_rn(f[5], f[7]);
-                        }
-                    }
-                    tmem_st32(lanes + kColQ + 32 * h, o);
-#pragma unroll
-                    for (int gg = 0; gg < 2; ++gg) {                   // sums of the rounded values of a group
-                        float sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 p = unpack2(o[16 * gg + i]);
-                            sum += p.x + p.y;
-                        }
-                        const int g = 2 * h + gg;
-                        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
-                        z[g >> 1] |= (uint32_t)__half_as_ushort(hi) << (16 * (g & 1));
-                        z[G / 2 + (g >> 1)] |= (uint32_t)__half_as_ushort(lo) << (16 * (g & 1));
-                    }
-                }
-                tmem_st32(lanes + kColZ, z);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(q_full);
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(elem_to_float<T>((uint16_t)(y[e >> 1] >> (16 * (e & 1))))));
             }
-            soft_sync();   // the factors
-            const float f = factors[r];
-            const int p = live ? w.q.len - w.q.fresh + tok : -1;       // the row's position
+            tops[half * kRows + r] = top;
+            soft_sync();
+            top = fmaxf(top, tops[(half ^ 1) * kRows + r]);
+            int e = top > 0.f ? 9 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+            e = min(max(e, -120), 120);
+            const float up = pow2i(e);
+            __half* z = reinterpret_cast<__half*>(base + M::kGroups) + r * 2 * G;
+#pragma unroll
+            for (int h = 0; h < G / 2; ++h) {                              // 32 dimensions: 16 columns
+                const int g = half * (G / 2) + h;
+                uint32_t o[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 q = v[4 * h + k];
+                    const uint32_t y[4] = {q.x, q.y, q.z, q.w};
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = elem_to_float<T>((uint16_t)(y[i >> 1] >> (16 * (i & 1)))) * up;
+                    if (BITS == 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[4 * k + i] = pack_half2_rn(f[i], f[i + 4]);
+                    } else {
+                        o[4 * k] = pack_half2_rn(f[0], f[2]), o[4 * k + 1] = pack_half2_rn(f[1], f[3]);
+                        o[4 * k + 2] = pack_half2_rn(f[4], f[6]), o[4 * k + 3] = pack_half2_rn(f[5], f[7]);
+                    }
+                }
+                tmem_st16_issue(lanes + kColQ + 16 * g, o);
+                float sum = 0.f;                                           // of the rounded values
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 w = unpack2(o[i]);
+                    sum += w.x + w.y;
+                }
+                z[g] = __float2half_rn(sum);
+                z[G + g] = __float2half_rn(sum - __half2float(z[g]));
+            }
+            soft_sync();
+            if (half == 0) {
+                const uint32_t* y = reinterpret_cast<const uint32_t*>(z);
+                tmem_st4_issue(lanes + kColZ, y[0], y[1], G == 4 ? y[2 % G] : 0u, G == 4 ? y[3 % G] : 0u);
+                tmem_st4_issue(lanes + kColZ + 4, 0, 0, 0, 0);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(q_full);
+            return fmaxf(P.scale_log2 * pow2i(-e), 0x1p-126f);             // (a hidden score is -inf times it)
+        };
+        int done = 0;
+        Walk<CTAS> w(P, R);
+        Row row(P, w.q, w.u, CTAS, rank, r);
+        float f = w.more ? put_queries(row) : 0.f;
+        while (w.more) {
+            const int nb = w.j1 - w.j0, p = row.p;
             float m = -INFINITY, l = 0.f, ref = 0.f;
             uint32_t poison = 0;                                       // groups of dimensions that saw no number
             // the value groups of a block (whose product is done) that this row saw and that are no numbers
@@ -677,18 +700,20 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     top4[2 + (k / 2 & 1)] = fmaxf(fmaxf(top4[2 + (k / 2 & 1)], __uint_as_float(xb[k])), __uint_as_float(xb[k + 1]));
                 }
                 float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * f;
-                // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile
-                const bool past = __any_sync(0xffffffffu, mx > m + kPast);
-                if (past && lane == 0) s_past[half][warp & 3] = i;
-                tell(mine);
+                // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile.  (In a unit's
+                // first block there is none yet.)
+                const bool past = j > 0 && __any_sync(0xffffffffu, mx > m + kPast);
+                if (past && lane == 0) s_past[i & 1][half][warp & 3] = i;
                 uint32_t pa[16], pb[16];
                 sum = make_float2(0.f, 0.f);
-                probabilities(xa, pa);
-                probabilities(xb, pb);
-                hear(other);
-                if (past || s_past[half ^ 1][warp & 3] == i) {         // (both warps of the rows alike)
+                if (j > 0) {
+                    probabilities(xa, pa);
+                    probabilities(xb, pb);
+                    rows_sync(warp & 3);
+                }
+                if (j == 0 || past || s_past[i & 1][half ^ 1][warp & 3] == i) {   // (both warps of the rows alike)
                     ml[half * kRows + r] = mx;
-                    asm volatile("bar.sync %0, 64;" ::"r"(both) : "memory");
+                    rows_sync(warp & 3);
                     mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
                     const float now = mx > m + kPast ? mx : m, a = m == now ? 1.f : ex2(m - now);
                     if (j > 0 && __any_sync(0xffffffffu, m != now)) {  // each thread its half of O's dimensions
@@ -721,16 +746,28 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 if (j >= 2) odd_values(i - 2, w.t.block(w.j0 + j - 2));
             }
 
+            // ---- the next unit's queries, whose scores are computed while this one's rows are written ----
+            const int last = done + nb - 1, kb_last = w.t.block(w.j1 - 1), kb_before = w.t.block(max(w.j1 - 2, w.j0));
+            const bool all_here = w.j0 == 0 && w.j1 == w.t.blocks;
+            const int64_t place = w.place;
+            const int from_first = w.j0, unit_blocks = w.t.blocks;
+            const Row here = row;
+            float f_next = 0.f;
+            w.next();
+            if (w.more) {
+                row = Row(P, w.q, w.u, CTAS, rank, r);
+                f_next = put_queries(row);
+            } else {
+                soft_sync();   // (as in there: the maxima's last readers are done)
+            }
             // ---- the unit's rows: each thread half of its row's dimensions ----
-            const int last = done + nb - 1;
-            soft_sync();   // (the maxima's last readers are done)
             ml[half * kRows + r] = l;
             soft_sync();
             l = ml[r] + ml[kRows + r];
             wait_o(last);
-            if (nb >= 2) odd_values(last - 1, w.t.block(w.j1 - 2));
-            odd_values(last, w.t.block(w.j1 - 1));
-            uint16_t* out = static_cast<uint16_t*>(P.out) + at * P.out_stride + (int64_t)qh * D;
+            if (nb >= 2) odd_values(last - 1, kb_before);
+            odd_values(last, kb_last);
+            uint16_t* out = static_cast<uint16_t*>(P.out) + here.at * P.out_stride + (int64_t)here.qh * D;
             auto finish = [&](int d, float (&v)[32], float inv) {      // 32 dimensions from d on
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
@@ -741,12 +778,11 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 }
             };
             auto finish_sum = [&](float top, float total) {
-                if (half == 0 && live && P.lse)
-                    P.lse[at * P.q_heads + qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPUp) * 0.6931471805599453f;
+                if (half == 0 && here.live && P.lse)
+                    P.lse[here.at * P.q_heads + here.qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPUp) * 0.6931471805599453f;
             };
-            const bool all_here = w.j0 == 0 && w.j1 == w.t.blocks;
             constexpr int kSlot = kRows * (D + 2);
-            float* slot = P.part + (int64_t)((2 * c + (w.j0 == 0 ? 1 : 0)) * CTAS + rank) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
+            float* slot = P.part + (int64_t)((2 * c + (from_first == 0 ? 1 : 0)) * CTAS + rank) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
@@ -757,7 +793,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     for (int k = 0; k < 32; ++k) v[k] = NAN;
                 }
                 if (all_here) {
-                    if (live) finish(d, v, inv);
+                    if (here.live) finish(d, v, inv);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
@@ -768,9 +804,9 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 finish_sum(m, l);
             } else {
                 if (half == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m, l);
-                const WideShares shares(s_total, C);
-                const int64_t from = w.place + kChunkUnitCost;
-                const int c0 = shares.of(from), c1 = shares.of(from + w.t.blocks - 1);
+                const WideShares shares(s_total, parties(s_total, C));
+                const int64_t from = place + kChunkUnitCost;
+                const int c0 = shares.of(from), c1 = shares.of(from + unit_blocks - 1);
                 soft_sync();
                 // (release of what the block wrote before the barrier, acquire of what the others did)
                 if (tid == 0) s_last = arrive_gpu(P.counters + c0 * CTAS + rank) == (unsigned)(c1 - c0);
@@ -799,15 +835,16 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                                 v[4 * q + 2] = fmaf(x.z, e, v[4 * q + 2]), v[4 * q + 3] = fmaf(x.w, e, v[4 * q + 3]);
                             }
                         }
-                        if (live) finish(d, v, all);
+                        if (here.live) finish(d, v, all);
                     }
                     finish_sum(top, total);
                     if (tid == 0) P.counters[c0 * CTAS + rank] = 0;
                 }
             }
             tc_fence_before();
-            soft_sync();   // both halves are done with O, the factors and the sums
+            soft_sync();   // both halves are done with O and the sums
             done += nb;
+            f = f_next;
         }
     }
     tc_fence_before();

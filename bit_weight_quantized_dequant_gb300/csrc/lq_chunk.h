@@ -9,7 +9,7 @@
 namespace lq {
 
 constexpr int kChunkKeys = 128;      // keys of a block
-constexpr int kChunkUnitCost = 6;    // what a unit costs a thread block, in its key blocks
+constexpr int kChunkUnitCost = 3;    // what a unit costs a thread block, in its key blocks
 
 // Tile `rt` (of `tile_rows` rows) of a request of `len` tokens of which `fresh` are new: its rows are (new token, query head of
 // the group), tokens slower.  window 0: none.
@@ -19,13 +19,12 @@ struct ChunkTile {
     int sunk, gap;     // key blocks that hold sinks only, and those left out behind them
     int blocks;        // key blocks that it visits, 1 at least
     LQ_HD ChunkTile(int len, int fresh, int group, int window, int sinks, int tile_rows, int rt) {
-        const int64_t r0 = (int64_t)rt * tile_rows, rows = (int64_t)fresh * group;
-        const int64_t r1 = (r0 + tile_rows < rows ? r0 + tile_rows : rows) - 1;
-        p0 = len - fresh + (int)(r0 / group);
-        p1 = len - fresh + (int)(r1 / group);
+        const unsigned r0 = (unsigned)rt * tile_rows, rows = (unsigned)fresh * group, all = r0 + tile_rows;   // (below 2^31)
+        p0 = len - fresh + (int)(r0 / (unsigned)group);
+        p1 = len - fresh + (int)(((all < rows ? all : rows) - 1) / (unsigned)group);
         lowest = window > 0 && p0 >= window ? p0 - window + 1 : 0;
         const int from = lowest / kChunkKeys, end = (p1 < 0 ? 0 : p1 / kChunkKeys + 1);
-        const int s = (int)(((int64_t)sinks + kChunkKeys - 1) / kChunkKeys);
+        const int s = (int)(((unsigned)sinks + kChunkKeys - 1) / kChunkKeys);
         sunk = s < from ? s : from;
         gap = from - sunk;
         blocks = end - gap > 1 ? end - gap : 1;
@@ -38,7 +37,7 @@ struct ChunkTile {
     }
 };
 
-LQ_HD int chunk_tiles(int fresh, int group, int tile_rows) { return (int)(((int64_t)fresh * group + tile_rows - 1) / tile_rows); }
+LQ_HD int chunk_tiles(int fresh, int group, int tile_rows) { return (int)(((unsigned)fresh * group + tile_rows - 1) / (unsigned)tile_rows); }
 
 // n things shared out to c parties in order, as Shares, past 32 bits.
 struct WideShares {
