@@ -692,26 +692,34 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                         pr[k / 2] = pack_half2_rn(e.x, e.y);
                     }
                 };
-                load();
-                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    top4[k / 2 & 1] = fmaxf(fmaxf(top4[k / 2 & 1], __uint_as_float(xa[k])), __uint_as_float(xa[k + 1]));
-                    top4[2 + (k / 2 & 1)] = fmaxf(fmaxf(top4[2 + (k / 2 & 1)], __uint_as_float(xb[k])), __uint_as_float(xb[k + 1]));
-                }
-                float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * f;
-                // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile.  (In a unit's
-                // first block there is none yet.)
-                const bool past = j > 0 && __any_sync(0xffffffffu, mx > m + kPast);
-                if (past && lane == 0) s_past[i & 1][half][warp & 3] = i;
                 uint32_t pa[16], pb[16];
-                sum = make_float2(0.f, 0.f);
+                bool past = false;
                 if (j > 0) {
+                    // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile
+                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto larger = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top4[k / 2 & 3] = fmaxf(fmaxf(top4[k / 2 & 3], __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+                    };
+                    sum = make_float2(0.f, 0.f);
+                    load();
                     probabilities(xa, pa);
+                    larger(xa);
                     probabilities(xb, pb);
+                    larger(xb);
+                    past = __any_sync(0xffffffffu, fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * f > m + kPast);
+                    if (past && lane == 0) s_past[i & 1][half][warp & 3] = i;
                     rows_sync(warp & 3);
                 }
-                if (j == 0 || past || s_past[i & 1][half ^ 1][warp & 3] == i) {   // (both warps of the rows alike)
+                if (j == 0 || past || s_past[i & 1][half ^ 1][warp & 3] == i) {   // (both warps of the rows alike; in a unit's first block there is no reference yet)
+                    load();
+                    float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        mx = fmaxf(fmaxf(mx, __uint_as_float(xa[k])), __uint_as_float(xa[k + 1]));
+                        my = fmaxf(fmaxf(my, __uint_as_float(xb[k])), __uint_as_float(xb[k + 1]));
+                    }
+                    mx = fmaxf(mx, my) * f;
                     ml[half * kRows + r] = mx;
                     rows_sync(warp & 3);
                     mx = fmaxf(mx, ml[(half ^ 1) * kRows + r]);
@@ -726,11 +734,11 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
                             tmem_st32(lanes + kColO + d, o);
                         }
+                        load();
                     }
                     l *= a;
                     m = now;
                     ref = now == -INFINITY ? 0.f : now - kPUp;
-                    load();
                     sum = make_float2(0.f, 0.f);
                     probabilities(xa, pa);
                     probabilities(xb, pb);
