@@ -58,7 +58,7 @@ static_assert(32 * (kSoftWarps * kSoftRegs + (kWarpsAll - kSoftWarps) * kOtherRe
 static_assert((kWarpsAll - kSoftWarps) / 4 * 3 == kKeyWarps + kValueWarps, "expanding warps");
 // tensor memory columns
 constexpr int kTmemCols = 512;
-constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64
+constexpr int kColS = 0;            // 2 x 128: S; then P, each half of the keys in the first 32 columns of its 64 (what its rounding left out in the others)
 constexpr int kColO = 256;          // D
 constexpr int kColQ = 384;          // D / 2
 constexpr int kColZ = 448;          // 8 (group sums of q)
@@ -349,6 +349,8 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     using M = ChunkSmem<BITS, D, CTAS>;
     constexpr int G = D / 32;
     constexpr bool kPair = CTAS == 2;
+    // Binary16 outputs, whose own rounding is no coarser than that of P to binary16: what it left out is multiplied too.
+    constexpr bool kFine = IsHalf<T>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // (the swizzle's 1024-byte atoms; alike in both CTAs)
     float* ml = reinterpret_cast<float*>(base + M::kMl);
@@ -509,6 +511,12 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                         for (int st = 0; st < kKeys / 16; ++st)
                             mma(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4), v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16,
                                 idO, j != 0 || st != 0);
+                        if (kFine) {
+#pragma unroll
+                            for (int st = 0; st < kKeys / 16; ++st)
+                                mma(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 32 + 8 * (st % 4),
+                                    v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, 1);
+                        }
                         commit(o_done + 8 * b);
                     }
                     __syncwarp();
@@ -683,16 +691,20 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     if (some) hide(0, xa), hide(1, xb);
                 };
                 float2 sum;
-                auto probabilities = [&](uint32_t (&x)[32], uint32_t (&pr)[16]) {
+                auto probabilities = [&](uint32_t (&x)[32], uint32_t (&pr)[16], uint32_t (&rest)[16]) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(f, f), make_float2(-ref, -ref));
                         const float2 e = make_float2(ex2(y.x), ex2(y.y));
                         sum = add2(sum, e);
                         pr[k / 2] = pack_half2_rn(e.x, e.y);
+                        if (kFine) {
+                            const float2 h = unpack2(pr[k / 2]);
+                            rest[k / 2] = pack_half2_rn(e.x - h.x, e.y - h.y);
+                        }
                     }
                 };
-                uint32_t pa[16], pb[16];
+                uint32_t pa[16], pb[16], ra[16], rb[16];
                 bool past = false;
                 if (j > 0) {
                     // P by the reference as it is; whether it has to move, in the other half too, turns out meanwhile
@@ -703,9 +715,9 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     };
                     sum = make_float2(0.f, 0.f);
                     load();
-                    probabilities(xa, pa);
+                    probabilities(xa, pa, ra);
                     larger(xa);
-                    probabilities(xb, pb);
+                    probabilities(xb, pb, rb);
                     larger(xb);
                     past = __any_sync(0xffffffffu, fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * f > m + kPast);
                     if (past && lane == 0) s_past[i & 1][half][warp & 3] = i;
@@ -740,11 +752,15 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     m = now;
                     ref = now == -INFINITY ? 0.f : now - kPUp;
                     sum = make_float2(0.f, 0.f);
-                    probabilities(xa, pa);
-                    probabilities(xb, pb);
+                    probabilities(xa, pa, ra);
+                    probabilities(xb, pb, rb);
                 }
                 tmem_st16_issue(col, pa);      // (over scores that have been read)
                 tmem_st16_issue(col + 16, pb);
+                if (kFine) {
+                    tmem_st16_issue(col + 32, ra);
+                    tmem_st16_issue(col + 48, rb);
+                }
                 l += sum.x + sum.y;
                 tmem_st_wait();
                 tc_fence_before();

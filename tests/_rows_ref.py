@@ -5,8 +5,8 @@ Bounds, with u = 2^-11 the relative rounding of a binary16:
 * a score is off by at most 2^-20 * scale * sum_d |q_d k_jd| (fp32 sums of D products, and the exponential's 2^-22), so lse by
   the largest such amount plus 2^-19, and each probability by twice that, relatively;
 * a probability is rounded by u.  lq_kv_attention: P S against c and P against Z, each by u, with |S c| <= |v| + |Z|, so
-  u (|v| + 2 |Z|) per unit of probability (its half-step figure u / 2 twice).  lq_kv_attention_chunk: P by u and the value
-  itself by u, or by 2^-25 below 2^-14;
+  u (|v| + 2 |Z|) per unit of probability (its half-step figure u / 2 twice).  lq_kv_attention_chunk: the value itself by u,
+  or by 2^-25 below 2^-14, and P by u, for binary16 outputs (which multiply what that left out too) by u^2;
 * lq_kv_attention holds P in units of 2^-11, lq_kv_attention_chunk of 2^-8; below 2^-14 it is a subnormal binary16, off by
   2^-25: 2^-36 and 2^-33 of a value's size for each of n keys;
 * the output's own rounding: 2^-8 of it for bfloat16, 2^-11 for binary16.
@@ -151,7 +151,8 @@ class Rows:
                 assert np.all(e <= 2.0 ** -20 * size[live] + 2.0 ** -19), (b, h, e.max())
                 most = np.abs(v[seen.any(0)]).max() if seen.any() else 0.0
                 if dense:
-                    bound = (2.0 ** -10 + 2.0 ** -22 + 2.0 ** -18 * (1 + size[..., None])) * mass + 2.0 ** -25
+                    of_p = 2.0 ** -11 if ulp > 2.0 ** -11 else 2.0 ** -22
+                    bound = (2.0 ** -11 + of_p + 2.0 ** -22 + 2.0 ** -18 * (1 + size[..., None])) * mass + 2.0 ** -25
                 else:
                     zmass = attend(q[rows, hs], k, z, seen, self.scale)[0]
                     bound = (2.0 ** -11 + 2.0 ** -18 * (1 + size[..., None])) * (mass + 2 * zmass)
