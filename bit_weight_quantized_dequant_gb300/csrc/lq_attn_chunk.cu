@@ -1,15 +1,48 @@
 // Attention of chunks of new tokens over the low-bit KV cache, on the tensor-memory tensor cores.
 //
-// A unit is 128 rows of one kv head of one request (rows are (new token, query head of the group), tokens slower) and the key
-// blocks that they see: a dense contraction as in lq_attn_prefix.cu, whose roles, operands and precision this kernel has, with
-// these differences.
+// A unit is 256 rows of one kv head of one request (rows are (new token, query head of the group), tokens slower) and the
+// blocks of 128 keys that they see.  A pair of CTAs takes it, 128 rows in each one's tensor memory:
+//   S [rows][128 keys] = Q K^T     Q in tensor memory, K in shared memory
+//   P = 2^(S f - m)                S read from and P written to tensor memory
+//   O [rows][D]       += P V       P in tensor memory, V [D][128 keys] in shared memory
+// by tcgen05.mma.cta_group::2 (M 256, binary16 operands, fp32 sums), of whose other operand each CTA holds half: the keys of
+// half a block, the values' half of the dimensions.  So each code is expanded once for 256 rows; one CTA with 128 rows
+// spent its issue slots on that (2048 tokens at the end of 32 Ki, 64 query heads over 8, 128 dimensions, 4 bits, bf16: 3582 us,
+// the pair 2985 with all else as it was).
+//
+// Operands and precision are those of lq_attn_prefix.cu: K's code part as two binary16 terms and its offset part as one more MMA
+// of 16 columns, so that scores keep fp32 precision; V and P rounded to binary16.  Binary16 outputs, whose own rounding is no
+// coarser, multiply what P's left out too (error of windowed chunks 3.2e-4 -> 2.9e-4, where the output's rounding alone is
+// 2.1e-4; 37 -> 42 us).  Terms past the end of binary16's range are clamped, in tiles whose S or Z say that there may be some.
+//
+// What is this kernel's own:
 //   - Every request has rows, pages and a length of its own, read on the device.  All units' key blocks form one sequence,
-//     each unit counted with its fixed cost, which the thread blocks share evenly (lq_chunk.h); a unit that is cut
-//     leaves partial sums in the workspace, and the last of its thread blocks to arrive joins them in order.
+//     each unit counted with its fixed cost, which the pairs share evenly (lq_chunk.h); a unit that is cut leaves partial
+//     sums in the workspace, and the last of its pairs to arrive joins them in order (results repeat bit for bit).
 //   - A row sees the tokens up to its own, and with a window the last of them and the sinks.  Blocks that no row of the unit
 //     sees are not visited; in one that not every row sees whole, scores are masked by two bounds per row.
 //   - A P of 0 times a cached NaN is NaN, so a value group (token and 32 dimensions) whose S or Z is no number counts as 0
 //     in the product, and rows that do see it get NaN in those dimensions at the unit's end.
+//
+// Roles (23 warps of 24): two load keys' and values' bytes by bulk copies, each into a ring of its own; one issues the MMAs (in
+// the even CTA); twelve expand codes, a 16-token tile each, four this CTA's keys, eight its half of all values' dimensions;
+// eight do the softmax, two threads per row with half of the keys each.  S and the stages of K and V are double: the next
+// block's scores are computed while this one's softmax runs.  All MMAs come from one thread and end in its order, so few
+// barriers suffice: K full, scores there (which frees K's stage and says that the product of the block before the last is done),
+// P full, V full, O done.  A wait tells a barrier's phases apart by their parity alone: every role waits for each phase
+// in turn, or at a point where the one before is known to have ended.  Every wait on a barrier in memory is bounded; a role whose
+// wait ran out goes on with what is there, so every loop ends, and the status word reports it.
+//
+// The steps from there, the same call: the MMA warp on a scheduler without expanding warps and its operands in uniform registers
+// (one elected lane) 2427 us; scores held in registers (read once), P by the reference so far while the two halves of a row find out
+// whether it has to move, which a limit of 2^7 makes rare, and clamps only where needed 2176; maximum and P of a block in one go 2027
+// (1050 TFLOP/s, 55 % of a library product's rate).  A unit's queries are put in place, and the scores begin, before the rows of the unit
+// before are written: a prompt of 2048 tokens of 40 heads 110 -> 98 us, 65 tokens at 365 17.9 -> 12.8.  Measured and not kept: a thread per row and every other
+// block for each half of the softmax warps (2527), a whole row's check by the sum of its P (2286), the next block's scores loaded ahead
+// (spills: 2900), queries by bulk copies one unit ahead (short calls 9 % slower), a longer suspension of waiting warps (no change).
+//
+// What bounds it now: the softmax of a block takes about 1900 cycles from its scores to its P, one block after another,
+// where its 25 MMAs take 1620 (tensor pipe 58 %, issue 63 %).
 
 #include <algorithm>
 #include <mutex>
@@ -30,11 +63,12 @@ struct ChunkParams {
     int requests, tokens, group, q_heads, max_len;
     int window, sinks;
     float scale_log2;
-    float* part;           // partial sums: 2 slots per thread block
-    unsigned* counters;    // one per thread block, zero between calls
+    float* part;           // partial sums: 2 slots per CTA
+    unsigned* counters;    // one per CTA, zero between calls
     int* status;
 };
 
+constexpr int kCtas = 2;            // CTAs of a pair
 constexpr int kRows = 128;          // rows of a CTA
 constexpr int kKeys = kTcKeys;      // keys of a block
 static_assert(kKeys == kChunkKeys, "key blocks");
@@ -64,22 +98,21 @@ constexpr int kColQ = 384;          // D / 2
 constexpr int kColZ = 448;          // 8 (group sums of q)
 static_assert(kColO + 128 <= kColQ && kColQ + 64 <= kColZ && kColZ + 8 <= kTmemCols, "tensor memory");
 
-// Shared memory of one of CTAS CTAs: its share of a block's keys (rows of K) and of the dimensions (rows of V).
-template <int BITS, int D, int CTAS>
+// Shared memory of one CTA of the pair: its half of a block's keys (rows of K) and of the dimensions (rows of V).
+template <int BITS, int D>
 struct ChunkSmem {
     using L = KvLayout<BITS, D>;
-    static constexpr int kKeysHere = kKeys / CTAS, kTilesHere = kTiles / CTAS, kDimsHere = D / CTAS;
+    static constexpr int kKeysHere = kKeys / kCtas, kTilesHere = kTiles / kCtas, kDimsHere = D / kCtas;
     static constexpr int kAtoms = TcOperand<D, kKeysHere>::kAtoms, kAtom = TcOperand<D, kKeysHere>::kAtom;
     static constexpr int kKStage = 2 * kAtoms * kAtom;           // K rounded, K's rest
     static constexpr int kVAtom = kDimsHere * 128;               // [dimensions][64 keys]
-    static constexpr int kVStages = CTAS == 2 ? 2 : 1;
     static constexpr int kRawTile = L::kCodes + 2 * L::kMeta;    // a tile's keys (or values): codes, S, Z
     static constexpr int kRawStageK = kTilesHere * kRawTile, kRawStageV = kTiles * kRawTile;
-    static constexpr int kRaw = CTAS == 2 ? (L::kBytes <= 2560 ? 4 : 3) : L::kBytes <= 2560 ? 2 : 1;   // blocks in flight
+    static constexpr int kRaw = L::kBytes <= 2560 ? 4 : 3;       // blocks in flight
     static constexpr int kK = 0;
     static constexpr int kZ = kK + 2 * kKStage;                  // Z of stage b in chunk 2 b of each key's row
-    static constexpr int kV = kZ + kAtom;
-    static constexpr int kRawK = kV + kVStages * 2 * kVAtom, kRawV = kRawK + kRaw * kRawStageK;
+    static constexpr int kV = kZ + kAtom;                        // two stages
+    static constexpr int kRawK = kV + 2 * 2 * kVAtom, kRawV = kRawK + kRaw * kRawStageK;
     static constexpr int kMl = kRawV + kRaw * kRawStageV;        // [2 halves][rows] maxima, then sums
     static constexpr int kF = kMl + 2 * kRows * 4;               // [2 halves][rows] queries' largest values
     static constexpr int kGroups = kF + 2 * kRows * 4;           // [rows] queries' group sums, their rests
@@ -120,9 +153,8 @@ struct Request {
         len = min(max(P.lens[b], 0), P.max_len);
     }
 };
-template <int CTAS>
 __device__ __forceinline__ ChunkTile tile_of(const ChunkParams& P, const Request& q, int rt) {
-    return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, CTAS * kRows, rt);
+    return ChunkTile(q.len, q.fresh, P.group, P.window, P.sinks, kCtas * kRows, rt);
 }
 
 // A thread's row of a unit: its place in q and out, its head, its token's position.
@@ -130,8 +162,8 @@ struct Row {
     int64_t at;
     int qh, p;
     bool live;
-    __device__ __forceinline__ Row(const ChunkParams& P, const Request& q, const Unit& u, int ctas, int rank, int r) {
-        const int row = (u.rt * ctas + rank) * kRows + r, tok = (unsigned)row / (unsigned)P.group;
+    __device__ __forceinline__ Row(const ChunkParams& P, const Request& q, const Unit& u, int rank, int r) {
+        const int row = (u.rt * kCtas + rank) * kRows + r, tok = (unsigned)row / (unsigned)P.group;
         live = row < q.fresh * P.group;
         at = (int64_t)q.row0 + tok;
         qh = u.head * P.group + (row - tok * P.group);
@@ -139,7 +171,7 @@ struct Row {
     }
 };
 
-// A thread block's share: from block `j0` of unit `first` (at `place` of the sequence) to before block `j1` of unit `last`.
+// A pair's share: from block `j0` of unit `first` (at `place` of the sequence) to before block `j1` of unit `last`.
 struct Range {
     Unit first, last;
     int j0, j1;
@@ -148,18 +180,17 @@ struct Range {
 };
 
 // A walk over a share's units; every role has one.
-template <int CTAS>
 struct Walk {
     const ChunkParams& P;
     Range R;
     Unit u;
     Request q;
     ChunkTile t;
-    int j0, j1;          // blocks of this unit that are this thread block's
+    int j0, j1;          // blocks of this unit that are this pair's
     int64_t place;       // of the unit's cost, its blocks follow
     bool more;
     __device__ __forceinline__ Walk(const ChunkParams& P_, const Range& r)
-        : P(P_), R(r), u(r.first), q(P_, r.first.b), t(tile_of<CTAS>(P_, q, r.first.rt)), place(r.place), more(!r.none) {
+        : P(P_), R(r), u(r.first), q(P_, r.first.b), t(tile_of(P_, q, r.first.rt)), place(r.place), more(!r.none) {
         j0 = r.j0;
         set_end();
     }
@@ -177,12 +208,12 @@ struct Walk {
         j0 = 0;
         if (++u.head == P.cache.kv_heads) {
             u.head = 0;
-            if (++u.rt == chunk_tiles(q.fresh, P.group, CTAS * kRows)) {
+            if (++u.rt == chunk_tiles(q.fresh, P.group, kCtas * kRows)) {
                 u.rt = 0;
                 do ++u.b; while (Request(P, u.b).fresh == 0);   // (the last unit lies ahead)
                 q = Request(P, u.b);
             }
-            t = tile_of<CTAS>(P, q, u.rt);
+            t = tile_of(P, q, u.rt);
         }
         set_end();
     }
@@ -195,7 +226,6 @@ __device__ __forceinline__ int parties(int64_t total, int C) {
 }
 
 // (All threads of a CTA together.)  The share of party c of C; `cum` has room for three sums of each request.
-template <int CTAS>
 __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, int64_t* cum, int64_t* total_out, Range* out) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto from_of = [&](int which) { return cum + (which + 1) * (kMaxAttnBatch + 1); };   // where each request's places begin, two copies
@@ -206,9 +236,9 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
             const int a0 = P.starts[b], a1 = P.starts[b + 1];
             if (a0 < 0 || a1 < a0 || a1 > P.tokens) atomicOr(P.status, kStatusIndex);
         }
-        const int tiles = chunk_tiles(q.fresh, P.group, CTAS * kRows);
+        const int tiles = chunk_tiles(q.fresh, P.group, kCtas * kRows);
         int64_t sum = 0;
-        for (int rt = lane; rt < tiles; rt += 32) sum += tile_of<CTAS>(P, q, rt).blocks + kChunkUnitCost;
+        for (int rt = lane; rt < tiles; rt += 32) sum += tile_of(P, q, rt).blocks + kChunkUnitCost;
 #pragma unroll
         for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         if (lane == 0) cum[b + 1] = sum * P.cache.kv_heads;
@@ -241,10 +271,10 @@ __device__ __forceinline__ Range range_of(const ChunkParams& P, int c, int C, in
             }
             u.b = lo;
             const Request q(P, lo);
-            const int tiles = chunk_tiles(q.fresh, P.group, CTAS * kRows), heads = P.cache.kv_heads;
+            const int tiles = chunk_tiles(q.fresh, P.group, kCtas * kRows), heads = P.cache.kv_heads;
             int64_t from = start[lo];
             for (int r0 = 0; r0 < tiles; r0 += 32) {
-                const int64_t each = r0 + lane < tiles ? tile_of<CTAS>(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
+                const int64_t each = r0 + lane < tiles ? tile_of(P, q, r0 + lane).blocks + kChunkUnitCost : 0;
                 int64_t v = each * heads;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -341,14 +371,11 @@ __device__ __noinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, i
     return __any_sync(0xffffffffu, mask != 0);
 }
 
-// CTAS = 2: a cluster of two CTAs takes units of 256 rows, 128 in each one's tensor memory.  The even CTA issues the pair's
-// MMAs (M 256), of whose other operand each CTA holds half: the keys of half a block, the values' half of the dimensions.
-template <int BITS, int D, class T, int CTAS>
-__device__ __forceinline__ void chunk_body(const ChunkParams& P) {
+template <int BITS, int D, class T>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams P) {
     using L = KvLayout<BITS, D>;
-    using M = ChunkSmem<BITS, D, CTAS>;
+    using M = ChunkSmem<BITS, D>;
     constexpr int G = D / 32;
-    constexpr bool kPair = CTAS == 2;
     // Binary16 outputs, whose own rounding is no coarser than that of P to binary16: what it left out is multiplied too.
     constexpr bool kFine = IsHalf<T>::value;
     extern __shared__ uint8_t smem_raw[];
@@ -363,10 +390,10 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
     __shared__ int s_last;
     __shared__ volatile int s_past[2][2][4];           // [odd or even blocks]: the last block in which a half's warp met a score past its row's reference
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int rank = (int)cluster_rank();
 
     const uint32_t bars = smem_u32(base + M::kBars);
-    // each CTA's: bytes of keys and values there and used, scores there, O done; the even CTA's: operands, P and Q there
+    // Each CTA's: bytes of keys and values there and used, scores there, O done.  The even CTA's: operands, P and Q there.
     const uint32_t kr_full = bars, kr_empty = kr_full + 8 * M::kRaw, vr_full = kr_empty + 8 * M::kRaw, vr_empty = vr_full + 8 * M::kRaw;
     const uint32_t s_full = vr_empty + 8 * M::kRaw, o_done = s_full + 16, k_full = o_done + 16, v_full = k_full + 16, p_full = v_full + 16;
     const uint32_t q_full = p_full + 16;
@@ -381,201 +408,183 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(s_full + 8 * b, 1);
             mbar_init(o_done + 8 * b, 1);
-            mbar_init(k_full + 8 * b, CTAS * kKeyWarps);
-            mbar_init(v_full + 8 * b, CTAS * kValueWarps);
-            mbar_init(p_full + 8 * b, CTAS * kSoftWarps);
+            mbar_init(k_full + 8 * b, kCtas * kKeyWarps);
+            mbar_init(v_full + 8 * b, kCtas * kValueWarps);
+            mbar_init(p_full + 8 * b, kCtas * kSoftWarps);
         }
-        mbar_init(q_full, CTAS * kSoftWarps);
+        mbar_init(q_full, kCtas * kSoftWarps);
         fence_mbar_init();
     }
     // (the odd chunks of the Z rows multiply nothing: zero for good)
     for (int i = tid; i < M::kAtom / 16; i += kThreads) sts128(base + M::kZ + 16 * i, 0, 0, 0, 0);
-    if (warp == kMmaWarp) {
-        if (kPair) tmem_alloc_pair(smem_u32(&s_tmem), kTmemCols);
-        else tmem_alloc(smem_u32(&s_tmem), kTmemCols);
-    }
+    if (warp == kMmaWarp) tmem_alloc_pair(smem_u32(&s_tmem), kTmemCols);
     fence_async_smem();
     tc_fence_before();
-    if (kPair) cluster_sync_all();
-    else __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_launch_dependents();
     pdl_wait();
 
-    const int c = blockIdx.x / CTAS, C = gridDim.x / CTAS;
-    const Range R = range_of<CTAS>(P, c, C, reinterpret_cast<int64_t*>(base + M::kK), &s_total, &s_range);
+    const int c = blockIdx.x / kCtas, C = gridDim.x / kCtas;
+    const Range R = range_of(P, c, C, reinterpret_cast<int64_t*>(base + M::kK), &s_total, &s_range);
     int own_abort = 0;
-    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded<kPair>(bar, parity & 1u, &own_abort, P.status); };
-    auto arrive = [&](uint32_t bar) {           // on the even CTA's barrier
-        if (kPair) mbar_arrive_remote(mapa_shared(bar, 0));
-        else mbar_arrive(bar);
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_bounded<true>(bar, parity & 1u, &own_abort, P.status); };
+    auto arrive = [&](uint32_t bar) { mbar_arrive_remote(mapa_shared(bar, 0)); };   // on the even CTA's barrier
 
     // The softmax warps hold a row's scores, the others little: kThreads * kRegs registers at launch, as many afterwards.
     if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp || warp == kLoadWarp + 4) {
-        // ---------------------------------------------------------------- keys' or values' bytes into their ring
-        const int what = warp != kLoadWarp;
-        const uint32_t full = what ? vr_full : kr_full, empty = what ? vr_empty : kr_empty;
-        const uint32_t dst0 = smem_u32(base + (what ? M::kRawV : M::kRawK));
-        const int stage_bytes = what ? M::kRawStageV : M::kRawStageK;
-        int s = 0, turn = -1, i = 0;             // blocks
-        for (Walk<CTAS> w(P, R); w.more; w.next()) {
-            const int32_t* table = P.block_table + w.u.b * P.bt_stride;
-            const int end = min(w.t.p1 + 1, w.q.len);
-            const uint8_t* src = nullptr;
-            for (int j = w.j0; j < w.j1; ++j, ++i) {
-                const int k = j - w.j0;
-                if (k % 4 == 0) {                // addresses of four blocks' tiles, one per lane
-                    src = nullptr;
-                    if (j + lane / kTiles < w.j1) {
-                        const int tile = w.t.block(j + lane / kTiles) * kTiles + lane % kTiles;
-                        if (tile * kKvTile < end) {
-                            const int pi = tile / P.cache.tiles_per_page, page = table[pi];
-                            if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
-                            else
-                                src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + w.u.head) * P.cache.tiles_per_page +
-                                                       (tile - pi * P.cache.tiles_per_page)) * (int64_t)L::kBytes;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kLoadWarp || warp == kLoadWarp + 4) {
+            // ---------------------------------------------------------------- keys' or values' bytes into their ring
+            const int what = warp != kLoadWarp;
+            const uint32_t full = what ? vr_full : kr_full, empty = what ? vr_empty : kr_empty;
+            const uint32_t dst0 = smem_u32(base + (what ? M::kRawV : M::kRawK));
+            const int stage_bytes = what ? M::kRawStageV : M::kRawStageK;
+            int s = 0, turn = -1, i = 0;             // blocks
+            for (Walk w(P, R); w.more; w.next()) {
+                const int32_t* table = P.block_table + w.u.b * P.bt_stride;
+                const int end = min(w.t.p1 + 1, w.q.len);
+                const uint8_t* src = nullptr;
+                for (int j = w.j0; j < w.j1; ++j, ++i) {
+                    const int k = j - w.j0;
+                    if (k % 4 == 0) {                // addresses of four blocks' tiles, one per lane
+                        src = nullptr;
+                        if (j + lane / kTiles < w.j1) {
+                            const int tile = w.t.block(j + lane / kTiles) * kTiles + lane % kTiles;
+                            // (what lies between the sinks and the windows is nobody's, and its pages need not exist)
+                            if (tile * kKvTile < end && (tile * kKvTile + kKvTile > w.t.lowest || tile * kKvTile < P.sinks)) {
+                                const int pi = tile / P.cache.tiles_per_page, page = table[pi];
+                                if (page < 0 || page >= P.cache.num_pages) atomicOr(P.status, kStatusIndex);
+                                else
+                                    src = P.cache.pages + (((int64_t)page * P.cache.kv_heads + w.u.head) * P.cache.tiles_per_page +
+                                                           (tile - pi * P.cache.tiles_per_page)) * (int64_t)L::kBytes;
+                            }
                         }
                     }
-                }
-                if (turn >= 0) wait(empty + 8 * s, turn);
-                __syncwarp();
-                const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (k % 4 * kTiles)) & ((1u << kTiles) - 1u);
-                // (of the keys only this CTA's half is loaded)
-                const uint32_t wanted = what ? there : there & (((1u << M::kTilesHere) - 1u) << (rank * M::kTilesHere));
-                if (lane == 0) {
-                    s_there[what][i & 7] = there;
-                    if (wanted) mbar_arrive_expect_tx(full + 8 * s, __popc(wanted) * M::kRawTile);
-                    else mbar_arrive(full + 8 * s);
-                }
-                __syncwarp();
-                const int no = lane % kTiles;
-                if (lane / kTiles == k % 4 && (wanted >> no & 1u)) {
-                    const uint32_t dst = dst0 + s * stage_bytes + (what ? no : no - rank * M::kTilesHere) * M::kRawTile;
-                    bulk_load(dst, src + (what ? L::kVc : 0), L::kCodes, full + 8 * s);
-                    bulk_load(dst + L::kCodes, src + (what ? L::kVs : L::kKs), 2 * L::kMeta, full + 8 * s);
-                }
-                if (++s == M::kRaw) s = 0, ++turn;
-            }
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- all MMAs, one thread of the even CTA
-        if (rank == 0) {
-            constexpr uint32_t idS = idesc_f16(false, CTAS * kRows, kKeys), idO = idesc_f16(false, CTAS * kRows, D);
-            auto mma = [&](uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
-                if (kPair) tc_mma_f16_ts_pair(d, a, b, id, add);
-                else tc_mma_f16_ts(d, a, b, id, add);
-            };
-            auto commit = [&](uint32_t bar) {
-                if (kPair) tc_commit_pair(bar);
-                else tc_commit(bar);
-            };
-            // (descriptors count 16-byte units from their first: a constant each)
-            const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
-            const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
-            auto scores = [&](int i) {
-                const int b = i & 1;
-                const uint32_t d = tmem + kColS + kKeys * b;
-                const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
-                wait(k_full + 8 * b, i >> 1);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int st = 0; st < D / 16; ++st)
-                            mma(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS, (part | st) != 0);
-                    mma(d, tmem + kColZ, zd + 2 * b, idS, 1);
-                    commit(s_full + 8 * b);
-                }
-                __syncwarp();
-            };
-            int done = 0, u = 0;   // blocks of earlier units, units
-            for (Walk<CTAS> w(P, R); w.more; w.next(), ++u) {
-                const int nb = w.j1 - w.j0;
-                wait(q_full, u);
-                tc_fence_after();
-                scores(done);
-                for (int j = 0; j < nb; ++j) {
-                    const int i = done + j, b = i & 1;
-                    if (j + 1 < nb) scores(i + 1);
-                    wait(v_full + 8 * b, i >> 1);
-                    wait(p_full + 8 * b, i >> 1);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t v = vd + (M::kVStages == 2 && b ? 2 * M::kVAtom / 16 : 0);
-#pragma unroll
-                        for (int st = 0; st < kKeys / 16; ++st)
-                            mma(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4), v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16,
-                                idO, j != 0 || st != 0);
-                        if (kFine) {
-#pragma unroll
-                            for (int st = 0; st < kKeys / 16; ++st)
-                                mma(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 32 + 8 * (st % 4),
-                                    v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, 1);
-                        }
-                        commit(o_done + 8 * b);
+                    if (turn >= 0) wait(empty + 8 * s, turn);
+                    __syncwarp();
+                    const uint32_t there = (__ballot_sync(0xffffffffu, src != nullptr) >> (k % 4 * kTiles)) & ((1u << kTiles) - 1u);
+                    // (of the keys only this CTA's half is loaded)
+                    const uint32_t wanted = what ? there : there & (((1u << M::kTilesHere) - 1u) << (rank * M::kTilesHere));
+                    if (lane == 0) {
+                        s_there[what][i & 7] = there;
+                        if (wanted) mbar_arrive_expect_tx(full + 8 * s, __popc(wanted) * M::kRawTile);
+                        else mbar_arrive(full + 8 * s);
                     }
                     __syncwarp();
+                    const int no = lane % kTiles;
+                    if (lane / kTiles == k % 4 && (wanted >> no & 1u)) {
+                        const uint32_t dst = dst0 + s * stage_bytes + (what ? no : no - rank * M::kTilesHere) * M::kRawTile;
+                        bulk_load(dst, src + (what ? L::kVc : 0), L::kCodes, full + 8 * s);
+                        bulk_load(dst + L::kCodes, src + (what ? L::kVs : L::kKs), 2 * L::kMeta, full + 8 * s);
+                    }
+                    if (++s == M::kRaw) s = 0, ++turn;
                 }
-                done += nb;
             }
-        }
-        __syncwarp();
-    } else if (dq_index(warp) >= 0) {
-        // ---------------------------------------------------------------- codes to operands
-        const bool keys = dq_index(warp) < kKeyWarps;
-        const int wi = keys ? dq_index(warp) : dq_index(warp) - kKeyWarps;
-        constexpr int tiles = M::kTilesHere / kKeyWarps;                     // this warp's tiles of every block: of keys, and one of values
-        static_assert(kValueWarps == kTiles, "a tile of values for each warp");
-        const uint32_t full = keys ? kr_full : vr_full, empty = keys ? kr_empty : vr_empty;
-        uint8_t* raw = base + (keys ? M::kRawK : M::kRawV);
-        int s = 0, turn = 0, i = 0;
-        for (Walk<CTAS> w(P, R); w.more; w.next()) {
-            const int end = min(w.t.p1 + 1, w.q.len);
-            for (int j = w.j0; j < w.j1; ++j, ++i) {
-                const int b = i & 1, kb = w.t.block(j);
-                wait(full + 8 * s, turn);
-                // the stage's last MMAs have read it
-                if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
-                if (!keys && i >= M::kVStages) wait(o_done + 8 * ((i - M::kVStages) & 1), (i - M::kVStages) >> 1);
-                const uint32_t there = s_there[keys ? 0 : 1][i & 7];
-                if (keys) {
-#pragma unroll 1
-                    for (int k = 0; k < tiles; ++k) {
-                        const int here = wi * tiles + k, no = rank * M::kTilesHere + here;   // tile of the stage, of the block
-                        const uint8_t* tile = raw + s * M::kRawStageK + here * M::kRawTile;
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- all MMAs, one thread of the even CTA
+            if (rank == 0) {
+                constexpr uint32_t idS = idesc_f16(false, kCtas * kRows, kKeys), idO = idesc_f16(false, kCtas * kRows, D);
+                // (descriptors count 16-byte units from their first: a constant each)
+                const uint64_t kd = smem_desc_sw128(smem_u32(base + M::kK)), zd = smem_desc_sw128(smem_u32(base + M::kZ));
+                const uint64_t vd = smem_desc_sw128(smem_u32(base + M::kV));
+                auto scores = [&](int i) {
+                    const int b = i & 1;
+                    const uint32_t d = tmem + kColS + kKeys * b;
+                    const uint64_t k = kd + (b ? M::kKStage / 16 : 0);
+                    wait(k_full + 8 * b, i >> 1);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int st = 0; st < D / 16; ++st)
+                                tc_mma_f16_ts_pair(d, tmem + kColQ + 8 * st, k + ((part * M::kAtoms + st / 4) * M::kAtom + 32 * (st % 4)) / 16, idS, (part | st) != 0);
+                        tc_mma_f16_ts_pair(d, tmem + kColZ, zd + 2 * b, idS, 1);
+                        tc_commit_pair(s_full + 8 * b);
+                    }
+                    __syncwarp();
+                };
+                int done = 0, u = 0;   // blocks of earlier units, units
+                for (Walk w(P, R); w.more; w.next(), ++u) {
+                    const int nb = w.j1 - w.j0;
+                    wait(q_full, u);
+                    tc_fence_after();
+                    scores(done);
+                    for (int j = 0; j < nb; ++j) {
+                        const int i = done + j, b = i & 1;
+                        if (j + 1 < nb) scores(i + 1);
+                        wait(v_full + 8 * b, i >> 1);
+                        wait(p_full + 8 * b, i >> 1);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t v = vd + (b ? 2 * M::kVAtom / 16 : 0);
+#pragma unroll
+                            for (int st = 0; st < kKeys / 16; ++st)
+                                tc_mma_f16_ts_pair(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 8 * (st % 4), v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16,
+                                    idO, j != 0 || st != 0);
+                            if (kFine) {
+#pragma unroll
+                                for (int st = 0; st < kKeys / 16; ++st)
+                                    tc_mma_f16_ts_pair(tmem + kColO, tmem + kColS + kKeys * b + (st / 4) * 64 + 32 + 8 * (st % 4),
+                                        v + ((st / 4) * M::kVAtom + 32 * (st % 4)) / 16, idO, 1);
+                            }
+                            tc_commit_pair(o_done + 8 * b);
+                        }
+                        __syncwarp();
+                    }
+                    done += nb;
+                }
+            }
+            __syncwarp();
+        } else if (dq_index(warp) >= 0) {
+            // ---------------------------------------------------------------- codes to operands
+            const bool keys = dq_index(warp) < kKeyWarps;
+            const int wi = keys ? dq_index(warp) : dq_index(warp) - kKeyWarps;
+            static_assert(M::kTilesHere == kKeyWarps && kTiles == kValueWarps, "a tile of every block for each warp");
+            const uint32_t full = keys ? kr_full : vr_full, empty = keys ? kr_empty : vr_empty;
+            uint8_t* raw = base + (keys ? M::kRawK : M::kRawV);
+            int s = 0, turn = 0, i = 0;
+            for (Walk w(P, R); w.more; w.next()) {
+                const int end = min(w.t.p1 + 1, w.q.len);
+                for (int j = w.j0; j < w.j1; ++j, ++i) {
+                    const int b = i & 1, kb = w.t.block(j);
+                    wait(full + 8 * s, turn);
+                    // the stage's last MMAs have read it
+                    if (keys && i >= 2) wait(s_full + 8 * b, (i >> 1) - 1);
+                    if (!keys && i >= 2) wait(o_done + 8 * b, (i >> 1) - 1);
+                    const uint32_t there = s_there[keys ? 0 : 1][i & 7];
+                    if (keys) {
+                        const int no = rank * M::kTilesHere + wi;              // tile of the block
+                        const uint8_t* tile = raw + s * M::kRawStageK + wi * M::kRawTile;
                         const int left = there >> no & 1u ? end - kb * kKeys - no * kKvTile : 0;
                         uint8_t *stage = base + M::kK + b * M::kKStage, *zs = base + M::kZ;
-                        if (wide_keys<BITS, D>(tile + L::kCodes, lane)) expand_wide_keys<BITS, D, M::kKeysHere>(tile, tile + L::kCodes, stage, zs, 2 * b, here, left, lane);
-                        else expand_keys<BITS, D, M::kKeysHere, false>(tile, tile + L::kCodes, stage, zs, 2 * b, here, left, lane);
-                    }
-                } else {
-                    uint8_t* tile = raw + s * M::kRawStageV + wi * M::kRawTile;
-                    const int left = there >> wi & 1u ? end - kb * kKeys - wi * kKvTile : 0;
-                    uint8_t* stage = base + M::kV + ((M::kVStages == 2 ? 2 * b : 0) + wi / 4) * M::kVAtom;
-                    bool no_numbers = false;
-                    if ((there >> wi & 1u) && wide_values<BITS, D>(tile + L::kCodes, lane)) {
-                        no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + wi * kKvTile, lane);
-                        expand_wide_values<BITS, D, CTAS>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                        if (wide_keys<BITS, D>(tile + L::kCodes, lane)) expand_wide_keys<BITS, D, M::kKeysHere>(tile, tile + L::kCodes, stage, zs, 2 * b, wi, left, lane);
+                        else expand_keys<BITS, D, M::kKeysHere, false>(tile, tile + L::kCodes, stage, zs, 2 * b, wi, left, lane);
                     } else {
-                        expand_values<BITS, D, CTAS, false>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                        uint8_t* tile = raw + s * M::kRawStageV + wi * M::kRawTile;
+                        const int left = there >> wi & 1u ? end - kb * kKeys - wi * kKvTile : 0;
+                        uint8_t* stage = base + M::kV + (2 * b + wi / 4) * M::kVAtom;
+                        bool no_numbers = false;
+                        if ((there >> wi & 1u) && wide_values<BITS, D>(tile + L::kCodes, lane)) {
+                            no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + wi * kKvTile, lane);
+                            expand_wide_values<BITS, D, kCtas>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                        } else {
+                            expand_values<BITS, D, kCtas, false>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
+                        }
+                        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[wi] = no_numbers;
                     }
-                    if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[wi] = no_numbers;
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive((keys ? k_full : v_full) + 8 * b);
+                        mbar_arrive(empty + 8 * s);
+                    }
+                    if (++s == M::kRaw) s = 0, ++turn;
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive((keys ? k_full : v_full) + 8 * b);
-                    mbar_arrive(empty + 8 * s);
-                }
-                if (++s == M::kRaw) s = 0, ++turn;
             }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ---------------------------------------------------------------- softmax: two threads per row
@@ -644,8 +653,8 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
             return fmaxf(P.scale_log2 * pow2i(-e), 0x1p-126f);             // (a hidden score is -inf times it)
         };
         int done = 0;
-        Walk<CTAS> w(P, R);
-        Row row(P, w.q, w.u, CTAS, rank, r);
+        Walk w(P, R);
+        Row row(P, w.q, w.u, rank, r);
         float f = w.more ? put_queries(row) : 0.f;
         while (w.more) {
             const int nb = w.j1 - w.j0, p = row.p;
@@ -779,7 +788,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
             float f_next = 0.f;
             w.next();
             if (w.more) {
-                row = Row(P, w.q, w.u, CTAS, rank, r);
+                row = Row(P, w.q, w.u, rank, r);
                 f_next = put_queries(row);
             } else {
                 soft_sync();   // (as in there: the maxima's last readers are done)
@@ -806,7 +815,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                     P.lse[here.at * P.q_heads + here.qh] = total == 0.f ? -INFINITY : (top + log2f(total) - kPUp) * 0.6931471805599453f;
             };
             constexpr int kSlot = kRows * (D + 2);
-            float* slot = P.part + (int64_t)((2 * c + (from_first == 0 ? 1 : 0)) * CTAS + rank) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
+            float* slot = P.part + (int64_t)((2 * c + (from_first == 0 ? 1 : 0)) * kCtas + rank) * kSlot;   // [D / 4][rows] of four, then [rows] m, l
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
@@ -833,10 +842,10 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                 const int c0 = shares.of(from), c1 = shares.of(from + unit_blocks - 1);
                 soft_sync();
                 // (release of what the block wrote before the barrier, acquire of what the others did)
-                if (tid == 0) s_last = arrive_gpu(P.counters + c0 * CTAS + rank) == (unsigned)(c1 - c0);
+                if (tid == 0) s_last = arrive_gpu(P.counters + c0 * kCtas + rank) == (unsigned)(c1 - c0);
                 soft_sync();
                 if (s_last) {
-                    auto part = [&](int k) { return P.part + (int64_t)((2 * (c0 + k) + (k == 0 ? 1 : 0)) * CTAS + rank) * kSlot; };
+                    auto part = [&](int k) { return P.part + (int64_t)((2 * (c0 + k) + (k == 0 ? 1 : 0)) * kCtas + rank) * kSlot; };
                     auto sums = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * r)); };
                     float top = -INFINITY, total = 0.f;
                     for (int k = 0; k <= c1 - c0; ++k) top = fmaxf(top, sums(k).x);
@@ -862,7 +871,7 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
                         if (here.live) finish(d, v, all);
                     }
                     finish_sum(top, total);
-                    if (tid == 0) P.counters[c0 * CTAS + rank] = 0;
+                    if (tid == 0) P.counters[c0 * kCtas + rank] = 0;
                 }
             }
             tc_fence_before();
@@ -872,28 +881,21 @@ __device__ __forceinline__ void chunk_body(const ChunkParams& P) {
         }
     }
     tc_fence_before();
-    if (kPair) cluster_sync_all();   // (no arrival or tensor-memory access of either CTA is still to come)
-    else __syncthreads();
+    cluster_sync_all();   // (no arrival or tensor-memory access of either CTA is still to come)
     tc_fence_after();
-    if (warp == kMmaWarp) {
-        if (kPair) tmem_dealloc_pair(tmem, kTmemCols);
-        else tmem_dealloc(tmem, kTmemCols);
-    }
+    if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
-
-template <int BITS, int D, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_pair_kernel(const __grid_constant__ ChunkParams P) { chunk_body<BITS, D, T, 2>(P); }
 
 // Clusters of the kernel that fit on the device at once (0 on error); sets its shared-memory attribute.  Kept per device.
 template <int BITS, int D, class T>
 int pairs_at_once(int device, int max_smem) {
     static std::mutex mu;
     static int known[kMaxDevices] = {};
-    constexpr int smem = ChunkSmem<BITS, D, 2>::kSize;
+    constexpr int smem = ChunkSmem<BITS, D>::kSize;
     if (device < 0 || device >= kMaxDevices || smem > max_smem) return 0;
     const std::lock_guard<std::mutex> lock(mu);
     if (known[device] == 0) {
-        auto kernel = chunk_pair_kernel<BITS, D, T>;
+        auto kernel = chunk_kernel<BITS, D, T>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2, 1, 1);
@@ -912,7 +914,7 @@ lq_status run(lq_handle h, const ChunkParams& P, cudaStream_t stream) {
     const int pairs = pairs_at_once<BITS, D, T>(h->device, h->max_smem_optin);
     if (pairs < 1) return LQ_ERR_UNSUPPORTED;
     if ((size_t)pairs * 2 > h->num_counters || (size_t)pairs * 4 * kRows * (D + 2) > h->partial_floats) return LQ_ERR_WORKSPACE;
-    return launch_overlapped(chunk_pair_kernel<BITS, D, T>, dim3(2 * pairs), kThreads, ChunkSmem<BITS, D, 2>::kSize, stream, P);
+    return launch_overlapped(chunk_kernel<BITS, D, T>, dim3(2 * pairs), kThreads, ChunkSmem<BITS, D>::kSize, stream, P);
 }
 
 }  // namespace

@@ -148,6 +148,22 @@ def test_pages_outside_the_cache_hide_their_tokens(lqm, handle):  # noqa: F811
         assert np.all(np.abs(out[:, 4 * h:4 * h + 4].float().cpu().numpy() - o) <= 2.0 ** -9 * mass + 2.0 ** -8 * np.abs(o) + 2.0 ** -22)
 
 
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("T", [1, 60, 300])
+def test_pages_outside_the_window_need_not_exist(lqm, handle, page, T):  # noqa: F811
+    n, window, sinks = 2000, 150, 20
+    c = Rows(lqm, [T, 5], [n, 40], page=page, window=window, sinks=sinks, seed=T)
+    want = c.chunk(handle)
+    handle.sync()
+    first = (n - T - window + 1) // page                # the first page with a token in some row's window
+    c.dev["bt"][0, -(-sinks // page):first] = -5
+    c.dev["bt"][1, -(-40 // page):] = 2 ** 31 - 1
+    got = c.chunk(handle)
+    handle.sync()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(*got)
+
+
 @pytest.mark.parametrize("bits,D", SHAPES)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
 @pytest.mark.parametrize("n", [40, 300, 3000])
