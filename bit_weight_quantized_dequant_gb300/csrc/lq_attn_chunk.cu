@@ -73,6 +73,9 @@ constexpr int kRows = 128;          // rows of a CTA
 constexpr int kKeys = kTcKeys;      // keys of a block
 static_assert(kKeys == kChunkKeys, "key blocks");
 constexpr int kTiles = kKeys / kKvTile;
+// Blocks of which is held what values are no numbers.  It is read behind the P of two blocks later; what has this place next
+// is written when the product of two blocks before its own is done, so five would do (a power of two).
+constexpr int kOdd = 8;
 // Warps: the softmax first (a warp reaches the tensor-memory lanes of its number mod 4).  Of the others those of one
 // scheduler (number mod 4 = 0) issue MMAs and load, the other three schedulers' expand: the MMA warp's instructions, few
 // and each waited for by the tensor cores, are not in line behind theirs.
@@ -116,8 +119,8 @@ struct ChunkSmem {
     static constexpr int kMl = kRawV + kRaw * kRawStageV;        // [2 halves][rows] maxima, then sums
     static constexpr int kF = kMl + 2 * kRows * 4;               // [2 halves][rows] queries' largest values
     static constexpr int kGroups = kF + 2 * kRows * 4;           // [rows] queries' group sums, their rests
-    static constexpr int kBad = kGroups + kRows * 2 * (D / 32) * 2;                  // [4 blocks][keys] groups of a value that are no numbers
-    static constexpr int kBars = kBad + 4 * kKeys;
+    static constexpr int kBad = kGroups + kRows * 2 * (D / 32) * 2;                  // [kOdd blocks][keys] groups of a value that are no numbers
+    static constexpr int kBars = kBad + kOdd * kKeys;
     static constexpr int kNumBars = 4 * kRaw + 2 * 5 + 1;
     static constexpr int kSize = 1024 + kBars + 8 * kNumBars;
     static_assert(kSize <= 226 * 1024 && kBars % 8 == 0 && kRawK % 128 == 0 && kRawTile % 16 == 0, "shared memory");
@@ -384,7 +387,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) chu
     float* tops = reinterpret_cast<float*>(base + M::kF);
     __shared__ uint32_t s_tmem;
     __shared__ volatile uint32_t s_there[2][8];        // a block's tiles in the cache, for keys (all of them) and values (no role is 8 ahead of another)
-    __shared__ volatile unsigned long long s_odd[4];   // a byte per tile of a block: whether it has values that are no numbers (read up to two blocks later)
+    __shared__ volatile unsigned long long s_odd[kOdd];   // a byte per tile of a block: whether it has values that are no numbers
     __shared__ Range s_range;
     __shared__ int64_t s_total;
     __shared__ int s_last;
@@ -568,12 +571,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) chu
                         uint8_t* stage = base + M::kV + (2 * b + wi / 4) * M::kVAtom;
                         bool no_numbers = false;
                         if ((there >> wi & 1u) && wide_values<BITS, D>(tile + L::kCodes, lane)) {
-                            no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & 3) * kKeys + wi * kKvTile, lane);
+                            no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & (kOdd - 1)) * kKeys + wi * kKvTile, lane);
                             expand_wide_values<BITS, D, kCtas>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
                         } else {
                             expand_values<BITS, D, kCtas, false>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
                         }
-                        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[wi] = no_numbers;
+                        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&s_odd[i & (kOdd - 1)])[wi] = no_numbers;
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -662,11 +665,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) chu
             uint32_t poison = 0;                                       // groups of dimensions that saw no number
             // the value groups of a block (whose product is done) that this row saw and that are no numbers
             auto odd_values = [&](int i, int kb) {
-                if (s_odd[i & 3] == 0) return;
+                if (s_odd[i & (kOdd - 1)] == 0) return;
                 for (int k = 0; k < kKeys; ++k) {
-                    if (!(reinterpret_cast<volatile uint8_t*>(&s_odd[i & 3])[k / kKvTile])) continue;
+                    if (!(reinterpret_cast<volatile uint8_t*>(&s_odd[i & (kOdd - 1)])[k / kKvTile])) continue;
                     const int j = kb * kKeys + k;
-                    if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & 3) * kKeys + k];
+                    if (j <= p && (P.window <= 0 || j > p - P.window || j < P.sinks)) poison |= (base + M::kBad)[(i & (kOdd - 1)) * kKeys + k];
                 }
             };
             // The product of block i.  A wait tells a barrier's phases apart by their parity alone: the product before on this

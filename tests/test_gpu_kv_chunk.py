@@ -194,6 +194,26 @@ def test_values_that_are_no_numbers_stay_with_the_rows_that_see_them(lqm, handle
     handle.sync()
 
 
+@pytest.mark.parametrize("bits,D", SHAPES)
+def test_a_value_that_is_no_number_among_many_blocks(lqm, handle, bits, D):  # noqa: F811
+    """As many units as there are pairs of CTAs, each of many key blocks: what a block's values are is looked at while
+    later blocks' are under way."""
+    n, T = 2048, 1024
+    c = Rows(lqm, [T], [n], hq=20, hkv=20, D=D, bits=bits, seed=3, poison=False)
+    good = c.chunk(handle)
+    clean = [m.copy() for m in c.meta]
+    for k in range(8):
+        c.meta = [m.copy() for m in clean]
+        page, tile, at = c.where(0, 128 * k + 127)          # the last key of block k, which all rows see
+        c.meta[3][page, :, tile, at, 1] = np.nan
+        c.repack()
+        out, lse = c.chunk(handle)
+        assert torch.equal(lse, good[1])
+        assert bool(out[..., 32:64].isnan().all()), int((~out[..., 32:64].isnan()).sum())
+        assert torch.equal(out[..., :32], good[0][..., :32]) and torch.equal(out[..., 64:], good[0][..., 64:])
+    handle.sync()
+
+
 def test_captured_calls_follow_lengths_and_rows(lqm, handle):  # noqa: F811
     c = Rows(lqm, [60, 40], [900, 300], seed=5, poison=False)
     want = c.chunk(handle)
