@@ -99,6 +99,10 @@ def test_logprobs_gradient(L):
         assert grad(L, **kw) == ALN, kw
 
 
+def test_more_rows_than_count(L):
+    assert score(L, n=0x7fff0001) == UNS and grad(L, n=0x7fff0001) == UNS
+
+
 def test_the_binding_of_chunks(handle):  # noqa: F811
     cache = types.SimpleNamespace(head_dim=64, kv_heads=2, page_size=16)
     D = _OnDevice
