@@ -10,7 +10,8 @@ Weight formats (see ``include/lq.h``):
   * NF4, block 64, fp32 absmax (AirQuant README, NF4 block-wise).
 
 Attention block: ``Handle.rope_table``, ``rope``, ``kv_append``, ``kv_read`` and
-``kv_attention`` over a paged ``KVCache`` in 4 or 8 bits.
+``kv_attention`` over a paged ``KVCache`` in 4 or 8 bits (with a sliding window and sinks if wanted),
+``kv_attention_chunk`` for prompts and pieces of them.  Scoring: ``Handle.token_logprobs``.
 """
 from __future__ import annotations
 

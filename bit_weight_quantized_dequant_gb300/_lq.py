@@ -734,7 +734,9 @@ class Handle:
         """Log probabilities of the given tokens (int64 [rows]; negative: left out, 0) under logits [rows][vocab] of fp32,
         float16 or bfloat16, the entropy of each row, and its `top` (up to 64) best tokens with theirs.  Returns
         (logprob, entropy, top_ids, top_logprobs): fp32 [rows] twice, int64 and fp32 [rows][top], equal logits by ascending
-        id (None both without top).  Logits that require a gradient get it through logprob and entropy."""
+        id (None both without top).  Logits that require a gradient get it through logprob and entropy (a first one
+        only; where it is captured into a CUDA graph, no graph of operations that was built outside of the capture
+        may hold the same leaves, as for any of torch's functions)."""
         torch = _torch()
         if logits.requires_grad and torch.is_grad_enabled():
             if stream is None:

@@ -39,7 +39,9 @@
 // (1050 TFLOP/s, 55 % of a library product's rate).  A unit's queries are put in place, and the scores begin, before the rows of the unit
 // before are written: a prompt of 2048 tokens of 40 heads 110 -> 98 us, 65 tokens at 365 17.9 -> 12.8.  Measured and not kept: a thread per row and every other
 // block for each half of the softmax warps (2527), a whole row's check by the sum of its P (2286), the next block's scores loaded ahead
-// (spills: 2900), queries by bulk copies one unit ahead (short calls 9 % slower), a longer suspension of waiting warps (no change).
+// (spills: 2900), queries by bulk copies one unit ahead, and rows written from shared memory by bulk copies (65 tokens at 365
+// 13.2 -> 15.1, windowed chunks 42 -> 47), both through shared memory with a warp's accesses side by side (13.2 -> 14.2, 2050 -> 2140),
+// a longer suspension of waiting warps (no change).
 //
 // What bounds it now: the softmax of a block takes about 1900 cycles from its scores to its P, one block after another,
 // where its 25 MMAs take 1620 (tensor pipe 58 %, issue 63 %).

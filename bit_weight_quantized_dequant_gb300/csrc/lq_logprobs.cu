@@ -14,6 +14,12 @@
 // threads hold anything above it.  Their chunks that do are read once more (from L2) and what passes the bound goes
 // to shared memory, where it is ranked by counting.  A logit and its index make one 64-bit key, larger for the larger logit
 // and then for the lower index, so no two are equal and no order of arrival matters.
+//
+// Measured: 2048 rows of 32000 bf16 logits 25.1 us (5.2 TB/s of a copy's 6.8), 1024 of 131072 47 us (5.7); the gradient of those
+// 82 us (6.5 TB/s); 333 rows of 50021 fp32 logits with 20 alternatives 22.5 us (3.0); one row of 32000 with 5 alternatives 7.6,
+// latency (a launch, the pass, the alternatives, the joining of parts).  On the way: packed pairs and maxima of words instead of
+// values one by one 38 -> 25; alternatives bounded by the threads' maxima instead of a search by bits over all values 63 -> 23.
+// Not kept: one block per place, taking parts in turn with the next one's loads under way (2048 x 32000: 34).
 
 #include <algorithm>
 

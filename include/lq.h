@@ -118,8 +118,9 @@ typedef enum lq_status {
     LQ_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out (reported by lq_sync) */
     LQ_ERR_RANGE = 7,         /* a decode GEMV met a weight table value |S*C+Z| >= 65520, outside the
                                  binary16 range of its tensor-core operands (reported by lq_sync) */
-    LQ_ERR_INDEX = 8          /* a kernel met a position outside the rotation table, or a slot or page
-                                 outside the cache, and left that element out (reported by lq_sync) */
+    LQ_ERR_INDEX = 8          /* a kernel met a position outside the rotation table, a slot or page outside
+                                 the cache, a token past the vocabulary, or rows of a request that are out of
+                                 order, and left that element out (reported by lq_sync) */
 } lq_status;
 
 typedef enum lq_format {
@@ -590,13 +591,18 @@ LQ_API lq_status lq_kv_attention_window(lq_handle h, const lq_kv_cache* cache, c
  *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
  * over kv head h / (q_heads / kv_heads).  A row that sees nothing (p < 0) gives out = 0 and lse = -inf.  Rows of q in no
  * request are not touched in out and lse.  Scores, their statistics and all sums are held in 32 bits; probabilities and
- * the cache's values are rounded to binary16 before their product.
+ * the cache's values are rounded to binary16 before their product (for binary16 outputs the first rounding is made up
+ * for).  A NaN or an infinity among the cached values of a token reaches the rows that see it, in the 32 dimensions of its
+ * group.  Keys and values that no row sees may be anything, and pages of nothing else need not exist.
  * q, out: [tokens][q_heads][head_dim] of dtype (LQ_F16 or LQ_BF16), token strides in elements, rows 16-byte aligned; out
  * may be q when the strides are equal.  lse: fp32 [tokens][q_heads] or NULL.  starts[] does not decrease and stays within
- * 0 .. tokens; an entry that does not is moved there and reported (LQ_ERR_INDEX).  lens, block_table, max_pages, scale and
+ * 0 .. tokens; an entry outside counts as the nearer end, a request that ends before it begins has no rows, and either is
+ * reported (LQ_ERR_INDEX).  lens, block_table, max_pages, scale and
  * pages outside the cache as in lq_kv_attention; lens, starts and block_table are read on the device, so a captured call
  * serves any division of the rows.  Uses the handle's workspace (LQ_ERR_WORKSPACE when it has no room for two blocks' rows
- * on each SM).  With tokens = 0 nothing is launched.
+ * on each SM: 20 MB for 128 dimensions).  tokens * (q_heads / kv_heads) goes up to 0x7fff0000, q_heads * head_dim and
+ * max_pages * page_size to 0x7fffff00 (LQ_ERR_UNSUPPORTED above, and where a device holds no pair of the kernel's
+ * blocks).  With tokens = 0 nothing is launched.
  */
 typedef struct lq_kv_chunk_args {
     const void* q;
@@ -625,7 +631,8 @@ LQ_API lq_status lq_kv_attention_chunk(lq_handle h, const lq_kv_cache* cache, co
  * (logprob 0); so is one at or past vocab (LQ_ERR_INDEX).  A logit of -inf is a token that cannot come; a row of nothing
  * else gives lse and every log probability -inf and entropy 0.  A NaN or +inf makes a row's logprob, entropy and
  * top_logprobs NaN (top_ids then count NaN as the largest).  entropy and lse may be NULL.  Sums are fp32 about the row's maximum.
- * Rows that are fewer than fill the device are split over blocks by means of the handle's workspace.
+ * Rows that are fewer than fill the device are split over blocks by means of the handle's workspace.  n and vocab go up to
+ * 0x7fff0000 (LQ_ERR_UNSUPPORTED above, and for more than 64 alternatives).
  */
 typedef struct lq_logprobs_args {
     const void* logits;
