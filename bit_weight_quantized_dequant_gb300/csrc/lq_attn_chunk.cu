@@ -40,7 +40,8 @@
 // before are written: a prompt of 2048 tokens of 40 heads 110 -> 98 us, 65 tokens at 365 17.9 -> 12.8.  Measured and not kept: a thread per row and every other
 // block for each half of the softmax warps (2527), a whole row's check by the sum of its P (2286), the next block's scores loaded ahead
 // (spills: 2900), queries by bulk copies one unit ahead, and rows written from shared memory by bulk copies (65 tokens at 365
-// 13.2 -> 15.1, windowed chunks 42 -> 47), both through shared memory with a warp's accesses side by side (13.2 -> 14.2, 2050 -> 2140),
+// 13.2 -> 15.1, windowed chunks 42 -> 47), both through shared memory with a warp's accesses side by side (2048 tokens
+// at the end of 32 Ki 2055 -> 2115, windowed chunks 42 -> 41),
 // a longer suspension of waiting warps (no change).
 //
 // What bounds it now: the softmax of a block takes about 1900 cycles from its scores to its P, one block after another,
@@ -113,7 +114,7 @@ struct ChunkSmem {
     static constexpr int kVAtom = kDimsHere * 128;               // [dimensions][64 keys]
     static constexpr int kRawTile = L::kCodes + 2 * L::kMeta;    // a tile's keys (or values): codes, S, Z
     static constexpr int kRawStageK = kTilesHere * kRawTile, kRawStageV = kTiles * kRawTile;
-    static constexpr int kRaw = L::kBytes <= 2560 ? 4 : 3;       // blocks in flight
+    static constexpr int kRaw = 3;                               // blocks in flight (a fourth: 430 -> 432 us for ragged requests)
     static constexpr int kK = 0;
     static constexpr int kZ = kK + 2 * kKStage;                  // Z of stage b in chunk 2 b of each key's row
     static constexpr int kV = kZ + kAtom;                        // two stages
