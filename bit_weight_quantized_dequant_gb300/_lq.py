@@ -100,14 +100,14 @@ class lq_logprobs_args(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n", ctypes.c_int), ("vocab", ctypes.c_int),
                 ("row_stride", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("logprob", ctypes.c_void_p),
                 ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("top", ctypes.c_int), ("top_ids", ctypes.c_void_p),
-                ("top_logprobs", ctypes.c_void_p)]
+                ("top_logprobs", ctypes.c_void_p), ("lse_rest", ctypes.c_void_p)]
 
 
 class lq_logprobs_grad_args(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("d_logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n", ctypes.c_int),
                 ("vocab", ctypes.c_int), ("row_stride", ctypes.c_int64), ("d_row_stride", ctypes.c_int64),
                 ("tokens", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
-                ("d_logprob", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p)]
+                ("d_logprob", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p), ("lse_rest", ctypes.c_void_p)]
 
 
 def library_path() -> Path:
@@ -760,12 +760,13 @@ class Handle:
 
         def new(shape, dtype):
             return torch.empty(shape, dtype=dtype, device=logits.device) if stream is None else self._new(shape, dtype, stream)
-        logprob, entropy, lse = (new((n,), torch.float32) for _ in range(3))
+        logprob, entropy = new((n,), torch.float32), new((n,), torch.float32)
+        lse = new((2, n), torch.float32)          # (and what its rounding left out)
         ids = best = None
         if top:
             ids, best = new((n, top), torch.int64), new((n, top), torch.float32)
         a = lq_logprobs_args(logits.data_ptr(), _code(logits.dtype), n, V, rs, tp, logprob.data_ptr(), entropy.data_ptr(),
-                             lse.data_ptr(), top, _ptr(ids), _ptr(best))
+                             lse.data_ptr(), top, _ptr(ids), _ptr(best), lse.data_ptr() + 4 * n)
         if n:
             st = self._lib.lq_logprobs(self._h, ctypes.byref(a), self._raw(stream))
             if st != LQ_OK:
@@ -779,7 +780,7 @@ class Handle:
         d_logits = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
         a = lq_logprobs_grad_args(logits.data_ptr(), d_logits.data_ptr(), _code(logits.dtype), n, V,
                                   self._logits("logits", logits), V, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
-                                  _ptr(grads[0]), _ptr(grads[1]))
+                                  _ptr(grads[0]), _ptr(grads[1]), lse.data_ptr() + 4 * n)
         if n:
             st = self._lib.lq_logprobs_grad(self._h, ctypes.byref(a), self._raw(None))
             if st != LQ_OK:

@@ -575,7 +575,7 @@ LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* st
     if (a.top > 0 && (!a.top_ids || !a.top_logprobs)) return LQ_ERR_INVALID_ARG;
     if (a.top > lq::kMaxLogprobTop || a.vocab > 0x7fff0000 || a.n > 0x7fff0000) return LQ_ERR_UNSUPPORTED;
     if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) || !aligned_to(a.top_ids, 8) || !aligned_to(a.logprob, 4) ||
-        !aligned_to(a.entropy, 4) || !aligned_to(a.lse, 4) || !aligned_to(a.top_logprobs, 4))
+        !aligned_to(a.entropy, 4) || !aligned_to(a.lse, 4) || !aligned_to(a.lse_rest, 4) || !aligned_to(a.top_logprobs, 4))
         return LQ_ERR_ALIGNMENT;
     if (a.n == 0) return LQ_OK;
     DeviceGuard guard(h->device);
@@ -592,7 +592,7 @@ LQ_API lq_status lq_logprobs_grad(lq_handle h, const lq_logprobs_grad_args* args
     if (a.n > 1 && a.d_row_stride < a.vocab) return LQ_ERR_INVALID_ARG;
     if (a.d_logits == a.logits && a.n > 1 && a.d_row_stride != a.row_stride) return LQ_ERR_INVALID_ARG;
     if (!aligned_to(a.logits, dtype_bytes(a.dtype)) || !aligned_to(a.d_logits, dtype_bytes(a.dtype)) || !aligned_to(a.tokens, 8) ||
-        !aligned_to(a.lse, 4) || !aligned_to(a.entropy, 4) || !aligned_to(a.d_logprob, 4) || !aligned_to(a.d_entropy, 4))
+        !aligned_to(a.lse, 4) || !aligned_to(a.lse_rest, 4) || !aligned_to(a.entropy, 4) || !aligned_to(a.d_logprob, 4) || !aligned_to(a.d_entropy, 4))
         return LQ_ERR_ALIGNMENT;
     if (a.n == 0) return LQ_OK;
     DeviceGuard guard(h->device);

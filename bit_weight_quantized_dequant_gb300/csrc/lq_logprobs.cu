@@ -4,6 +4,10 @@
 //   lse = m + ln s,  logprob = x_t - m - ln s,  entropy = ln s - w / s
 //   d x_i = p_i (-g - h (ln p_i + entropy)) + g [i = t],  p_i = e^(x_i - lse), g and h the gradients that came
 //
+// One fp32 lse is off by up to 2^-24 of its size, which would go whole into every p_i (logits about 1e5: 0.2 %; a row of the type's
+// lowest value: p = 1 for each).  So the forward pass leaves what its rounding dropped as well, and ln p_i = d - rest with d = x_i - lse,
+// which is exact wherever the rest matters; |rest| <= ln s, as m is an fp32 number.  The rest goes into the sums that are formed anyway.
+//
 // Bound by the logits' bytes: one pass forward, one more (and the gradient written) backward.  A thread keeps its own
 // running m, s and w over vectors of 16 bytes, four of this chunk and four of the next in flight, so that nothing passes
 // between threads before a row's end.  The grid is as large as the device holds at once and takes rows, or parts of rows,
@@ -44,7 +48,7 @@ struct LogprobParams {
     const void* x;
     int64_t stride;
     const int64_t* tokens;
-    float *logprob, *entropy, *lse;
+    float *logprob, *entropy, *lse, *rest;
     int64_t* top_ids;
     float* top_logprobs;
     int n, V, top, splits;
@@ -465,7 +469,12 @@ __global__ void __launch_bounds__(kThreads, TOP ? kPerSm - 1 : kPerSm) logprobs_
     }
     if (tid == 0) {
         if (P.entropy) P.entropy[part.row] = none ? 0.f : ln - all.w / all.s;
-        if (P.lse) P.lse[part.row] = none ? -INFINITY : ref + ln;
+        const float lse = __fadd_rn(ref, ln);
+        if (P.lse) P.lse[part.row] = none ? -INFINITY : lse;
+        if (P.rest) {                    // ref + ln - lse, exactly (whichever of the two is the larger)
+            const float of_ln = __fsub_rn(lse, ref);
+            P.rest[part.row] = none ? 0.f : __fadd_rn(__fsub_rn(ref, __fsub_rn(lse, of_ln)), __fsub_rn(ln, of_ln));
+        }
         const int64_t t = P.tokens[part.row];
         if (t >= V) atomicOr(P.status, kStatusIndex);
         P.logprob[part.row] = t < 0 || t >= V ? 0.f : none ? -INFINITY : to_float(part.x[t]) - ref - ln;
@@ -478,13 +487,14 @@ struct GradParams {
     void* dx;
     int64_t dx_stride;
     const int64_t* tokens;
-    const float *lse, *entropy, *d_logprob, *d_entropy;
+    const float *lse, *rest, *entropy, *d_logprob, *d_entropy;
     int n, V, splits;
 };
 
-// Blocks of a row take its vectors in turn.
+// Blocks of a row take its vectors in turn.  (Five to an SM: left to itself the compiler takes fewer registers, and 1024 rows of 131072
+// bf16 logits 87 us, not 84.)
 template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_constant__ GradParams P) {
+__global__ void __launch_bounds__(kThreads, kPerSm) logprobs_grad_kernel(const __grid_constant__ GradParams P) {
     constexpr int VEC = 16 / sizeof(T);
     pdl_launch_dependents();
     pdl_wait();
@@ -496,14 +506,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     const bool alike = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
     const int64_t t = P.tokens[row];
     const bool given = t >= 0 && t < V;
-    const float lse = P.lse[row], ref = lse == -INFINITY ? 0.f : lse;
+    const float lse = P.lse[row], ref = lse == -INFINITY ? 0.f : lse, rest = P.rest ? P.rest[row] : 0.f;
     const float g = given && P.d_logprob ? P.d_logprob[row] : 0.f;
     const float h = P.d_entropy ? P.d_entropy[row] : 0.f, H = h != 0.f ? P.entropy[row] : 0.f;
-    const float c = -g - h * H;
+    const float c = -g - h * (H - rest), far = -rest * kLog2e;
     auto gradient = [&](float2 v) {
         float2 d = add2(v, make_float2(-ref, -ref));
         d = make_float2(max_nan(d.x, kFar), max_nan(d.y, kFar));
-        const float2 y = mul2(d, make_float2(kLog2e, kLog2e)), p = make_float2(ex2f(y.x), ex2f(y.y));
+        const float2 y = fma2(d, make_float2(kLog2e, kLog2e), make_float2(far, far)), p = make_float2(ex2f(y.x), ex2f(y.y));
         return mul2(p, fma2(d, make_float2(-h, -h), make_float2(c, c)));
     };
     const int64_t step = (int64_t)P.splits * kThreads * VEC;
@@ -554,7 +564,7 @@ lq_status run_top(const LogprobParams& P, cudaStream_t stream) {
 lq_status launch_logprobs(lq_handle h, const lq_logprobs_args& a, cudaStream_t stream) {
     LogprobParams P = {};
     P.x = a.logits, P.stride = a.row_stride, P.tokens = a.tokens;
-    P.logprob = a.logprob, P.entropy = a.entropy, P.lse = a.lse, P.top_ids = a.top_ids, P.top_logprobs = a.top_logprobs;
+    P.logprob = a.logprob, P.entropy = a.entropy, P.lse = a.lse, P.rest = a.lse_rest, P.top_ids = a.top_ids, P.top_logprobs = a.top_logprobs;
     P.n = a.n, P.V = a.vocab, P.top = a.top;
     P.status = h->status_flag;
     // Parts of a row.  In units of the time in which all resident blocks read a chunk each (1.5 us): the bytes, or a block's
@@ -583,7 +593,7 @@ lq_status launch_logprobs(lq_handle h, const lq_logprobs_args& a, cudaStream_t s
 lq_status launch_logprobs_grad(lq_handle h, const lq_logprobs_grad_args& a, cudaStream_t stream) {
     GradParams P = {};
     P.x = a.logits, P.stride = a.row_stride, P.dx = a.d_logits, P.dx_stride = a.d_row_stride, P.tokens = a.tokens;
-    P.lse = a.lse, P.entropy = a.entropy, P.d_logprob = a.d_logprob, P.d_entropy = a.d_entropy;
+    P.lse = a.lse, P.rest = a.lse_rest, P.entropy = a.entropy, P.d_logprob = a.d_logprob, P.d_entropy = a.d_entropy;
     P.n = a.n, P.V = a.vocab;
     const int e = a.dtype == LQ_F32 ? 4 : 2, chunk = kThreads * kVecs * 16 / e;
     const int64_t want = std::max<int64_t>(1, (int64_t)h->num_sms * 16 / a.n);

@@ -630,7 +630,9 @@ LQ_API lq_status lq_kv_attention_chunk(lq_handle h, const lq_kv_cache* cache, co
  * largest first, equal ones by ascending index, top_logprobs[r][k] their log probabilities.  A negative token is left out
  * (logprob 0); so is one at or past vocab (LQ_ERR_INDEX).  A logit of -inf is a token that cannot come; a row of nothing
  * else gives lse and every log probability -inf and entropy 0.  A NaN or +inf makes a row's logprob, entropy and
- * top_logprobs NaN (top_ids then count NaN as the largest).  entropy and lse may be NULL.  Sums are fp32 about the row's maximum.
+ * top_logprobs NaN (top_ids then count NaN as the largest).  entropy, lse and lse_rest may be NULL.  Sums are fp32 about the row's
+ * maximum, so results are as good about any offset of a row's logits.  lse itself is rounded; lse_rest is what its rounding left out
+ * (lse + lse_rest is m + ln sum_i exp(x_i - m) without a further error), which the gradient of rows far from zero needs.
  * Rows that are fewer than fill the device are split over blocks by means of the handle's workspace.  n and vocab go up to
  * 0x7fff0000 (LQ_ERR_UNSUPPORTED above, and for more than 64 alternatives).
  */
@@ -644,6 +646,7 @@ typedef struct lq_logprobs_args {
     int top;
     int64_t* top_ids;          /* [n][top] */
     float* top_logprobs;       /* [n][top] */
+    float* lse_rest;           /* [n] */
 } lq_logprobs_args;
 
 LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* stream);
@@ -652,7 +655,9 @@ LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* st
  * lq_logprobs_grad — the gradient of lq_logprobs' logprob and entropy: with g = d_logprob[r] and e = d_entropy[r] (either
  * may be NULL: zeros; g counts as 0 for a token that was left out),
  *     d_logits[r][i] = p_i (-g - e (ln p_i + entropy[r])) + (i == t ? g : 0)     (fp32, rounded once to dtype)
- * and 0 where p_i is 0 and i is not t.  tokens, lse and entropy (needed with d_entropy only) are lq_logprobs' own.
+ * and 0 where p_i is 0 and i is not t.  tokens, lse and entropy (needed with d_entropy only) are lq_logprobs' own, and so is
+ * lse_rest: p_i = exp((x_i - lse) - lse_rest).  Without it (NULL) lse counts as it is, rounded: every p_i of the row is then off by up to
+ * 2^-24 |lse| relatively (0.2 % about 1e5; about 1e8 nothing of it is left).
  * d_logits has dtype and its own row stride (at least vocab), and may be logits when the strides are equal.
  */
 typedef struct lq_logprobs_grad_args {
@@ -664,6 +669,7 @@ typedef struct lq_logprobs_grad_args {
     const int64_t* tokens;
     const float *lse, *entropy;
     const float *d_logprob, *d_entropy;
+    const float* lse_rest;     /* [n] or NULL */
 } lq_logprobs_grad_args;
 
 LQ_API lq_status lq_logprobs_grad(lq_handle h, const lq_logprobs_grad_args* args, void* stream);
