@@ -354,24 +354,26 @@ __device__ __noinline__ void expand_wide_values(const uint8_t* tile, const uint8
 }
 
 // Value groups of one tile whose S or Z is no number are left out of meta (made 0) and recorded in bad[16], a bit per group
-// of the tile's tokens.  Returns whether there is one.
+// of the tile's tokens.  Returns whether there is one.  The tile's tokens from .. to - 1, which no row sees, are left out and not recorded:
+// theirs may be anything, also numbers whose S c + Z is infinite in binary16, and P = 0 times that is NaN.
 template <int BITS, int D>
-__device__ __noinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, int lane) {
+__device__ __noinline__ bool leave_out_odd_values(uint8_t* meta, uint8_t* bad, int from, int to, int lane) {
     using L = KvLayout<BITS, D>;
     constexpr int G = D / 32;
     uint32_t mask = 0;
     if (lane < 16) {       // lane: the token's place in the rows of S and Z
+        // place 4 q + e holds token 2 q + (e & 1) + 8 (e >> 1)
+        const int tok = 2 * (lane >> 2) + (lane & 1) + 8 * (lane >> 1 & 1);
+        const bool nobodys = tok >= from && tok < to;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint16_t* s = reinterpret_cast<uint16_t*>(meta + g * 32 + 2 * lane);
             uint16_t* z = reinterpret_cast<uint16_t*>(meta + L::kMeta + g * 32 + 2 * lane);
-            if ((*s & 0x7c00u) == 0x7c00u || (*z & 0x7c00u) == 0x7c00u) {
-                mask |= 1u << g;
-                *s = *z = 0;
-            }
+            const bool odd = (*s & 0x7c00u) == 0x7c00u || (*z & 0x7c00u) == 0x7c00u;
+            if (odd && !nobodys) mask |= 1u << g;
+            if (odd || nobodys) *s = *z = 0;
         }
-        // place 4 q + e holds token 2 q + (e & 1) + 8 (e >> 1)
-        bad[2 * (lane >> 2) + (lane & 1) + 8 * (lane >> 1 & 1)] = (uint8_t)mask;
+        bad[tok] = (uint8_t)mask;
     }
     __syncwarp();
     return __any_sync(0xffffffffu, mask != 0);
@@ -574,7 +576,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) chu
                         uint8_t* stage = base + M::kV + (2 * b + wi / 4) * M::kVAtom;
                         bool no_numbers = false;
                         if ((there >> wi & 1u) && wide_values<BITS, D>(tile + L::kCodes, lane)) {
-                            no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & (kOdd - 1)) * kKeys + wi * kKvTile, lane);
+                            const int first = kb * kKeys + wi * kKvTile;
+                            no_numbers = leave_out_odd_values<BITS, D>(tile + L::kCodes, base + M::kBad + (i & (kOdd - 1)) * kKeys + wi * kKvTile,
+                                                                       P.sinks - first, w.t.lowest - first, lane);
                             expand_wide_values<BITS, D, kCtas>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
                         } else {
                             expand_values<BITS, D, kCtas, false>(tile, tile + L::kCodes, stage, wi % 4, left, lane, rank);
