@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? kPerSm - 1 : kPerSm) logprobs_
             __syncthreads();
         } else {
             last = __shfl_sync(0xffffffffu, last, 0);
+            __syncwarp();        // (the other lanes read the parts behind lane 0's acquisition: a shuffle alone orders no memory)
         }
         if (!last) return;
         const float* p = P.part + 3 * ((int64_t)part.row * P.splits + lane);
