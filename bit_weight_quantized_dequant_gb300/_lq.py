@@ -521,8 +521,7 @@ class Handle:
     def rope(self, x, positions, table, layout=ROPE_HALF, inverse=False, out=None, stream=None):
         """Rotate the first table.shape[1] dimensions of x [n][heads][dim] (any token and head stride) by
         its int32 positions' table rows; inverse=True applies the transpose (the gradient).  An x that
-        requires a gradient gets it through the result (then without out); no other call of a Handle
-        carries gradients."""
+        requires a gradient gets it through the result (then without out)."""
         torch = _torch()
         if x.requires_grad and torch.is_grad_enabled():
             if out is not None:
@@ -734,9 +733,10 @@ class Handle:
         """Log probabilities of the given tokens (int64 [rows]; negative: left out, 0) under logits [rows][vocab] of fp32,
         float16 or bfloat16, the entropy of each row, and its `top` (up to 64) best tokens with theirs.  Returns
         (logprob, entropy, top_ids, top_logprobs): fp32 [rows] twice, int64 and fp32 [rows][top], equal logits by ascending
-        id (None both without top).  Logits that require a gradient get it through logprob and entropy (a first one
-        only; where it is captured into a CUDA graph, no graph of operations that was built outside of the capture
-        may hold the same leaves, as for any of torch's functions)."""
+        id (None both without top).  Logits that require a gradient get it through logprob and entropy, as accurate about
+        any offset of a row's logits: a first one only (a backward pass with create_graph is refused); where it is captured
+        into a CUDA graph, no graph of operations that was built outside of the capture may hold the same leaves, as for
+        any of torch's functions.  Of a Handle's calls this and rope carry gradients."""
         torch = _torch()
         if logits.requires_grad and torch.is_grad_enabled():
             if stream is None:

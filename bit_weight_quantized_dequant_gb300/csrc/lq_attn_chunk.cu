@@ -22,7 +22,8 @@
 //   - A row sees the tokens up to its own, and with a window the last of them and the sinks.  Blocks that no row of the unit
 //     sees are not visited; in one that not every row sees whole, scores are masked by two bounds per row.
 //   - A P of 0 times a cached NaN is NaN, so a value group (token and 32 dimensions) whose S or Z is no number counts as 0
-//     in the product, and rows that do see it get NaN in those dimensions at the unit's end.
+//     in the product, and rows that do see it get NaN in those dimensions at the unit's end.  So does, in a tile whose S or Z are
+//     large or no numbers, every value between the sinks and the windows, which may be anything and is nobody's.
 //
 // Roles (23 warps of 24): two load keys' and values' bytes by bulk copies, each into a ring of its own; one issues the MMAs (in
 // the even CTA); twelve expand codes, a 16-token tile each, four this CTA's keys, eight its half of all values' dimensions;
@@ -45,7 +46,10 @@
 // a longer suspension of waiting warps (no change).
 //
 // What bounds it now: the softmax of a block takes about 1900 cycles from its scores to its P, one block after another,
-// where its 25 MMAs take 1620 (tensor pipe 58 %, issue 63 %).
+// where its 25 MMAs take 1620 (tensor pipe 58 %, issue 63 %).  That is this schedule's bound, not the hardware's: a second row
+// tile's softmax could run under the first one's MMAs.  With heads of 64 dimensions two tiles' S, O and Q take 464 of tensor memory's
+// 512 columns; with 128 Q would have to be the operand in shared memory (S and O alone fill 512).  Not built.  The 206 to 240 bytes a
+// thread that the compiler spills are seldom touched: 0.4 % of the instructions executed are local loads and stores.
 
 #include <algorithm>
 #include <mutex>

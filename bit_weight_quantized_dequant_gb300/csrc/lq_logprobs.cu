@@ -9,10 +9,9 @@
 // which is exact wherever the rest matters; |rest| <= ln s, as m is an fp32 number.  The rest goes into the sums that are formed anyway.
 //
 // Bound by the logits' bytes: one pass forward, one more (and the gradient written) backward.  A thread keeps its own
-// running m, s and w over vectors of 16 bytes, four of this chunk and four of the next in flight, so that nothing passes
-// between threads before a row's end.  The grid is as large as the device holds at once and takes rows, or parts of rows,
-// in turn: as many parts as make the last turn a full one.  The last block to arrive joins a row's parts in their order
-// (results repeat bit for bit).
+// running m, s and w over vectors of 16 bytes, four in flight, so that nothing passes between threads before a row's end; five
+// blocks share an SM, so that some load while others add.  A block takes a row, or one of a row's equal parts, as many as make the
+// device's last turn of blocks a full one.  The last block to arrive joins a row's parts in their order (results repeat bit for bit).
 //
 // The best k of a row: the k-th largest of the threads' own maxima bounds the k-th largest logit from below, and few
 // threads hold anything above it.  Their chunks that do are read once more (from L2) and what passes the bound goes
@@ -20,7 +19,7 @@
 // and then for the lower index, so no two are equal and no order of arrival matters.
 //
 // Measured: 2048 rows of 32000 bf16 logits 25.1 us (5.2 TB/s of a copy's 6.8), 1024 of 131072 47 us (5.7); the gradient of those
-// 82 us (6.5 TB/s); 333 rows of 50021 fp32 logits with 20 alternatives 22.5 us (3.0); one row of 32000 with 5 alternatives 7.6,
+// 82 to 84 us (6.4 to 6.5 TB/s); 333 rows of 50021 fp32 logits with 20 alternatives 22.5 us (3.0); one row of 32000 with 5 alternatives 7.6,
 // latency (a launch, the pass, the alternatives, the joining of parts).  On the way: packed pairs and maxima of words instead of
 // values one by one 38 -> 25; alternatives bounded by the threads' maxima instead of a search by bits over all values 63 -> 23.
 // Not kept: one block per place, taking parts in turn with the next one's loads under way (2048 x 32000: 34).
