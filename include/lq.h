@@ -656,8 +656,8 @@ LQ_API lq_status lq_logprobs(lq_handle h, const lq_logprobs_args* args, void* st
  * may be NULL: zeros; g counts as 0 for a token that was left out),
  *     d_logits[r][i] = p_i (-g - e (ln p_i + entropy[r])) + (i == t ? g : 0)     (fp32, rounded once to dtype)
  * and 0 where p_i is 0 (one below 2^-126 counts as 0) and i is not t.  tokens, lse and entropy (needed with d_entropy only) are
- * lq_logprobs' own, and so is lse_rest: p_i = exp((x_i - lse) - lse_rest).  Without it (NULL) lse counts as it is, rounded: every p_i of the row is then off by up to
- * 2^-24 |lse| relatively (0.2 % about 1e5; about 1e8 nothing of it is left).
+ * lq_logprobs' own, and so is lse_rest: p_i = exp((x_i - lse) - lse_rest).  Without it (NULL) lse counts as it is, rounded: every
+ * p_i of the row is then off by up to 2^-24 |lse| relatively (0.2 % about 1e5; about 1e8 nothing of it is left).
  * d_logits has dtype and its own row stride (at least vocab), and may be logits when the strides are equal.
  */
 typedef struct lq_logprobs_grad_args {
